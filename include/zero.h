@@ -65,7 +65,9 @@ typedef enum {
     ZERO_ERR_BOUNDS = 6       /* a request exceeds a fixed capacity of the library   */
 } zero_status;
 
-typedef enum { ZERO_BF16 = 0, ZERO_FP16 = 1 } zero_dtype;
+/* ZERO_FP32 is accepted by the layer norm and the matrix operators; the step's
+ * gradients and parameters are 16-bit.                                      */
+typedef enum { ZERO_BF16 = 0, ZERO_FP16 = 1, ZERO_FP32 = 2 } zero_dtype;
 
 /* bits of zero_dev_scalars.status */
 #define ZERO_DEV_TIMEOUT 1 /* a bounded wait inside a kernel ran out; that kernel stopped early */
@@ -473,6 +475,53 @@ ZERO_API zero_status zero_step_layers(const zero_hparams* hp, int n_layers, cons
                                       int micro_batches, int gathers, int n_gathered, void* const* gathered,
                                       signed char* const* gathered_codes, float* const* gathered_scales,
                                       zero_dev_scalars* scalars_dev, void* ws, void* stream, void* gather_stream);
+
+/* ------------------------------------------------------------ layer norm --- */
+/* Layer norm over the last dimension of [rows, cols] activations, and its
+ * backward pass with the reduction of the weight gradients -- the norm vectors
+ * of a layer, whose gradients the step's reduce-scatter takes in the ranks'
+ * 16-bit type (w_dtype the gradient type and dgain / dbias inside a rank's
+ * flat buffer) or in fp32:
+ *   mean = sum(x) / cols,  rstd = 1 / sqrt(sum((x - mean)^2) / cols + eps)
+ *   y = (x - mean) * rstd * gain + bias
+ *   dx = rstd * (h - sum(h)/cols - xhat * sum(h*xhat)/cols),
+ *        h = dy * gain, xhat = (x - mean) * rstd
+ *   dgain = sum over rows of dy * xhat,  dbias = sum over rows of dy
+ * Sums are fp32 or wider whatever the types, and each result is rounded once.
+ * Every result is the same bits for the same inputs on the same device.
+ *
+ * x, y, dy, dx have `dtype`, gain, bias, dgain, dbias `w_dtype`; mean and rstd
+ * are fp32 [rows].  Strides are in elements between rows, 0 meaning cols, else
+ * >= cols.  All these pointers need only the alignment of their element type;
+ * bases and strides that are multiples of 16 bytes take the wide-load kernels.
+ * rows may be 0: the activations and statistics may then be NULL, and the
+ * backward pass writes zero weight gradients.
+ * 1 <= cols <= ZERO_MAX_NORM_COLS.                                          */
+#define ZERO_MAX_NORM_COLS (1 << 24)
+typedef struct {
+    long long rows;
+    int cols;
+    zero_dtype dtype;
+    zero_dtype w_dtype;
+    float eps;
+    long long x_stride, y_stride, dy_stride, dx_stride;
+} zero_layernorm;
+
+/* Bytes of workspace zero_layernorm_backward needs (256-byte aligned; its
+ * contents need not be kept or cleared); 0 for an invalid descriptor.       */
+ZERO_API size_t zero_layernorm_workspace_bytes(const zero_layernorm* desc);
+
+/* y may be x (same stride); any other overlap is refused.  gain NULL: ones,
+ * bias NULL: zeros; mean and rstd NULL: not stored.  One kernel.            */
+ZERO_API zero_status zero_layernorm_forward(const zero_layernorm* desc, const void* x, const void* gain,
+                                            const void* bias, void* y, float* mean, float* rstd, void* stream);
+
+/* mean and rstd as the forward call stored them.  dx may be dy or x (same
+ * stride).  dgain and dbias are overwritten, not accumulated; either may be
+ * NULL (not computed).                                                      */
+ZERO_API zero_status zero_layernorm_backward(const zero_layernorm* desc, const void* dy, const void* x,
+                                             const void* gain, const float* mean, const float* rstd, void* dx,
+                                             void* dgain, void* dbias, void* ws, void* stream);
 
 /* ----------------------------------------------------------- diagnostics --- */
 /* Launch one kernel that waits on a barrier nothing completes, with a wait

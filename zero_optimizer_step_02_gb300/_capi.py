@@ -15,6 +15,7 @@ LIB_PATH = os.path.join(_HERE, "libzero.so")
 
 ZERO_BF16 = 0
 ZERO_FP16 = 1
+ZERO_FP32 = 2
 ZERO_MAX_RANKS = 256
 ZERO_DEV_TIMEOUT = 1
 NOALLOC_SCRATCH_BYTES = 32768 + 4 * (1 << 20)   # ZERO_NOALLOC_SCRATCH_BYTES
@@ -66,6 +67,13 @@ class ZeroLayer(ctypes.Structure):
                 ("state_on_host", ctypes.c_int)]
 
 
+class ZeroLayerNorm(ctypes.Structure):
+    """zero_layernorm of zero.h: the shape, types and strides of a layer norm."""
+    _fields_ = [("rows", ctypes.c_longlong), ("cols", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("w_dtype", ctypes.c_int), ("eps", ctypes.c_float), ("x_stride", ctypes.c_longlong),
+                ("y_stride", ctypes.c_longlong), ("dy_stride", ctypes.c_longlong), ("dx_stride", ctypes.c_longlong)]
+
+
 _SIGS = {
     "zero_status_str": (ctypes.c_char_p, [_i32]),
     "zero_abi_version": (_i32, []),
@@ -100,6 +108,10 @@ _SIGS = {
                                            _vp, _vp, _vp]),
     "zero_step_layers": (_i32, [_hp, _i32, ctypes.POINTER(ZeroLayer), _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
                                 _vp]),
+    "zero_layernorm_workspace_bytes": (_sz, [ctypes.POINTER(ZeroLayerNorm)]),
+    "zero_layernorm_forward": (_i32, [ctypes.POINTER(ZeroLayerNorm), _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "zero_layernorm_backward": (_i32, [ctypes.POINTER(ZeroLayerNorm), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                       _vp]),
     "zero_layers_workspace_bytes": (_sz, [_hp, _i32, ctypes.POINTER(ZeroLayer)]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -388,6 +400,29 @@ def zero_step_layers(hp, layers, gathers, gathered, scalars, ws=None, micro_batc
     gs = None if gather_stream is None else _stream(gather_stream)
     _check(_lib.zero_step_layers(ctypes.byref(hp), len(stack), stack.array, micro_batches, gathers, len(gptr), gptr,
                                  cptr, sptr, _addr(scalars), _addr(ws), _stream(stream), gs), "zero_step_layers")
+
+
+def layernorm(rows, cols, dtype=ZERO_BF16, w_dtype=ZERO_FP32, eps=1e-5, x_stride=0, y_stride=0, dy_stride=0,
+              dx_stride=0):
+    """Descriptor of a layer norm over [rows, cols]; strides in elements, 0 for cols."""
+    return ZeroLayerNorm(rows, cols, dtype, w_dtype, eps, x_stride, y_stride, dy_stride, dx_stride)
+
+
+def zero_layernorm_workspace_bytes(desc):
+    return _lib.zero_layernorm_workspace_bytes(ctypes.byref(desc))
+
+
+def zero_layernorm_forward(desc, x, gain, bias, y, mean=None, rstd=None, stream=None):
+    """y = layer norm of x; mean and rstd (fp32 [rows], or None) are what the backward pass reads."""
+    _check(_lib.zero_layernorm_forward(ctypes.byref(desc), _addr(x), _addr(gain), _addr(bias), _addr(y), _addr(mean),
+                                       _addr(rstd), _stream(stream)), "zero_layernorm_forward")
+
+
+def zero_layernorm_backward(desc, dy, x, gain, mean, rstd, dx, dgain, dbias, ws, stream=None):
+    """dx, dgain and dbias (either None: not computed); ws: zero_layernorm_workspace_bytes(desc) bytes."""
+    _check(_lib.zero_layernorm_backward(ctypes.byref(desc), _addr(dy), _addr(x), _addr(gain), _addr(mean),
+                                        _addr(rstd), _addr(dx), _addr(dgain), _addr(dbias), _addr(ws),
+                                        _stream(stream)), "zero_layernorm_backward")
 
 
 def zero_launch_count():

@@ -6,8 +6,7 @@
 #include <cstring>
 #include <new>
 
-#include <nvtx3/nvToolsExt.h>
-
+#include "zk_capi.h"
 #include "zk_common.cuh"
 #include "zk_launch.h"
 
@@ -27,22 +26,12 @@ namespace {
 
 using zk::StreamArgs;
 
-// An NVTX range named after the entry point around each call that launches
-// work, so that profilers (nsys, ncu --nvtx) group its kernels; with no tool
-// attached it costs a branch.
-struct CallRange {
-    explicit CallRange(const char* name) { nvtxRangePushA(name); }
-    ~CallRange() { nvtxRangePop(); }
-    CallRange(const CallRange&) = delete;
-    CallRange& operator=(const CallRange&) = delete;
-};
-#define ZK_CALL_RANGE() const CallRange zk_call_range_(__func__)
+using zk::aligned;
+using zk::as_stream;
+using zk::check_dev;
+using zk::from_cuda;
 
 constexpr size_t kPartialBytes = sizeof(double) * zk::kMaxPartials;  // 32 KB, 256-aligned
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-zero_status from_cuda(cudaError_t e) { return e == cudaSuccess ? ZERO_OK : ZERO_ERR_CUDA; }
 
 #define ZK_TRY(expr)                              \
     do {                                          \
@@ -72,14 +61,6 @@ zero_status check_ranks(const zero_plan* p, const void* const* ranks)
     }
     return ZERO_OK;
 }
-
-zero_status check_dev(const void* ptr, uintptr_t align = 16)
-{
-    if (ptr == nullptr) return ZERO_ERR_INVALID_ARG;
-    return aligned(ptr, align) ? ZERO_OK : ZERO_ERR_MISALIGNED;
-}
-
-cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
 long long tiles_of(long long n) { return (n + zk::kTile - 1) / zk::kTile; }
 
