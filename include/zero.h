@@ -523,6 +523,85 @@ ZERO_API zero_status zero_layernorm_backward(const zero_layernorm* desc, const v
                                              const void* gain, const float* mean, const float* rstd, void* dx,
                                              void* dgain, void* dbias, void* ws, void* stream);
 
+/* --------------------------------------- orthogonalised matrix updates --- */
+/* Orthogonalising an update by Newton-Schulz products, and the Muon step built
+ * on it: the optimizer of a layer's weight matrices, beside Adam for its
+ * vectors.  For each matrix of a batch of equal ones:
+ *   x = g / (|g|_F + eps)
+ *   `steps` times:  G = x x^T,  x <- a x + (b G + c G G) x     (rows <= cols;
+ *                   G = x^T x,  x <- a x + x (b G + c G G)      for tall ones)
+ * Each step maps every singular value s of x to a s + b s^3 + c s^5 and keeps
+ * the singular vectors.  The products run on fp16 tensor cores with fp32
+ * accumulation: `products` 1 multiplies fp16 values (relative error of the
+ * result 2e-4 .. 2e-3, 2-norm), 3 multiplies pairs of them (about 1e-6, up to
+ * 3e-5 for a side of 4096, from the accumulator) at three times the work; 0
+ * picks 1 where the result is rounded to bf16 and 3 elsewhere (a Muon step,
+ * whose result is added to fp32 weights, takes 3).  Matrices whose short side
+ * is under 256 always take 3.
+ * A matrix of zeros gives zeros; one with a NaN or an infinity gives NaN.
+ * The same inputs give the same bits on the same device.
+ *
+ * coefs: host array of steps * 3 floats {a, b, c} for each step, read during
+ * the call, or NULL: {3.4445, -4.7750, 2.0315} for every step.  steps 0 (with
+ * coefs NULL): 5.  A schedule that takes singular values in [0, 1] to where
+ * s^2 or |b s^2 + c s^4| pass 15 is refused (ZERO_ERR_INVALID_ARG).
+ * Leading dimensions (between rows) and strides (between matrices) are in
+ * elements; 0 means packed.  Sizes beyond ZERO_MAX_MATRIX_DIM a side,
+ * ZERO_MAX_MATRIX_ELEMS a matrix, 65535 matrices or 2^30 tiles of 128 x 64
+ * are ZERO_ERR_BOUNDS.                                                      */
+#define ZERO_MAX_NS_STEPS 32
+#define ZERO_MAX_MATRIX_DIM 65536
+#define ZERO_MAX_MATRIX_ELEMS (1LL << 31)
+typedef struct {
+    int rows, cols, batch;
+    zero_dtype dtype;     /* of the input (Muon: of the rank gradients, 16-bit)     */
+    zero_dtype out_dtype; /* of the result (Muon: of the 16-bit weights)            */
+    long long in_ld, out_ld;
+    long long in_stride, out_stride;
+    int steps;
+    const float* coefs;
+    float eps;            /* >= 1e-30                                               */
+    int products;         /* 0, 1 or 3                                              */
+} zero_matrices;
+
+/* Bytes of workspace (256-byte aligned; its contents need not be kept or
+ * cleared); 0 for an invalid descriptor.                                    */
+ZERO_API size_t zero_orthogonalize_workspace_bytes(const zero_matrices* desc);
+ZERO_API size_t zero_muon_workspace_bytes(const zero_matrices* desc);
+
+/* out = the orthogonalised g.  g and out need the alignment of their element
+ * type (16-byte bases and strides take the wide loads and stores); out may
+ * overlap g, neither may overlap ws.  scalars_dev (may be NULL, else 256-byte
+ * aligned) only receives ZERO_DEV_TIMEOUT if a bounded wait runs out.       */
+ZERO_API zero_status zero_orthogonalize(const zero_matrices* desc, const void* g, void* out, void* ws,
+                                        zero_dev_scalars* scalars_dev, void* stream);
+
+/* Muon hyper-parameters, copied by value at each call.                      */
+typedef struct {
+    float lr;
+    float momentum;      /* mu, in [0, 1)                                            */
+    float weight_decay;  /* decoupled                                                */
+    float rms_scale;     /* > 0: update times rms_scale * sqrt(max(rows, cols)), so
+                            that its entries have that root mean square; 0: times
+                            sqrt(max(1, rows / cols))                                */
+    float loss_scale;    /* a fixed scale the gradients carry; 0 reads as 1          */
+    int nesterov;        /* 1: direction g + mu m, 0: m                              */
+} zero_muon_hparams;
+
+/* One Muon step of a batch of equal matrices that lie in the flat parameter
+ * space of the step: row-major without gaps, matrix i at element i * in_stride
+ * (0: packed; a multiple of 8 with more than one matrix) of every array.
+ *   g = (sum over ranks in order, from +0.0f, of the rank's gradient) / (n_d * loss_scale)
+ *   m <- mu m + g,   u = g + mu m (nesterov) or m
+ *   w <- w (1 - lr wd) - lr * scale * orthogonalised(u)
+ *   lp_out = 16-bit cast of w (NULL: none)
+ * momentum, master: fp32, updated in place.  rank_grads: host array of n_d
+ * device pointers to the first matrix.  All 16-byte aligned; no array that is
+ * written may overlap another one.                                          */
+ZERO_API zero_status zero_muon_step(const zero_matrices* desc, const zero_muon_hparams* hp, int n_d,
+                                    const void* const* rank_grads, float* momentum, float* master, void* lp_out,
+                                    void* ws, zero_dev_scalars* scalars_dev, void* stream);
+
 /* ----------------------------------------------------------- diagnostics --- */
 /* Launch one kernel that waits on a barrier nothing completes, with a wait
  * limit of timeout_ns (at most 10 s).  When the limit runs out the kernel sets
@@ -549,6 +628,13 @@ ZERO_API zero_status zero_debug_stream_timeout(int kernel, void* scratch, zero_d
 
 ZERO_API zero_status zero_debug_wait_timeout(zero_dev_scalars* scalars_dev, long long timeout_ns,
                                              void* stream);
+
+/* The matrix product's timeout path: one 64 x 64 x 64 product whose copies are
+ * never issued, so every bounded wait runs out after timeout_ns (at most 10 s);
+ * it sets ZERO_DEV_TIMEOUT in scalars->status, gives its tensor memory back and
+ * returns without writing a result.  scratch: 16 KB, 256-byte aligned.      */
+ZERO_API zero_status zero_debug_matmul_timeout(void* scratch, zero_dev_scalars* scalars_dev, long long timeout_ns,
+                                               void* stream);
 
 /* ------------------------------------------------- allocation-free step --- */
 /* The pages have no counterpart to this entry point.  It serves callers

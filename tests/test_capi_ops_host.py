@@ -1,4 +1,4 @@
-"""Argument checks of the training operators (layer norm): no GPU needed, no
+"""Argument checks of the training operators (layer norm, matrix updates): no GPU needed, no
 call here reaches a launch."""
 import ctypes
 
@@ -69,3 +69,78 @@ def test_layernorm_workspace_size(z):
     assert one % 256 == 0 and many % 256 == 0
     # bounded partial sums, and two row means for each row
     assert many <= 256 + 304 * 2 * 64 * 4 + 256 + (1 << 20) * 8 + 256
+
+
+# ------------------------------------------------ orthogonalised updates, Muon
+def orthogonalize(z, d, g=A, out=B, ws=C, sc=D):
+    return z._capi.raw_status("zero_orthogonalize", ctypes.byref(d) if d is not None else None, g, out, ws, sc, None)
+
+
+def muon(z, d, hp=None, n_d=2, ranks=(A, B), momentum=C, master=D, lp=E, ws=F, sc=G):
+    hp = z.muon_hparams() if hp is None else hp
+    arr = (ctypes.c_void_p * len(ranks))(*ranks) if ranks is not None else None
+    return z._capi.raw_status("zero_muon_step", ctypes.byref(d) if d is not None else None, ctypes.byref(hp), n_d, arr,
+                              momentum, master, lp, ws, sc, None)
+
+
+BOUNDS = 6
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(rows=0), INVALID), (dict(cols=-1), INVALID), (dict(batch=0), INVALID), (dict(dtype=5), INVALID),
+    (dict(out_dtype=-1), INVALID), (dict(eps=0.0), INVALID), (dict(eps=float("nan")), INVALID),
+    (dict(products=2), INVALID), (dict(steps=-1), INVALID), (dict(steps=33), INVALID), (dict(in_ld=63), INVALID),
+    (dict(out_ld=1), INVALID), (dict(stride=100), INVALID), (dict(out_stride=1), INVALID),
+    (dict(rows=65537), BOUNDS), (dict(cols=65537), BOUNDS), (dict(batch=65536), BOUNDS),
+    (dict(rows=65536, cols=65536), BOUNDS), (dict(rows=32768, cols=32768, batch=65535), BOUNDS),
+    (dict(coefs=[(float("nan"), 0.0, 0.0)]), INVALID), (dict(coefs=[(100.0, 0.0, 0.0)] * 2), INVALID),
+    (dict(coefs=[(3.0, -40.0, 1.0)]), INVALID)])
+def test_matrices_descriptor_is_checked(z, kw, status):
+    d = z.matrices(**dict(dict(rows=32, cols=64), **kw))
+    assert z.zero_orthogonalize_workspace_bytes(d) == 0 and z.zero_muon_workspace_bytes(d) == 0
+    assert orthogonalize(z, d) == status and muon(z, d) == status
+    assert orthogonalize(z, None) == INVALID and muon(z, None) == INVALID
+
+
+def test_schedules_that_fit_are_accepted(z):
+    for coefs in (None, [(1.5, -0.5, 0.0)] * 32, [(1.875, -1.25, 0.375)] * 10, [(4.0, -6.0, 3.0)], [(1.0, 0.0, 0.0)]):
+        assert z.zero_orthogonalize_workspace_bytes(z.matrices(32, 64, coefs=coefs)) > 0
+    with pytest.raises(ValueError):
+        z.matrices(32, 64, coefs=[(1.0, 2.0)])
+
+
+def test_matrices_pointers_are_checked(z):
+    d = z.matrices(32, 64, dtype=z.ZERO_BF16, out_dtype=z.ZERO_FP32)
+    for k in ("g", "out", "ws"):
+        assert orthogonalize(z, d, **{k: None}) == INVALID
+    assert orthogonalize(z, d, g=A + 1) == MISALIGNED and orthogonalize(z, d, out=B + 2) == MISALIGNED
+    assert orthogonalize(z, d, ws=C + 16) == MISALIGNED and orthogonalize(z, d, sc=D + 16) == MISALIGNED
+    n = z.zero_orthogonalize_workspace_bytes(d)
+    assert orthogonalize(z, d, g=C + n - 2) == INVALID and orthogonalize(z, d, out=C - 4) == INVALID
+
+
+def test_muon_arguments_are_checked(z):
+    d = z.matrices(32, 64)
+    for k in ("ranks", "momentum", "master", "ws"):
+        assert muon(z, d, **{k: None}) == INVALID
+    assert muon(z, d, ranks=(A, None)) == INVALID and muon(z, d, n_d=0) == INVALID and muon(z, d, n_d=257) == INVALID
+    for k, v in (("ranks", (A, B + 2)), ("momentum", C + 4), ("master", D + 4), ("lp", E + 2), ("ws", F + 16), ("sc", G + 8)):
+        assert muon(z, d, **{k: v}) == MISALIGNED
+    for kw in (dict(lr=-1.0), dict(lr=float("nan")), dict(momentum=1.0), dict(momentum=-0.1), dict(weight_decay=-1.0),
+               dict(rms_scale=float("inf")), dict(loss_scale=-2.0)):
+        assert muon(z, d, hp=z.muon_hparams(**kw)) == INVALID
+    for kw in (dict(dtype=z.ZERO_FP32), dict(out_dtype=z.ZERO_FP32), dict(in_ld=72), dict(out_ld=72),
+               dict(out_stride=4096)):
+        assert muon(z, z.matrices(32, 64, **kw)) == INVALID
+    assert muon(z, z.matrices(5, 5, batch=2)) == MISALIGNED                 # 25 elements: the second matrix is unaligned
+    size = 32 * 64
+    assert muon(z, d, momentum=D + 4 * size - 16) == INVALID                # over the end of master
+    assert muon(z, d, lp=C + 16) == INVALID and muon(z, d, master=A + 16) == INVALID
+    assert muon(z, d, ws=B) == INVALID and muon(z, d, lp=B + 2 * size - 16) == INVALID
+
+
+def test_matmul_timeout_arguments_are_checked(z):
+    call = lambda *a: z._capi.raw_status("zero_debug_matmul_timeout", *a, None)  # noqa: E731
+    assert call(None, A, 1000) == INVALID and call(A, None, 1000) == INVALID
+    assert call(A + 16, B, 1000) == MISALIGNED and call(A, B + 16, 1000) == MISALIGNED
+    assert call(A, B, 0) == INVALID and call(A, B, 10_000_000_001) == INVALID

@@ -24,10 +24,12 @@ from ._capi import (NOALLOC_SCRATCH_BYTES, ZERO_BF16, ZERO_FP16, ZERO_FP32, ZERO
                     zero_quantize_grads, zero_step_fused_qgz, zero_step_fused_offload, zero_accumulate_grads,
                     zero_step_fused_accum, zero_debug_stream_timeout, zero_step_fused_qgz_qgather, rank_ptrs,
                     zero_step_layers, zero_layers_workspace_bytes, LayerStack, ZeroLayer,
-                    layernorm, zero_layernorm_workspace_bytes, zero_layernorm_forward, zero_layernorm_backward)
+                    layernorm, zero_layernorm_workspace_bytes, zero_layernorm_forward, zero_layernorm_backward,
+                    matrices, muon_hparams, zero_orthogonalize_workspace_bytes, zero_orthogonalize,
+                    zero_muon_workspace_bytes, zero_muon_step, zero_debug_matmul_timeout)
 
 __all__ = ["Plan", "StepBuffers", "read_scalars", "row_len", "hparams", "rank_ptrs", "ZeroError", "ZeroHparams",
-           "LayerStack", "ZeroLayer", "layernorm",
+           "LayerStack", "ZeroLayer", "layernorm", "matrices", "muon_hparams",
            "ZERO_BF16", "ZERO_FP16", "ZERO_FP32", "ZERO_DEV_TIMEOUT", "NOALLOC_SCRATCH_BYTES"] + [n for n in dir(_capi) if n.startswith("zero_")]
 
 

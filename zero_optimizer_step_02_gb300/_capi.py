@@ -74,6 +74,19 @@ class ZeroLayerNorm(ctypes.Structure):
                 ("y_stride", ctypes.c_longlong), ("dy_stride", ctypes.c_longlong), ("dx_stride", ctypes.c_longlong)]
 
 
+class ZeroMatrices(ctypes.Structure):
+    """zero_matrices of zero.h: a batch of equal matrices and the Newton-Schulz schedule."""
+    _fields_ = [("rows", ctypes.c_int), ("cols", ctypes.c_int), ("batch", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("out_dtype", ctypes.c_int), ("in_ld", ctypes.c_longlong), ("out_ld", ctypes.c_longlong),
+                ("in_stride", ctypes.c_longlong), ("out_stride", ctypes.c_longlong), ("steps", ctypes.c_int),
+                ("coefs", ctypes.POINTER(ctypes.c_float)), ("eps", ctypes.c_float), ("products", ctypes.c_int)]
+
+
+class ZeroMuonHparams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("momentum", ctypes.c_float), ("weight_decay", ctypes.c_float),
+                ("rms_scale", ctypes.c_float), ("loss_scale", ctypes.c_float), ("nesterov", ctypes.c_int)]
+
+
 _SIGS = {
     "zero_status_str": (ctypes.c_char_p, [_i32]),
     "zero_abi_version": (_i32, []),
@@ -108,6 +121,12 @@ _SIGS = {
                                            _vp, _vp, _vp]),
     "zero_step_layers": (_i32, [_hp, _i32, ctypes.POINTER(ZeroLayer), _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
                                 _vp]),
+    "zero_orthogonalize_workspace_bytes": (_sz, [ctypes.POINTER(ZeroMatrices)]),
+    "zero_muon_workspace_bytes": (_sz, [ctypes.POINTER(ZeroMatrices)]),
+    "zero_orthogonalize": (_i32, [ctypes.POINTER(ZeroMatrices), _vp, _vp, _vp, _vp, _vp]),
+    "zero_muon_step": (_i32, [ctypes.POINTER(ZeroMatrices), ctypes.POINTER(ZeroMuonHparams), _i32, _vp, _vp, _vp, _vp,
+                              _vp, _vp, _vp]),
+    "zero_debug_matmul_timeout": (_i32, [_vp, _vp, _ll, _vp]),
     "zero_layernorm_workspace_bytes": (_sz, [ctypes.POINTER(ZeroLayerNorm)]),
     "zero_layernorm_forward": (_i32, [ctypes.POINTER(ZeroLayerNorm), _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "zero_layernorm_backward": (_i32, [ctypes.POINTER(ZeroLayerNorm), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
@@ -423,6 +442,59 @@ def zero_layernorm_backward(desc, dy, x, gain, mean, rstd, dx, dgain, dbias, ws,
     _check(_lib.zero_layernorm_backward(ctypes.byref(desc), _addr(dy), _addr(x), _addr(gain), _addr(mean),
                                         _addr(rstd), _addr(dx), _addr(dgain), _addr(dbias), _addr(ws),
                                         _stream(stream)), "zero_layernorm_backward")
+
+
+def matrices(rows, cols, batch=1, dtype=ZERO_BF16, out_dtype=None, in_ld=0, out_ld=0, stride=0, out_stride=None,
+             steps=0, coefs=None, eps=1e-7, products=0):
+    """Descriptor of a batch of equal matrices to orthogonalise.  stride: elements
+    between matrices of the input, and of the output unless out_stride is given
+    (0: packed).  coefs: a sequence of (a, b, c), one for each step, or None for
+    five steps of the default quintic (`steps` of it when given)."""
+    arr = None
+    if coefs is not None:
+        flat = [float(v) for c in coefs for v in c]
+        arr = (ctypes.c_float * len(flat))(*flat)
+        if len(flat) != 3 * len(coefs) or steps not in (0, len(coefs)):
+            raise ValueError("coefs holds one (a, b, c) for each step")
+        steps = len(coefs)
+    d = ZeroMatrices(rows, cols, batch, dtype, dtype if out_dtype is None else out_dtype, in_ld, out_ld, stride,
+                     stride if out_stride is None else out_stride, steps, arr, eps, products)
+    d._coefs = arr    # keeps the array the descriptor points at
+    return d
+
+
+def muon_hparams(lr=0.02, momentum=0.95, weight_decay=0.0, rms_scale=0.0, loss_scale=1.0, nesterov=True):
+    return ZeroMuonHparams(lr, momentum, weight_decay, rms_scale, loss_scale, int(bool(nesterov)))
+
+
+def zero_orthogonalize_workspace_bytes(desc):
+    return _lib.zero_orthogonalize_workspace_bytes(ctypes.byref(desc))
+
+
+def zero_muon_workspace_bytes(desc):
+    return _lib.zero_muon_workspace_bytes(ctypes.byref(desc))
+
+
+def zero_orthogonalize(desc, g, out, ws, scalars=None, stream=None):
+    """out = the orthogonalised g, matrix by matrix; ws: zero_orthogonalize_workspace_bytes(desc) bytes."""
+    _check(_lib.zero_orthogonalize(ctypes.byref(desc), _addr(g), _addr(out), _addr(ws), _addr(scalars),
+                                   _stream(stream)), "zero_orthogonalize")
+
+
+def zero_muon_step(desc, hp, rank_grads, momentum, master, lp_out, ws, scalars=None, stream=None):
+    """One Muon step of the batch: rank mean, momentum, orthogonalised update,
+    fp32 master and 16-bit weights (lp_out, or None); momentum and master in
+    place.  ws: zero_muon_workspace_bytes(desc) bytes."""
+    ranks = _ptr_array(rank_grads)
+    _check(_lib.zero_muon_step(ctypes.byref(desc), ctypes.byref(hp), len(ranks), ranks, _addr(momentum),
+                               _addr(master), _addr(lp_out), _addr(ws), _addr(scalars), _stream(stream)),
+           "zero_muon_step")
+
+
+def zero_debug_matmul_timeout(scratch, scalars, timeout_ns, stream=None):
+    """One matrix product whose copies are never issued: every wait runs out (tests the timeout path)."""
+    _check(_lib.zero_debug_matmul_timeout(_addr(scratch), _addr(scalars), timeout_ns, _stream(stream)),
+           "zero_debug_matmul_timeout")
 
 
 def zero_launch_count():

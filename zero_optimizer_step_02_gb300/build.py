@@ -18,7 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libzero.so")
 BUILD = os.path.join(PKG, "_build")
 
-SOURCES = ["zk_stream.cu", "zk_aux.cu", "zk_capi.cu", "zk_noalloc.cu", "zk_small.cu", "zk_norm.cu",
+SOURCES = ["zk_stream.cu", "zk_aux.cu", "zk_capi.cu", "zk_noalloc.cu", "zk_small.cu", "zk_norm.cu", "zk_ortho.cu",
            "zk_capi_ops.cu"]
 HEADERS = ["zk_common.cuh", "zk_launch.h", "zk_capi.h", "zk_ops.h", "zk_tc.cuh"]
 

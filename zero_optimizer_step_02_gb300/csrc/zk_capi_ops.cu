@@ -72,9 +72,201 @@ zk::LnArgs ln_args(const zero_layernorm* d)
     return a;
 }
 
+// --------------------------------------------------- matrix update batches
+const float kQuintic[3] = {3.4445f, -4.7750f, 2.0315f};
+constexpr int kDefaultSteps = 5;
+
+long long extent(const zero_matrices* d, long long ld) { return (d->rows - 1) * ld + d->cols; }
+
+// The products keep x, its Gram matrix G and b G + c G G in fp16 times 2^12,
+// so their entries (bounded by the largest singular value s of x, by s^2 and
+// by |b s^2 + c s^4|) must stay below 16.  x starts with every singular value
+// in [0, 1]; the schedule is followed over a grid of them.
+bool schedule_fits(int steps, const float* coefs)
+{
+    constexpr int kGrid = 512;
+    for (int i = 0; i <= kGrid; ++i) {
+        double s = static_cast<double>(i) / kGrid;
+        for (int k = 0; k < steps; ++k) {
+            const double a = coefs[3 * k], b = coefs[3 * k + 1], c = coefs[3 * k + 2], g = s * s;
+            const double p = b * g + c * g * g;
+            if (!(g <= 15.0) || !(std::fabs(p) <= 15.0)) return false;
+            s = s * (a + p);
+        }
+        if (!std::isfinite(s)) return false;
+    }
+    return true;
+}
+
+zero_status check_matrices(const zero_matrices* d)
+{
+    if (d == nullptr) return ZERO_ERR_INVALID_ARG;
+    if (d->rows < 1 || d->cols < 1 || d->batch < 1) return ZERO_ERR_INVALID_ARG;
+    if (!dtype_ok(d->dtype) || !dtype_ok(d->out_dtype)) return ZERO_ERR_INVALID_ARG;
+    if (d->steps < 0 || d->steps > ZERO_MAX_NS_STEPS || (d->coefs != nullptr && d->steps == 0)) return ZERO_ERR_INVALID_ARG;
+    if (!(d->eps >= 1e-30f) || std::isinf(d->eps)) return ZERO_ERR_INVALID_ARG;
+    if (d->products != 0 && d->products != 1 && d->products != 3) return ZERO_ERR_INVALID_ARG;
+    if (d->rows > ZERO_MAX_MATRIX_DIM || d->cols > ZERO_MAX_MATRIX_DIM || d->batch > 65535) return ZERO_ERR_BOUNDS;
+    if (static_cast<long long>(d->rows) * d->cols > ZERO_MAX_MATRIX_ELEMS) return ZERO_ERR_BOUNDS;
+    // every kernel numbers its tiles in 32 bits
+    const long long tiles = ((d->rows + 127LL) / 128) * ((d->cols + 63LL) / 64);
+    const long long side = (((d->rows < d->cols ? d->rows : d->cols) + 127LL) / 128) + 1;
+    if ((tiles > side * side ? tiles : side * side) * d->batch > (1LL << 30)) return ZERO_ERR_BOUNDS;
+    const long long ld[] = {d->in_ld, d->out_ld}, st[] = {d->in_stride, d->out_stride};
+    for (int i = 0; i < 2; ++i) {
+        if (ld[i] != 0 && (ld[i] < d->cols || ld[i] > (1LL << 32))) return ZERO_ERR_INVALID_ARG;
+        if (st[i] != 0 && (st[i] < extent(d, stride_of(ld[i], d->cols)) || st[i] > (1LL << 40))) return ZERO_ERR_INVALID_ARG;
+    }
+    if (d->coefs != nullptr && !schedule_fits(d->steps, d->coefs)) return ZERO_ERR_INVALID_ARG;
+    return ZERO_OK;
+}
+
+// products = 0: one product where the result is rounded to bf16, whose own
+// rounding is as large as that product's error; else three.  A short side under
+// kFewRows takes three in any case: the operands' roundings then hardly average
+// out (2 x 3: 7e-3 off, 64 x 64: 1.8e-3, 768 x 768: 1.2e-3), and the products
+// are too short to matter beside the launches.
+constexpr int kFewRows = 256;
+int products_of(const zero_matrices* d, bool muon)
+{
+    if ((d->rows < d->cols ? d->rows : d->cols) < kFewRows) return 3;
+    if (d->products != 0) return d->products;
+    return !muon && d->out_dtype == ZERO_BF16 ? 1 : 3;
+}
+
+void set_schedule(zk::NsArgs& a, const zero_matrices* d)
+{
+    a.rows = d->rows;
+    a.cols = d->cols;
+    a.batch = d->batch;
+    a.steps = d->steps == 0 ? kDefaultSteps : d->steps;
+    for (int i = 0; i < a.steps; ++i)
+        for (int k = 0; k < 3; ++k) a.coef[i][k] = d->coefs != nullptr ? d->coefs[3 * i + k] : kQuintic[k];
+    a.eps = d->eps;
+    a.in_dtype = d->dtype;
+}
+
+bool overlap(const void* p, const void* q, size_t np, size_t nq)
+{
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return a < b + nq && b < a + np;
+}
+
 }  // namespace
 
 extern "C" {
+
+ZERO_API size_t zero_orthogonalize_workspace_bytes(const zero_matrices* d)
+{
+    if (check_matrices(d) != ZERO_OK) return 0;
+    return zk::ns_workspace_bytes(d->rows, d->cols, d->batch, products_of(d, false), false);
+}
+
+ZERO_API size_t zero_muon_workspace_bytes(const zero_matrices* d)
+{
+    if (check_matrices(d) != ZERO_OK) return 0;
+    return zk::ns_workspace_bytes(d->rows, d->cols, d->batch, products_of(d, true), true);
+}
+
+ZERO_API zero_status zero_orthogonalize(const zero_matrices* d, const void* g, void* out, void* ws,
+                                        zero_dev_scalars* sc, void* stream)
+{
+    ZK_CALL_RANGE();
+    zero_status s;
+    if ((s = check_matrices(d)) != ZERO_OK) return s;
+    if ((s = check_elems(g, d->dtype)) != ZERO_OK || (s = check_elems(out, d->out_dtype)) != ZERO_OK) return s;
+    if ((s = zk::check_dev(ws, 256)) != ZERO_OK) return s;
+    if (sc != nullptr && (s = zk::check_dev(sc, 256)) != ZERO_OK) return s;
+    zk::NsArgs a;
+    std::memset(&a, 0, sizeof(a));
+    set_schedule(a, d);
+    a.products = products_of(d, false);
+    a.in = g;
+    a.in_ld = stride_of(d->in_ld, d->cols);
+    a.in_stride = d->in_stride != 0 ? d->in_stride : d->rows * a.in_ld;
+    a.out = out;
+    a.out_dtype = d->out_dtype;
+    a.out_ld = stride_of(d->out_ld, d->cols);
+    a.out_stride = d->out_stride != 0 ? d->out_stride : d->rows * a.out_ld;
+    const size_t ni = static_cast<size_t>((d->batch - 1) * a.in_stride + extent(d, a.in_ld)) * zk::dtype_bytes(d->dtype);
+    const size_t no = static_cast<size_t>((d->batch - 1) * a.out_stride + extent(d, a.out_ld)) * zk::dtype_bytes(d->out_dtype);
+    const size_t nw = zk::ns_workspace_bytes(d->rows, d->cols, d->batch, a.products, false);
+    if (overlap(g, ws, ni, nw) || overlap(out, ws, no, nw)) return ZERO_ERR_INVALID_ARG;
+    a.ws = ws;
+    a.sc = sc;
+    return from_cuda(zk::launch_ns(a, as_stream(stream)));
+}
+
+ZERO_API zero_status zero_muon_step(const zero_matrices* d, const zero_muon_hparams* hp, int n_d,
+                                    const void* const* rank_grads, float* momentum, float* master, void* lp_out,
+                                    void* ws, zero_dev_scalars* sc, void* stream)
+{
+    ZK_CALL_RANGE();
+    zero_status s;
+    if ((s = check_matrices(d)) != ZERO_OK) return s;
+    if (hp == nullptr || rank_grads == nullptr) return ZERO_ERR_INVALID_ARG;
+    if (n_d < 1 || n_d > ZERO_MAX_RANKS) return ZERO_ERR_INVALID_ARG;
+    // the flat parameter space: whole rows, one index for every array
+    if (d->dtype == ZERO_FP32 || d->out_dtype == ZERO_FP32) return ZERO_ERR_INVALID_ARG;
+    if ((d->in_ld != 0 && d->in_ld != d->cols) || (d->out_ld != 0 && d->out_ld != d->cols)) return ZERO_ERR_INVALID_ARG;
+    const long long elems = static_cast<long long>(d->rows) * d->cols;
+    const long long stride = d->in_stride != 0 ? d->in_stride : elems;
+    if (d->out_stride != 0 && d->out_stride != stride) return ZERO_ERR_INVALID_ARG;
+    if (d->batch > 1 && stride % 8 != 0) return ZERO_ERR_MISALIGNED;
+    const float v[] = {hp->lr, hp->momentum, hp->weight_decay, hp->rms_scale, hp->loss_scale};
+    for (float x : v)
+        if (!std::isfinite(x) || x < 0.0f) return ZERO_ERR_INVALID_ARG;
+    if (hp->momentum >= 1.0f || (hp->nesterov != 0 && hp->nesterov != 1)) return ZERO_ERR_INVALID_ARG;
+    for (int r = 0; r < n_d; ++r)
+        if ((s = zk::check_dev(rank_grads[r])) != ZERO_OK) return s;
+    if ((s = zk::check_dev(momentum)) != ZERO_OK || (s = zk::check_dev(master)) != ZERO_OK) return s;
+    if (lp_out != nullptr && (s = zk::check_dev(lp_out)) != ZERO_OK) return s;
+    if ((s = zk::check_dev(ws, 256)) != ZERO_OK) return s;
+    if (sc != nullptr && (s = zk::check_dev(sc, 256)) != ZERO_OK) return s;
+    const int products = products_of(d, true);
+    const size_t n = static_cast<size_t>((d->batch - 1) * stride + elems);
+    const void* arr[] = {momentum, master, lp_out, ws};
+    const size_t len[] = {4 * n, 4 * n, lp_out != nullptr ? 2 * n : 0,
+                          zk::ns_workspace_bytes(d->rows, d->cols, d->batch, products, true)};
+    for (int i = 0; i < 4; ++i) {
+        for (int j = i + 1; j < 4; ++j)
+            if (len[i] != 0 && len[j] != 0 && overlap(arr[i], arr[j], len[i], len[j])) return ZERO_ERR_INVALID_ARG;
+        for (int r = 0; r < n_d; ++r)
+            if (len[i] != 0 && overlap(arr[i], rank_grads[r], len[i], 2 * n)) return ZERO_ERR_INVALID_ARG;
+    }
+    zk::NsArgs a;
+    std::memset(&a, 0, sizeof(a));
+    set_schedule(a, d);
+    a.products = products;
+    a.ranks = rank_grads;
+    a.n_d = n_d;
+    a.divisor = static_cast<float>(n_d) * (hp->loss_scale > 0.0f ? hp->loss_scale : 1.0f);
+    a.mu = hp->momentum;
+    a.nesterov = hp->nesterov;
+    a.momentum = momentum;
+    a.master = master;
+    a.lp = lp_out;
+    a.lp_dtype = d->out_dtype;
+    a.flat_stride = stride;
+    const double ratio = static_cast<double>(d->rows) / d->cols;
+    const double longest = d->rows > d->cols ? d->rows : d->cols;
+    const double scale = hp->rms_scale > 0.0f ? hp->rms_scale * std::sqrt(longest) : std::sqrt(ratio > 1.0 ? ratio : 1.0);
+    a.decay = static_cast<float>(1.0 - static_cast<double>(hp->lr) * hp->weight_decay);
+    a.step = static_cast<float>(hp->lr * scale);
+    a.ws = ws;
+    a.sc = sc;
+    return from_cuda(zk::launch_ns(a, as_stream(stream)));
+}
+
+ZERO_API zero_status zero_debug_matmul_timeout(void* scratch, zero_dev_scalars* sc, long long timeout_ns, void* stream)
+{
+    ZK_CALL_RANGE();
+    zero_status s;
+    if ((s = zk::check_dev(scratch, 256)) != ZERO_OK) return s;
+    if ((s = zk::check_dev(sc, 256)) != ZERO_OK) return s;
+    if (timeout_ns < 1 || timeout_ns > 10000000000LL) return ZERO_ERR_INVALID_ARG;
+    return from_cuda(zk::launch_mm_starved(scratch, sc, static_cast<unsigned long long>(timeout_ns), as_stream(stream)));
+}
 
 ZERO_API size_t zero_layernorm_workspace_bytes(const zero_layernorm* d)
 {

@@ -37,4 +37,43 @@ struct LnArgs {
 cudaError_t launch_ln_forward(const LnArgs& a, cudaStream_t st);
 cudaError_t launch_ln_backward(const LnArgs& a, cudaStream_t st);
 
+// ------------------------------------------- orthogonalised matrix updates
+constexpr int kNsMaxSteps = 32;
+
+// A batch of equal matrices and what becomes of them.
+struct NsArgs {
+    int rows, cols, batch;
+    int steps;
+    float coef[kNsMaxSteps][3];   // a, b, c of x <- a x + (b G + c G G) x, G the Gram matrix
+    float eps;
+    int products;                 // 1: fp16 operands; 3: pairs of fp16 (see zk_ortho.cu)
+    // input: a matrix of `in_dtype`, or (Muon) the rank gradients
+    const void* in;
+    int in_dtype;
+    long long in_ld, in_stride;
+    // output
+    void* out;
+    int out_dtype;
+    long long out_ld, out_stride;
+    // Muon: out is null
+    const void* const* ranks;     // host array
+    int n_d;
+    float divisor, mu;
+    int nesterov;
+    float* momentum;
+    float* master;
+    void* lp;
+    int lp_dtype;
+    float decay, step;
+    long long flat_stride;
+    void* ws;
+    zero_dev_scalars* sc;
+};
+
+size_t ns_workspace_bytes(int rows, int cols, int batch, int products, bool muon);
+cudaError_t launch_ns(const NsArgs& a, cudaStream_t st);
+// one matrix product whose copies are never issued (tests the timeout path);
+// scratch: 16 KB
+cudaError_t launch_mm_starved(void* scratch, zero_dev_scalars* sc, unsigned long long timeout_ns, cudaStream_t st);
+
 }  // namespace zk

@@ -28,6 +28,9 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, int
         : "memory");
 }
 
+// order plain global accesses (made visible to this thread) before later TMA copies
+__device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+
 // ------------------------------------------------- dependent launch (PDL)
 // Everything before pdl_wait() may overlap the previous kernel of the stream;
 // nothing that kernel writes may be touched before it.
