@@ -653,25 +653,6 @@ int sm_count()
     return n;
 }
 
-// a launch that may begin while the previous kernel of the stream drains
-template <typename... P, typename... A>
-cudaError_t launch_after(void (*k)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, const A&... args)
-{
-    cudaLaunchConfig_t c;
-    std::memset(&c, 0, sizeof(c));
-    c.gridDim = grid;
-    c.blockDim = block;
-    c.dynamicSmemBytes = smem;
-    c.stream = st;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    c.attrs = &at;
-    c.numAttrs = 1;
-    count_launch();
-    return cudaLaunchKernelEx(&c, k, args...);
-}
-
 template <int BN, int EPI>
 cudaError_t launch_mm_as(const MmArgs& a, int sms, cudaStream_t st)
 {
