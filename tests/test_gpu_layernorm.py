@@ -150,6 +150,19 @@ def test_strided_and_unaligned_views(rows, cols, dt, pad, shift):
     c.guards_intact()
 
 
+@pytest.mark.parametrize("rows,cols", [(5000, 33), (5001, 130), (4000, 255), (3001, 511), (2500, 1023), (3000, 2047),
+                                       (1300, 4095), (700, 5000), (400, 8191)])
+@pytest.mark.parametrize("dt", [BF16, FP16, FP32])
+def test_many_rows(rows, cols, dt):
+    # full CTAs: as many row groups as registers and shared memory allow
+    c = Case(rows, cols, dt, FP32)
+    c.forward()
+    c.check_forward()
+    c.backward()
+    c.check_backward()
+    c.guards_intact()
+
+
 @pytest.mark.parametrize("gain,bias", [(False, False), (True, False), (False, True)])
 @pytest.mark.parametrize("cols", [768, 1601, 8192])
 def test_without_gain_or_bias(cols, gain, bias):

@@ -6,8 +6,7 @@
 //   dx = rstd * (h - mean_C(h) - xhat * mean_C(h * xhat))
 //   dgain = sum over rows of dy * xhat,  dbias = sum over rows of dy
 //
-// Every sum is fp32 (the last stage of the column sums fp64); the results are
-// rounded once, to the tensor's type.  The sum of squares is taken about the
+// Every sum is fp32; the results are rounded once, to the tensor's type.  The sum of squares is taken about the
 // mean in a second pass over the row, so an offset in x costs no digits.
 #include "zk_common.cuh"
 #include "zk_launch.h"
@@ -162,155 +161,21 @@ __global__ void __launch_bounds__(256) ln_backward_cols(const __grid_constant__ 
     p[a.cols + c] = db;
 }
 
-// ---------------------------------------------------------- wide-load kernels
-// VEC consecutive elements: 16 bytes where bases, strides and the width are
-// multiples of 16 bytes, else one element.  Held as they came from memory and
-// widened at each use, so that a row costs half the registers in 16 bits
-// (keep() makes the compiler forget the widened values it has).
-template <int DT, int VEC>
-struct Chunk;
+// ------------------------------------------------------------- row pipelines
+// A row is cut into chunks of 16 bytes (V = 8 or 4 columns).  A group of
+// `warps` warps takes R consecutive rows at a time, thread t of the group the
+// chunks t, t + width, ... of each (NCH of them); a persistent CTA of `groups`
+// groups walks the rows.  A thread's columns never change, so weights and
+// column sums stay in registers, and the rows to come are already on their way
+// into a ring of DEPTH stages in shared memory (16-byte asynchronous copies).
+//
+// ALIGNED: bases, strides and the width are multiples of 16 bytes.  A thread
+// then fills and empties its own ring slots alone.  Otherwise the group copies
+// the 16-byte words that cover a row as they lie in memory, a chunk is two
+// words of shared memory shifted into place, and results go through shared
+// memory too, so that global memory still sees whole words.
 template <int DT>
-struct Chunk<DT, 8> {
-    uint4 w;
-    __device__ __forceinline__ void keep() { asm volatile("" : "+r"(w.x), "+r"(w.y), "+r"(w.z), "+r"(w.w)); }
-    __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void load(const void* p) { w = __ldcs(static_cast<const uint4*>(p)); }
-    __device__ __forceinline__ void up(float (&v)[8]) const
-    {
-        const uint32_t a[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[2 * i] = Lp<DT>::lo(a[i]), v[2 * i + 1] = Lp<DT>::hi(a[i]);
-    }
-    __device__ static __forceinline__ void store(void* p, const float (&v)[8])
-    {
-        __stcs(static_cast<uint4*>(p), make_uint4(Lp<DT>::narrow2(v[0], v[1]), Lp<DT>::narrow2(v[2], v[3]),
-                                                  Lp<DT>::narrow2(v[4], v[5]), Lp<DT>::narrow2(v[6], v[7])));
-    }
-};
-template <>
-struct Chunk<ZERO_FP32, 4> {
-    float4 w;
-    __device__ __forceinline__ void keep() {}
-    __device__ __forceinline__ void zero() { w = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
-    __device__ __forceinline__ void load(const void* p) { w = __ldcs(static_cast<const float4*>(p)); }
-    __device__ __forceinline__ void up(float (&v)[4]) const { v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w; }
-    __device__ static __forceinline__ void store(void* p, const float (&v)[4])
-    {
-        __stcs(static_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
-    }
-};
-template <int DT>
-struct Chunk<DT, 1> {
-    typename El<DT>::T w;
-    __device__ __forceinline__ void keep() {}
-    __device__ __forceinline__ void zero() { w = 0; }
-    __device__ __forceinline__ void load(const void* p) { w = *static_cast<const typename El<DT>::T*>(p); }
-    __device__ __forceinline__ void up(float (&v)[1]) const { v[0] = El<DT>::up(w); }
-    __device__ static __forceinline__ void store(void* p, const float (&v)[1])
-    {
-        *static_cast<typename El<DT>::T*>(p) = El<DT>::down(v[0]);
-    }
-};
-
-// VEC weights from column c on, in whichever type they have
-template <int VEC>
-__device__ __forceinline__ void weights_at(const void* w, int dt, int c, float none, float (&v)[VEC])
-{
-    if (w == nullptr) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) v[e] = none;
-    } else if (VEC == 1) {
-        v[0] = weight_at(w, dt, c);
-    } else if (dt == ZERO_FP32) {
-#pragma unroll
-        for (int e = 0; e < VEC; e += 4) {
-            const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(w) + c + e);
-            v[e] = x.x, v[e + 1] = x.y, v[e + 2] = x.z, v[e + 3] = x.w;
-        }
-    } else {
-        const uint32_t* p = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(w) + c);
-        uint32_t a[VEC / 2 > 0 ? VEC / 2 : 1];
-        if (VEC == 8) {
-            const uint4 x = *reinterpret_cast<const uint4*>(p);
-            a[0] = x.x, a[1] = x.y, a[VEC / 2 - 2] = x.z, a[VEC / 2 - 1] = x.w;
-        } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(p);
-            a[0] = x.x, a[VEC / 2 - 1] = x.y;
-        }
-#pragma unroll
-        for (int e = 0; e < VEC / 2; ++e) {
-            v[2 * e] = dt == ZERO_BF16 ? Lp<ZERO_BF16>::lo(a[e]) : Lp<ZERO_FP16>::lo(a[e]);
-            v[2 * e + 1] = dt == ZERO_BF16 ? Lp<ZERO_BF16>::hi(a[e]) : Lp<ZERO_FP16>::hi(a[e]);
-        }
-    }
-}
-
-// Forward, the row in registers: NCH chunks a lane, a warp (BLOCK false) or a
-// whole CTA a row.  One read of x, one write of y.
-template <int DT, int VEC, int NCH, bool BLOCK>
-__global__ void __launch_bounds__(BLOCK ? 1024 : 256, BLOCK ? 1 : 2) ln_forward_row(const __grid_constant__ LnArgs a)
-{
-    using T = typename El<DT>::T;
-    __shared__ float red[32];
-    pdl_wait();
-    pdl_launch();
-    const long long r = BLOCK ? blockIdx.x : blockIdx.x * static_cast<long long>(blockDim.x / 32) + (threadIdx.x >> 5);
-    if (r >= a.rows) return;
-    const int t = BLOCK ? threadIdx.x : threadIdx.x & 31, width = BLOCK ? blockDim.x : 32;
-    const T* x = static_cast<const T*>(a.x) + r * a.x_stride;
-    T* y = static_cast<T*>(a.out) + r * a.out_stride;
-    const float inv_c = 1.0f / static_cast<float>(a.cols);
-    Chunk<DT, VEC> v[NCH];
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-        const int c = (t + i * width) * VEC;
-        if (c < a.cols)
-            v[i].load(x + c);
-        else
-            v[i].zero();
-    }
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-        float f[VEC];
-        v[i].up(f);
-        float p = 0.0f;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) p += f[e];
-        s += p;
-    }
-    const float mean = (BLOCK ? block_sum(s, red) : warp_sum(s)) * inv_c;
-    float q = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-        if ((t + i * width) * VEC >= a.cols) break;
-        float f[VEC];
-        v[i].keep();
-        v[i].up(f);
-        float p = 0.0f;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) p = fmaf(f[e] - mean, f[e] - mean, p);
-        q += p;
-    }
-    const float rstd = 1.0f / sqrtf((BLOCK ? block_sum(q, red) : warp_sum(q)) * inv_c + a.eps);
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-        const int c = (t + i * width) * VEC;
-        if (c >= a.cols) break;
-        float f[VEC], g[VEC], b[VEC];
-        v[i].keep();
-        v[i].up(f);
-        weights_at<VEC>(a.gain, a.w_dtype, c, 1.0f, g);
-        weights_at<VEC>(a.bias, a.w_dtype, c, 0.0f, b);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) f[e] = fmaf((f[e] - mean) * rstd, g[e], b[e]);
-        Chunk<DT, VEC>::store(y + c, f);
-    }
-    if (t == 0) {
-        if (a.mean_out != nullptr) a.mean_out[r] = mean;
-        if (a.rstd_out != nullptr) a.rstd_out[r] = rstd;
-    }
-}
+constexpr int kV = DT == ZERO_FP32 ? 4 : 8;
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src)
 {
@@ -323,177 +188,576 @@ __device__ __forceinline__ void cp_async_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Backward: a persistent CTA of `groups` row groups of `warps` warps.  A thread
-// keeps the same NCH * VEC columns for all its rows, so the column sums (and
-// the gain) stay in its registers; the rows to come are on their way into a
-// ring that each thread fills and empties alone (16-byte copies, DEPTH rows;
-// without them the next row waits in registers).  One exchange between the
-// warps of a group for the two row sums, double-buffered.
-template <int DT, int VEC, int NCH, int DEPTH>
-__global__ void __launch_bounds__(512) ln_backward_fused(const __grid_constant__ LnArgs a, int warps, int groups)
+// the compiler forgets that it has this chunk's values widened already
+__device__ __forceinline__ void forget(uint4& w) { asm volatile("" : "+r"(w.x), "+r"(w.y), "+r"(w.z), "+r"(w.w)); }
+
+template <int DT>
+__device__ __forceinline__ void widen(const uint4& w, float (&v)[kV<DT>])
 {
-    using T = typename El<DT>::T;
-    extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ float red[2][16][2];
-    const int width = warps * 32;
-    const int grp = threadIdx.x / width, t = threadIdx.x % width, lane = threadIdx.x & 31, wg = t >> 5;
-    const long long step = static_cast<long long>(gridDim.x) * groups;
-    const T* xb = static_cast<const T*>(a.x);
-    const T* db = static_cast<const T*>(a.dy);
-    const float inv_c = 1.0f / static_cast<float>(a.cols);
-    pdl_wait();
-    pdl_launch();
-    float gain[NCH][VEC], dg[NCH][VEC], dbias[NCH][VEC];
+    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+    if constexpr (DT == ZERO_FP32) {
 #pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-        const int c = (t + i * width) * VEC;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) gain[i][e] = 0.0f, dg[i][e] = 0.0f, dbias[i][e] = 0.0f;
-        if (c < a.cols) weights_at<VEC>(a.gain, a.w_dtype, c, 1.0f, gain[i]);
-    }
-    uint4* ring = reinterpret_cast<uint4*>(smem) + threadIdx.x;   // [DEPTH][2][NCH][blockDim.x]
-    const int slot = 2 * NCH * blockDim.x;
-    Chunk<DT, VEC> nx[NCH], nd[NCH];
-    const long long r0 = static_cast<long long>(blockIdx.x) * groups + grp;
-    auto fetch = [&](long long r, int s) {
-        if (r < a.rows) {
-#pragma unroll
-            for (int i = 0; i < NCH; ++i) {
-                const int c = (t + i * width) * VEC;
-                if (c >= a.cols) break;
-                if (DEPTH > 0) {
-                    cp_async16(ring + s * slot + i * blockDim.x, xb + r * a.x_stride + c);
-                    cp_async16(ring + s * slot + (NCH + i) * blockDim.x, db + r * a.dy_stride + c);
-                } else {
-                    nx[i].load(xb + r * a.x_stride + c);
-                    nd[i].load(db + r * a.dy_stride + c);
-                }
-            }
-        }
-        if (DEPTH > 0) cp_async_commit();
-    };
-    if (DEPTH > 0) {
-        for (int s = 0; s < DEPTH - 1; ++s) fetch(r0 + s * step, s);
+        for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(a[i]);
     } else {
 #pragma unroll
-        for (int i = 0; i < NCH; ++i) nx[i].zero(), nd[i].zero();
-        fetch(r0, 0);
+        for (int i = 0; i < 4; ++i) v[2 * i] = Lp<DT>::lo(a[i]), v[2 * i + 1] = Lp<DT>::hi(a[i]);
     }
-    int s = 0, buf = 0;
-    float mean = 0.0f, rstd = 0.0f;
-    if (r0 < a.rows) mean = a.mean[r0], rstd = a.rstd[r0];
-    for (long long r = r0; r < a.rows; r += step) {
-        Chunk<DT, VEC> cx[NCH], cd[NCH];
-        float mean_n = 0.0f, rstd_n = 0.0f;
-        if (r + step < a.rows) mean_n = a.mean[r + step], rstd_n = a.rstd[r + step];
-        if (DEPTH > 0) {
-            cp_async_wait<DEPTH - 2 >= 0 ? DEPTH - 2 : 0>();
+}
+
+// the same as register pairs, for the packed fp32 operations
+template <int DT>
+__device__ __forceinline__ void widen(const uint4& w, f32x2 (&v)[kV<DT> / 2])
+{
+    float f[kV<DT>];
+    widen<DT>(w, f);
 #pragma unroll
-            for (int i = 0; i < NCH; ++i) {
-                cx[i].zero(), cd[i].zero();
-                if ((t + i * width) * VEC < a.cols) {
-                    *reinterpret_cast<uint4*>(&cx[i]) = ring[s * slot + i * blockDim.x];
-                    *reinterpret_cast<uint4*>(&cd[i]) = ring[s * slot + (NCH + i) * blockDim.x];
+    for (int i = 0; i < kV<DT> / 2; ++i) v[i] = pack2(f[2 * i], f[2 * i + 1]);
+}
+template <int N>
+__device__ __forceinline__ void unpack(const f32x2 (&p)[N], float (&v)[2 * N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) unpack2(p[i], v[2 * i], v[2 * i + 1]);
+}
+__device__ __forceinline__ float both(f32x2 v)
+{
+    float a, b;
+    unpack2(v, a, b);
+    return a + b;
+}
+
+// a chunk without the columns from `cols` on (zeros there); c: its first
+template <int DT>
+__device__ __forceinline__ uint4 masked(const uint4& w, int c, int cols)
+{
+    if (c + kV<DT> <= cols) return w;
+    uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (DT == ZERO_FP32) {
+            if (c + i >= cols) a[i] = 0;
+        } else {
+            if (c + 2 * i >= cols)
+                a[i] = 0;
+            else if (c + 2 * i + 1 >= cols)
+                a[i] &= 0xFFFFu;
+        }
+    }
+    return make_uint4(a[0], a[1], a[2], a[3]);
+}
+
+template <int DT>
+__device__ __forceinline__ uint4 narrowed(const float (&v)[kV<DT>])
+{
+    if constexpr (DT == ZERO_FP32)
+        return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    else
+        return make_uint4(Lp<DT>::narrow2(v[0], v[1]), Lp<DT>::narrow2(v[2], v[3]), Lp<DT>::narrow2(v[4], v[5]),
+                          Lp<DT>::narrow2(v[6], v[7]));
+}
+
+// 16 bytes from byte `off` (0 .. 15, the same in every thread) of two words
+__device__ __forceinline__ uint4 shifted(const uint4& p, const uint4& q, uint32_t off)
+{
+    uint32_t w[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+    if (off & 8u) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (off & 4u) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    if (off & 2u) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A [rows, cols] array read row by row.
+template <int DT>
+struct RowSource {
+    using T = typename El<DT>::T;
+    const T* base;
+    long long stride;
+    uintptr_t lo, hi;   // the bytes from the first row's first to the last row's last element
+
+    __device__ __forceinline__ RowSource(const void* p, long long s, long long rows, int cols)
+        : base(static_cast<const T*>(p)), stride(s), lo(reinterpret_cast<uintptr_t>(p)),
+          hi(lo + static_cast<uintptr_t>((rows - 1) * s + cols) * sizeof(T))
+    {
+    }
+    __device__ __forceinline__ uintptr_t row(long long r) const { return reinterpret_cast<uintptr_t>(base + r * stride); }
+
+    // The words that cover row r into dst, word j by thread j, j + width, ...
+    // Every word lies inside the array but for the first of the first row and
+    // the last of the last one, which are copied element by element.
+    __device__ __forceinline__ void copy_words(uint4* dst, long long r, int cols, int t, int width) const
+    {
+        const uintptr_t from = row(r), to = from + static_cast<uintptr_t>(cols) * sizeof(T);
+        uintptr_t at = (from & ~static_cast<uintptr_t>(15)) + 16u * t;
+        for (int j = t; at < to; j += width, at += 16u * width) {
+            if (at >= lo && at + 16 <= hi) {
+                cp_async16(dst + j, reinterpret_cast<const void*>(at));
+            } else {
+                T* d = reinterpret_cast<T*>(dst + j);
+                for (int e = 0; e < static_cast<int>(16 / sizeof(T)); ++e) {
+                    const uintptr_t q = at + e * sizeof(T);
+                    if (q >= from && q < to) d[e] = *reinterpret_cast<const T*>(q);
                 }
             }
-            fetch(r + (DEPTH - 1) * step, s == 0 ? DEPTH - 1 : s - 1);
-            s = s + 1 == DEPTH ? 0 : s + 1;
+        }
+    }
+};
+
+// A row's results from shared memory, where they lie chunk by chunk from word 1
+// on (word 0 may hold anything), to memory in whole words but at its ends.
+template <int DT>
+__device__ __forceinline__ void write_words(const uint4* src, uintptr_t from, int cols, int t, int width)
+{
+    using T = typename El<DT>::T;
+    const uint32_t off = from & 15u;
+    const uintptr_t to = from + static_cast<uintptr_t>(cols) * sizeof(T);
+    uintptr_t at = from - off + 16u * t;
+    for (int j = t; at < to; j += width, at += 16u * width) {
+        const uint4 w = off == 0 ? src[j + 1] : shifted(src[j], src[j + 1], 16u - off);
+        if (at >= from && at + 16 <= to) {
+            __stcs(reinterpret_cast<uint4*>(at), w);
         } else {
+            const uint32_t a[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int i = 0; i < NCH; ++i) cx[i] = nx[i], cd[i] = nd[i];
-            fetch(r + step, 0);
-        }
-        float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NCH; ++i) {
-            if ((t + i * width) * VEC >= a.cols) break;
-            float x[VEC], d[VEC];
-            cx[i].up(x);
-            cd[i].up(d);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float xhat = (x[e] - mean) * rstd, h = d[e] * gain[i][e];
-                dg[i][e] = fmaf(d[e], xhat, dg[i][e]);
-                dbias[i][e] += d[e];
-                s1 += h;
-                s2 = fmaf(h, xhat, s2);
-            }
-        }
-        s1 = warp_sum(s1);
-        s2 = warp_sum(s2);
-        if (warps > 1) {
-            if (lane == 0) red[buf][threadIdx.x >> 5][0] = s1, red[buf][threadIdx.x >> 5][1] = s2;
-            named_bar_sync(1 + grp, width);
-            s1 = s2 = 0.0f;
-            for (int w = 0; w < warps; ++w) s1 += red[buf][grp * warps + w][0], s2 += red[buf][grp * warps + w][1];
-            buf ^= 1;
-        }
-        s1 *= inv_c;
-        s2 *= inv_c;
-        T* out = static_cast<T*>(a.out) + r * a.out_stride;
-#pragma unroll
-        for (int i = 0; i < NCH; ++i) {
-            const int c = (t + i * width) * VEC;
-            if (c >= a.cols) break;
-            float x[VEC], d[VEC];
-            cx[i].keep();
-            cd[i].keep();
-            cx[i].up(x);
-            cd[i].up(d);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) x[e] = rstd * (fmaf(d[e], gain[i][e], -s1) - (x[e] - mean) * rstd * s2);
-            Chunk<DT, VEC>::store(out + c, x);
-        }
-        mean = mean_n, rstd = rstd_n;
-    }
-    // the CTA's column sums: its row groups add up one after the other (the
-    // ring's memory is free by then), then one row of partial sums leaves
-    float* p = a.parts + static_cast<long long>(blockIdx.x) * 2 * a.cols;
-    float* acc = reinterpret_cast<float*>(smem);
-    if (groups > 1) {
-        cp_async_wait<0>();
-        __syncthreads();
-        for (int g = groups - 1; g > 0; --g) {
-            if (grp == g) {
-#pragma unroll
-                for (int i = 0; i < NCH; ++i)
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        const int k = (i * VEC + e) * 2 * width + t;
-                        acc[k] = dg[i][e] + (g < groups - 1 ? acc[k] : 0.0f);
-                        acc[k + width] = dbias[i][e] + (g < groups - 1 ? acc[k + width] : 0.0f);
-                    }
-            }
-            __syncthreads();
-        }
-    }
-    if (grp == 0) {
-#pragma unroll
-        for (int i = 0; i < NCH; ++i) {
-            const int c = (t + i * width) * VEC;
-            if (c >= a.cols) break;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const int k = (i * VEC + e) * 2 * width + t;
-                p[c + e] = dg[i][e] + (groups > 1 ? acc[k] : 0.0f);
-                p[a.cols + c + e] = dbias[i][e] + (groups > 1 ? acc[k + width] : 0.0f);
+            for (int e = 0; e < static_cast<int>(16 / sizeof(T)); ++e) {
+                const uintptr_t q = at + e * sizeof(T);
+                if (q < from || q >= to) continue;
+                if constexpr (sizeof(T) == 4)
+                    *reinterpret_cast<uint32_t*>(q) = a[e];
+                else
+                    *reinterpret_cast<uint16_t*>(q) = static_cast<uint16_t>(a[e / 2] >> (16 * (e & 1)));
             }
         }
     }
 }
 
+// V weights from column c on, in whichever type they have; `none` without a
+// vector, 0 past the last column
+template <int V>
+__device__ __forceinline__ void weights_at(const void* w, int dt, int c, int cols, float none, f32x2 (&v)[V / 2])
+{
+    float f[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) f[e] = c + e >= cols ? 0.0f : w == nullptr ? none : weight_at(w, dt, c + e);
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) v[e] = pack2(f[2 * e], f[2 * e + 1]);
+}
+
+constexpr int kMaxWarps = 16;   // of a group
+
+// Sums of N values over a group of `warps` warps, the same in all its threads.
+// Each shuffle step carries as many values as are still apart (N = 4: six
+// shuffles for twenty); red: this group's kMaxWarps * N floats.
+template <int N>
+__device__ __forceinline__ void group_sums(float (&v)[N], float* red, int warps, int bar, int width, int wg)
+{
+    static_assert(N == 1 || N == 2 || N == 4 || N == 8, "");
+    const int lane = threadIdx.x & 31;
+    // halve the values while lanes are left to carry them: lane bits 16, 8, 4
+    // end up naming the value a lane holds
+    int o = 16;
+#pragma unroll
+    for (int n = N; n > 1; n /= 2, o /= 2) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int k = 0; k < n / 2; ++k) {
+            const float keep = up ? v[k + n / 2] : v[k], send = up ? v[k] : v[k + n / 2];
+            v[k] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, o);
+        }
+    }
+    float x = v[0];
+#pragma unroll
+    for (int q = 16 / N; q > 0; q /= 2) x += __shfl_xor_sync(0xFFFFFFFFu, x, q);
+    constexpr int kStep = 32 / N;   // lane k * kStep holds value k
+    if (warps == 1) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] = N == 1 ? x : __shfl_sync(0xFFFFFFFFu, x, k * kStep);
+        return;
+    }
+    if (lane % kStep == 0) red[wg * N + lane / kStep] = x;
+    named_bar_sync(bar, width);
+    // red holds kMaxWarps rows of N (zeros past the group's warps): every lane
+    // takes N / 2 neighbouring sums, and lanes with the same values meet
+    constexpr int P = N > 1 ? N / 2 : 1;
+    float y[P];
+#pragma unroll
+    for (int k = 0; k < P; ++k) y[k] = red[(lane * P + k) % (kMaxWarps * N)];
+#pragma unroll
+    for (int q = N > 1 ? 2 : 1; q < (N > 1 ? 32 : 16); q *= 2)
+#pragma unroll
+        for (int k = 0; k < P; ++k) y[k] += __shfl_xor_sync(0xFFFFFFFFu, y[k], q);
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = N > 1 ? __shfl_sync(0xFFFFFFFFu, y[k % P], k / P) : y[0];
+}
+
+// words of shared memory that one row's copy takes: its chunks, one more for
+// the shift, one that a shifted read may touch; as many for a row of results
+__host__ __device__ constexpr int row_words(int chunks) { return chunks + 2; }
+
+// the threads of a group meet (a group of one warp needs no barrier of its own)
+__device__ __forceinline__ void group_sync(int grp, int warps, int width)
+{
+    if (warps == 1)
+        __syncwarp();
+    else
+        named_bar_sync(1 + grp, width);
+}
+
+template <int DT, int NCH, int R, int DEPTH, int MINB, bool ALIGNED>
+__global__ void __launch_bounds__(512, MINB)
+    ln_forward_rows(const __grid_constant__ LnArgs a, int warps, int groups)
+{
+    constexpr int V = kV<DT>;
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ float red[2][8][kMaxWarps * R];
+    const int width = warps * 32, grp = threadIdx.x / width, t = threadIdx.x % width, wg = t >> 5;
+    const int chunks = (a.cols + V - 1) / V, words = row_words(chunks);
+    const float inv_c = 1.0f / static_cast<float>(a.cols);
+    for (int i = threadIdx.x; i < 2 * 8 * kMaxWarps * R; i += blockDim.x) (&red[0][0][0])[i] = 0.0f;
+    __syncthreads();
+    pdl_wait();
+    pdl_launch();
+    f32x2 gain[NCH][V / 2], bias[NCH][V / 2];
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+        weights_at<V>(a.gain, a.w_dtype, (t + i * width) * V, a.cols, 1.0f, gain[i]);
+        weights_at<V>(a.bias, a.w_dtype, (t + i * width) * V, a.cols, 0.0f, bias[i]);
+    }
+    const RowSource<DT> x(a.x, a.x_stride, a.rows, a.cols);
+    // ALIGNED: [DEPTH][R][NCH][threads], else a group's [DEPTH][R][words] and [R][words] of results
+    uint4* ring = reinterpret_cast<uint4*>(smem) + (ALIGNED ? threadIdx.x : grp * (DEPTH + 1) * R * words);
+    uint4* outs = ring + DEPTH * R * words;
+    auto fetch = [&](long long r0, int s) {
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            if (r0 + k >= a.rows) break;
+            if (ALIGNED) {
+#pragma unroll
+                for (int i = 0; i < NCH; ++i)
+                    if (t + i * width < chunks)
+                        cp_async16(ring + ((s * R + k) * NCH + i) * blockDim.x, x.base + (r0 + k) * x.stride + (t + i * width) * V);
+            } else {
+                x.copy_words(ring + (s * R + k) * words, r0 + k, a.cols, t, width);
+            }
+        }
+        cp_async_commit();
+    };
+    const long long step = static_cast<long long>(gridDim.x) * groups * R;
+    long long r0 = (static_cast<long long>(blockIdx.x) * groups + grp) * R;
+    for (int s = 0; s < DEPTH - 1; ++s) fetch(r0 + s * step, s);
+    for (int s = 0; r0 < a.rows; r0 += step, s = s + 1 == DEPTH ? 0 : s + 1) {
+        cp_async_wait<DEPTH - 2>();
+        if (!ALIGNED) group_sync(grp, warps, width);
+        uint4 w[R][NCH];
+#pragma unroll
+        for (int k = 0; k < R; ++k)
+#pragma unroll
+            for (int i = 0; i < NCH; ++i) {
+                w[k][i] = make_uint4(0, 0, 0, 0);
+                if (t + i * width >= chunks || r0 + k >= a.rows) continue;
+                if (ALIGNED) {
+                    w[k][i] = ring[((s * R + k) * NCH + i) * blockDim.x];
+                } else {
+                    const uint4* p = ring + (s * R + k) * words + t + i * width;
+                    w[k][i] = masked<DT>(shifted(p[0], p[1], x.row(r0 + k) & 15u), (t + i * width) * V, a.cols);
+                }
+            }
+        fetch(r0 + (DEPTH - 1) * step, s == 0 ? DEPTH - 1 : s - 1);
+        float mean[R], rstd[R];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            f32x2 sum = 0;
+#pragma unroll
+            for (int i = 0; i < NCH; ++i) {
+                f32x2 f[V / 2];
+                widen<DT>(w[k][i], f);
+#pragma unroll
+                for (int e = 0; e < V / 2; ++e) sum = add2(sum, f[e]);
+            }
+            mean[k] = both(sum);
+        }
+        group_sums<R>(mean, red[0][grp & 7], warps, 1 + grp, width, wg);
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            mean[k] *= inv_c;
+            const f32x2 m = pack2(mean[k], mean[k]);
+            f32x2 sum = 0;
+#pragma unroll
+            for (int i = 0; i < NCH; ++i) {
+                const int c = (t + i * width) * V;
+                forget(w[k][i]);
+                if (c + V <= a.cols) {
+                    f32x2 f[V / 2];
+                    widen<DT>(w[k][i], f);
+#pragma unroll
+                    for (int e = 0; e < V / 2; ++e) {
+                        f[e] = sub2(f[e], m);
+                        sum = fma2(f[e], f[e], sum);
+                    }
+                } else if (!ALIGNED && c < a.cols) {
+                    float f[V], part = 0.0f;
+                    widen<DT>(w[k][i], f);
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        if (c + e < a.cols) part = fmaf(f[e] - mean[k], f[e] - mean[k], part);
+                    sum = add2(sum, pack2(part, 0.0f));
+                }
+            }
+            rstd[k] = both(sum);
+        }
+        group_sums<R>(rstd, red[1][grp & 7], warps, 1 + grp, width, wg);
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            if (r0 + k >= a.rows) break;
+            rstd[k] = 1.0f / sqrtf(rstd[k] * inv_c + a.eps);
+            const RowSource<DT> y(a.out, a.out_stride, a.rows, a.cols);
+            // xhat in one operation: x * rstd - mean * rstd
+            const f32x2 rs = pack2(rstd[k], rstd[k]), nm = pack2(-mean[k] * rstd[k], -mean[k] * rstd[k]);
+#pragma unroll
+            for (int i = 0; i < NCH; ++i) {
+                const int c = (t + i * width) * V;
+                if (c >= a.cols) break;
+                f32x2 f[V / 2];
+                float o[V];
+                forget(w[k][i]);
+                widen<DT>(w[k][i], f);
+#pragma unroll
+                for (int e = 0; e < V / 2; ++e) f[e] = fma2(fma2(f[e], rs, nm), gain[i][e], bias[i][e]);
+                unpack(f, o);
+                if (ALIGNED)
+                    __stcs(reinterpret_cast<uint4*>(y.row(r0 + k)) + t + i * width, narrowed<DT>(o));
+                else
+                    outs[k * words + 1 + t + i * width] = narrowed<DT>(o);
+            }
+            if (t == 0) {
+                if (a.mean_out != nullptr) a.mean_out[r0 + k] = mean[k];
+                if (a.rstd_out != nullptr) a.rstd_out[r0 + k] = rstd[k];
+            }
+        }
+        if (!ALIGNED) {
+            group_sync(grp, warps, width);
+            const RowSource<DT> y(a.out, a.out_stride, a.rows, a.cols);
+#pragma unroll
+            for (int k = 0; k < R; ++k)
+                if (r0 + k < a.rows) write_words<DT>(outs + k * words, y.row(r0 + k), a.cols, t, width);
+        }
+    }
+}
+
+template <int DT, int NCH, int R, int DEPTH, int MINB, bool ALIGNED>
+__global__ void __launch_bounds__(512, MINB)
+    ln_backward_rows_fused(const __grid_constant__ LnArgs a, int warps, int groups)
+{
+    constexpr int V = kV<DT>;
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ float red[2][8][kMaxWarps * 2 * R];
+    const int width = warps * 32, grp = threadIdx.x / width, t = threadIdx.x % width, wg = t >> 5;
+    const int chunks = (a.cols + V - 1) / V, words = row_words(chunks);
+    const float inv_c = 1.0f / static_cast<float>(a.cols);
+    for (int i = threadIdx.x; i < 2 * 8 * kMaxWarps * 2 * R; i += blockDim.x) (&red[0][0][0])[i] = 0.0f;
+    __syncthreads();
+    pdl_wait();
+    pdl_launch();
+    f32x2 gain[NCH][V / 2], dg2[NCH][V / 2], db2[NCH][V / 2];
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+        weights_at<V>(a.gain, a.w_dtype, (t + i * width) * V, a.cols, 1.0f, gain[i]);
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) dg2[i][e] = db2[i][e] = 0;
+    }
+    const RowSource<DT> x(a.x, a.x_stride, a.rows, a.cols), dy(a.dy, a.dy_stride, a.rows, a.cols);
+    // ALIGNED: [DEPTH][R][2][NCH][threads], else a group's [DEPTH][R][2][words] and [R][words] of results
+    uint4* ring = reinterpret_cast<uint4*>(smem) + (ALIGNED ? threadIdx.x : grp * (2 * DEPTH + 1) * R * words);
+    uint4* outs = ring + 2 * DEPTH * R * words;
+    auto fetch = [&](long long r0, int s) {
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            if (r0 + k >= a.rows) break;
+            if (ALIGNED) {
+#pragma unroll
+                for (int i = 0; i < NCH; ++i)
+                    if (t + i * width < chunks) {
+                        uint4* p = ring + ((s * R + k) * 2 * NCH + i) * blockDim.x;
+                        cp_async16(p, x.base + (r0 + k) * x.stride + (t + i * width) * V);
+                        cp_async16(p + NCH * blockDim.x, dy.base + (r0 + k) * dy.stride + (t + i * width) * V);
+                    }
+            } else {
+                uint4* p = ring + (s * R + k) * 2 * words;
+                x.copy_words(p, r0 + k, a.cols, t, width);
+                dy.copy_words(p + words, r0 + k, a.cols, t, width);
+            }
+        }
+        cp_async_commit();
+    };
+    const long long step = static_cast<long long>(gridDim.x) * groups * R;
+    long long r0 = (static_cast<long long>(blockIdx.x) * groups + grp) * R;
+    for (int s = 0; s < DEPTH - 1; ++s) fetch(r0 + s * step, s);
+    float mean[R], rstd[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) mean[k] = r0 + k < a.rows ? a.mean[r0 + k] : 0.0f, rstd[k] = r0 + k < a.rows ? a.rstd[r0 + k] : 0.0f;
+    int buf = 0;
+    for (int s = 0; r0 < a.rows; r0 += step, s = s + 1 == DEPTH ? 0 : s + 1, buf ^= 1) {
+        cp_async_wait<DEPTH - 2>();
+        if (!ALIGNED) group_sync(grp, warps, width);
+        uint4 wx[R][NCH], wd[R][NCH];
+#pragma unroll
+        for (int k = 0; k < R; ++k)
+#pragma unroll
+            for (int i = 0; i < NCH; ++i) {
+                wx[k][i] = wd[k][i] = make_uint4(0, 0, 0, 0);
+                if (t + i * width >= chunks || r0 + k >= a.rows) continue;
+                if (ALIGNED) {
+                    const uint4* p = ring + ((s * R + k) * 2 * NCH + i) * blockDim.x;
+                    wx[k][i] = p[0];
+                    wd[k][i] = p[NCH * blockDim.x];
+                } else {
+                    const uint4* p = ring + (s * R + k) * 2 * words + t + i * width;
+                    const int c = (t + i * width) * V;
+                    wx[k][i] = masked<DT>(shifted(p[0], p[1], x.row(r0 + k) & 15u), c, a.cols);
+                    wd[k][i] = masked<DT>(shifted(p[words], p[words + 1], dy.row(r0 + k) & 15u), c, a.cols);
+                }
+            }
+        fetch(r0 + (DEPTH - 1) * step, s == 0 ? DEPTH - 1 : s - 1);
+        float next_mean[R], next_rstd[R];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const long long r = r0 + step + k;
+            next_mean[k] = r < a.rows ? a.mean[r] : 0.0f;
+            next_rstd[k] = r < a.rows ? a.rstd[r] : 0.0f;
+        }
+        // chunks and columns past the row are zeros and add nothing
+        float sum[2 * R];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const f32x2 rs = pack2(rstd[k], rstd[k]), nm = pack2(-mean[k] * rstd[k], -mean[k] * rstd[k]);
+            f32x2 s1 = 0, s2 = 0;
+#pragma unroll
+            for (int i = 0; i < NCH; ++i) {
+                f32x2 xv[V / 2], dv[V / 2];
+                widen<DT>(wx[k][i], xv);
+                widen<DT>(wd[k][i], dv);
+#pragma unroll
+                for (int e = 0; e < V / 2; ++e) {
+                    const f32x2 xhat = fma2(xv[e], rs, nm), h = mul2(dv[e], gain[i][e]);
+                    dg2[i][e] = fma2(dv[e], xhat, dg2[i][e]);
+                    db2[i][e] = add2(db2[i][e], dv[e]);
+                    s1 = add2(s1, h);
+                    s2 = fma2(h, xhat, s2);
+                }
+            }
+            sum[2 * k] = both(s1);
+            sum[2 * k + 1] = both(s2);
+        }
+        group_sums<2 * R>(sum, red[buf][grp & 7], warps, 1 + grp, width, wg);
+        const RowSource<DT> out(a.out, a.out_stride, a.rows, a.cols);
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            if (r0 + k >= a.rows) break;
+            // dx = rstd * (dy * gain - s1 - xhat * s2)
+            const float s1 = sum[2 * k] * inv_c, s2 = sum[2 * k + 1] * inv_c;
+            const f32x2 m = pack2(mean[k], mean[k]), rs = pack2(rstd[k], rstd[k]), n1 = pack2(-s1, -s1);
+            const f32x2 n2 = pack2(-s2 * rstd[k], -s2 * rstd[k]);
+#pragma unroll
+            for (int i = 0; i < NCH; ++i) {
+                const int c = (t + i * width) * V;
+                if (c >= a.cols) break;
+                f32x2 xv[V / 2], dv[V / 2];
+                float o[V];
+                forget(wx[k][i]);
+                forget(wd[k][i]);
+                widen<DT>(wx[k][i], xv);
+                widen<DT>(wd[k][i], dv);
+#pragma unroll
+                for (int e = 0; e < V / 2; ++e)
+                    xv[e] = mul2(rs, fma2(sub2(xv[e], m), n2, fma2(dv[e], gain[i][e], n1)));
+                unpack(xv, o);
+                if (ALIGNED)
+                    __stcs(reinterpret_cast<uint4*>(out.row(r0 + k)) + t + i * width, narrowed<DT>(o));
+                else
+                    outs[k * words + 1 + t + i * width] = narrowed<DT>(o);
+            }
+        }
+        if (!ALIGNED) {
+            group_sync(grp, warps, width);
+#pragma unroll
+            for (int k = 0; k < R; ++k)
+                if (r0 + k < a.rows) write_words<DT>(outs + k * words, out.row(r0 + k), a.cols, t, width);
+        }
+#pragma unroll
+        for (int k = 0; k < R; ++k) mean[k] = next_mean[k], rstd[k] = next_rstd[k];
+    }
+    float dg[NCH][V], db[NCH][V];
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+        unpack(dg2[i], dg[i]);
+        unpack(db2[i], db[i]);
+    }
+    // the CTA's column sums: its row groups add up pairwise through the ring's
+    // memory (free by then), then one row of partial sums leaves
+    float* p = a.parts + static_cast<long long>(blockIdx.x) * 2 * a.cols;
+    float* acc = reinterpret_cast<float*>(smem);
+    if (groups > 1) {
+        cp_async_wait<0>();
+        __syncthreads();
+        for (int n = groups, h = (n + 1) / 2; n > 1; n = h, h = (n + 1) / 2) {
+#pragma unroll
+            for (int i = 0; i < NCH; ++i)
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const int k = (i * V + e) * 2 * width + t;
+                    if (grp >= h && grp < n) {
+                        acc[(grp - h) * NCH * V * 2 * width + k] = dg[i][e];
+                        acc[(grp - h) * NCH * V * 2 * width + k + width] = db[i][e];
+                    }
+                }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < NCH; ++i)
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const int k = (i * V + e) * 2 * width + t;
+                    if (grp < n - h) {
+                        dg[i][e] += acc[grp * NCH * V * 2 * width + k];
+                        db[i][e] += acc[grp * NCH * V * 2 * width + k + width];
+                    }
+                }
+            __syncthreads();
+        }
+    }
+    if (grp == 0) {
+#pragma unroll
+        for (int i = 0; i < NCH; ++i)
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const int c = (t + i * width) * V + e;
+                if (c >= a.cols) break;
+                p[c] = dg[i][e];
+                p[a.cols + c] = db[i][e];
+            }
+    }
+}
+
 // The partial column sums, in a fixed order: 32 columns a CTA, sixteen slices
-// of the parts side by side, fp64.
+// of the parts side by side.
 __global__ void __launch_bounds__(512) ln_backward_finish(const __grid_constant__ LnArgs a, int parts)
 {
-    __shared__ double red[16][33];
-    pdl_wait();
+    __shared__ float red[16][33];
     const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
     const int i = blockIdx.x * 32 + lane;
-    double s = 0.0;
+    const float* p = a.parts + i;
+    pdl_wait();
+    float s = 0.0f;
     if (i < 2 * a.cols) {
-#pragma unroll 8
-        for (int p = slice; p < parts; p += 16) s += static_cast<double>(a.parts[static_cast<long long>(p) * 2 * a.cols + i]);
+#pragma unroll 10
+        for (int k = slice; k < parts; k += 16) s += p[static_cast<long long>(k) * 2 * a.cols];
     }
     red[slice][lane] = s;
     __syncthreads();
@@ -501,8 +765,14 @@ __global__ void __launch_bounds__(512) ln_backward_finish(const __grid_constant_
     const bool bias = i >= a.cols;
     void* out = bias ? a.dbias : a.dgain;
     if (out == nullptr) return;
-    for (int k = 1; k < 16; ++k) s += red[k][lane];
-    put_weight(out, a.w_dtype, bias ? i - a.cols : i, static_cast<float>(s));
+    float v[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[k] = red[k][lane];
+#pragma unroll
+    for (int n = 8; n > 0; n /= 2)
+#pragma unroll
+        for (int k = 0; k < n; ++k) v[k] += v[k + n];
+    put_weight(out, a.w_dtype, bias ? i - a.cols : i, v[0]);
 }
 
 // ------------------------------------------------------------------- host
@@ -516,114 +786,117 @@ int sms_of_device()
 
 bool wide(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-template <int DT, int VEC, int NCH>
-cudaError_t forward_row(const LnArgs& a, int sms, cudaStream_t st)
+constexpr size_t kRowSmem = 220 * 1024;   // of the 227 KB a CTA may have
+
+// how a launch cuts its rows up
+struct RowShape {
+    int warps, groups, threads;
+    long long grid;
+};
+
+// Groups share a CTA of up to 512 threads, fewer where the rows would not
+// cover the SMs otherwise.
+RowShape row_shape(const LnArgs& a, int chunks, int nch, int r, int per_sm, size_t group_smem, int sms)
 {
-    // a warp a row; as few rows a CTA as spreads them over the SMs
-    const long long per = (a.rows + sms - 1) / sms;
-    const int warps = per < 8 ? static_cast<int>(per) : 8;
-    return launch_after(ln_forward_row<DT, VEC, NCH, false>, dim3(static_cast<unsigned>((a.rows + warps - 1) / warps)),
-                        dim3(32 * warps), 0, st, a);
+    RowShape s;
+    s.warps = (chunks + 32 * nch - 1) / (32 * nch);
+    const long long sets = (a.rows + r - 1) / r;
+    const long long spread = (sets + sms - 1) / sms;
+    s.groups = kMaxWarps / s.warps;
+    if (s.groups > static_cast<int>(kRowSmem / per_sm / group_smem)) s.groups = static_cast<int>(kRowSmem / per_sm / group_smem);
+    if (s.groups > spread) s.groups = static_cast<int>(spread);
+    s.threads = 32 * s.warps * s.groups;
+    s.grid = (sets + s.groups - 1) / s.groups;
+    if (s.grid > static_cast<long long>(sms) * per_sm) s.grid = static_cast<long long>(sms) * per_sm;
+    return s;
 }
 
-template <int DT, int VEC, int NCH>
-cudaError_t forward_block(const LnArgs& a, int chunks, cudaStream_t st)
+template <typename K>
+cudaError_t launch_rows(K kernel, const LnArgs& a, const RowShape& s, size_t smem, cudaStream_t st)
 {
-    const int threads = ((chunks + NCH - 1) / NCH + 31) / 32 * 32;
-    return launch_after(ln_forward_row<DT, VEC, NCH, true>, dim3(static_cast<unsigned>(a.rows)), dim3(threads), 0, st, a);
-}
-
-// A row stays in a warp's registers up to kWarpChunks chunks a lane (16 x 16
-// bytes: 4096 columns in 16 bits; 64 single elements), in a CTA's up to four
-// (16 single) a thread; wider rows are read again for each pass.
-template <int DT, int VEC>
-cudaError_t forward_vec(const LnArgs& a, int sms, cudaStream_t st, bool& done)
-{
-    done = true;
-    const int chunks = (a.cols + VEC - 1) / VEC;
-    if (a.rows < (1LL << 31)) {
-        if constexpr (VEC > 1) {
-            if (chunks <= 32) return forward_row<DT, VEC, 1>(a, sms, st);
-            if (chunks <= 64) return forward_row<DT, VEC, 2>(a, sms, st);
-            if (chunks <= 96) return forward_row<DT, VEC, 3>(a, sms, st);
-            if (chunks <= 128) return forward_row<DT, VEC, 4>(a, sms, st);
-            if (chunks <= 256) return forward_row<DT, VEC, 8>(a, sms, st);
-            if (chunks <= 512) return forward_row<DT, VEC, 16>(a, sms, st);
-            if (chunks <= 4096) return forward_block<DT, VEC, 4>(a, chunks, st);
-        } else {
-            if (chunks <= 256) return forward_row<DT, VEC, 8>(a, sms, st);
-            if (chunks <= 1024) return forward_row<DT, VEC, 32>(a, sms, st);
-            if (chunks <= 2048) return forward_row<DT, VEC, 64>(a, sms, st);
-            if (chunks <= 16384) return forward_block<DT, VEC, 16>(a, chunks, st);
-        }
+    if (smem > 40 * 1024) {   // 48 KB without asking, the static arrays included
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
     }
-    done = false;
-    return cudaSuccess;
+    return launch_after(kernel, dim3(static_cast<unsigned>(s.grid)), dim3(s.threads), smem, st, a, s.warps, s.groups);
 }
+
+template <int DT, int NCH, int R, int DEPTH, int MINB, bool ALIGNED>
+cudaError_t forward_as(const LnArgs& a, int sms, cudaStream_t st)
+{
+    const int chunks = (a.cols + kV<DT> - 1) / kV<DT>;
+    const int warps = (chunks + 32 * NCH - 1) / (32 * NCH);
+    const size_t per = 16u * R * (ALIGNED ? static_cast<size_t>(DEPTH) * NCH * 32 * warps : static_cast<size_t>(DEPTH + 1) * row_words(chunks));
+    const RowShape s = row_shape(a, chunks, NCH, R, MINB, per, sms);
+    return launch_rows(ln_forward_rows<DT, NCH, R, DEPTH, MINB, ALIGNED>, a, s, per * s.groups, st);
+}
+
+template <int DT, int NCH, int R, int DEPTH, int MINB, bool ALIGNED>
+cudaError_t backward_as(const LnArgs& a, int sms, cudaStream_t st, int& parts)
+{
+    const int chunks = (a.cols + kV<DT> - 1) / kV<DT>;
+    const int warps = (chunks + 32 * NCH - 1) / (32 * NCH);
+    const size_t per = 16u * R * (ALIGNED ? static_cast<size_t>(2 * DEPTH) * NCH * 32 * warps : static_cast<size_t>(2 * DEPTH + 1) * row_words(chunks));
+    RowShape s = row_shape(a, chunks, NCH, R, MINB, per, sms);
+    if (s.grid > kLnMaxParts) s.grid = kLnMaxParts;
+    parts = static_cast<int>(s.grid);
+    size_t smem = per * s.groups;
+    const size_t sums = static_cast<size_t>(s.groups / 2) * 2 * NCH * kV<DT> * 32 * s.warps * sizeof(float);
+    if (smem < sums) smem = sums;
+    return launch_rows(ln_backward_rows_fused<DT, NCH, R, DEPTH, MINB, ALIGNED>, a, s, smem, st);
+}
+
+// A thread holds 16 columns of a row (one chunk of it where the row has no more
+// than a warp's worth), so that what a row costs each thread besides its
+// columns is spread; sixteen warps then hold kMaxCols columns.
+constexpr int kMaxCols = 8192;
+template <int DT>
+constexpr int kNch = 16 / kV<DT>;
+// columns up to which a group's five unaligned stages (eleven rows of words,
+// 176 bytes for each 8 or 4 columns) fit shared memory
+template <int DT>
+constexpr int kDeepCols = DT == ZERO_FP32 ? 4096 : 8192;
 
 template <int DT>
 cudaError_t forward_of(const LnArgs& a, cudaStream_t st)
 {
-    constexpr int V = DT == ZERO_FP32 ? 4 : 8;
+    constexpr int V = kV<DT>;
     const int sms = sms_of_device();
     if (sms == 0) return cudaErrorInvalidDevice;
-    bool done;
-    const bool vec = a.cols % V == 0 && a.x_stride % V == 0 && a.out_stride % V == 0 && wide(a.x) && wide(a.out) &&
-                     wide(a.gain) && wide(a.bias);
-    const cudaError_t e = vec ? forward_vec<DT, V>(a, sms, st, done) : forward_vec<DT, 1>(a, sms, st, done);
-    if (done) return e;
+    const bool al = a.cols % V == 0 && a.x_stride % V == 0 && a.out_stride % V == 0 && wide(a.x) && wide(a.out);
+    const int chunks = (a.cols + V - 1) / V;
+    constexpr int N = kNch<DT>;
+    if (chunks <= 32) return al ? forward_as<DT, 1, 2, 4, 2, true>(a, sms, st) : forward_as<DT, 1, 2, 3, 2, false>(a, sms, st);
+    if (a.cols <= kMaxCols) {
+        if (al) return forward_as<DT, N, 2, 3, 1, true>(a, sms, st);
+        return a.cols <= kDeepCols<DT> ? forward_as<DT, N, 1, 5, 1, false>(a, sms, st) : forward_as<DT, N, 1, 3, 1, false>(a, sms, st);
+    }
     const long long grid = a.rows < (1 << 30) ? a.rows : (1 << 30);
     return launch_after(ln_forward_any<DT>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, a);
-}
-
-template <int DT, int VEC, int NCH, int DEPTH>
-cudaError_t backward_fused(const LnArgs& a, int warps, int sms, cudaStream_t st, int& parts)
-{
-    // about 512 threads an SM in CTAs of up to 512 (256 where a row needs no
-    // more); small problems in as many CTAs as they have row groups
-    int groups = warps > 8 ? 1 : 8 / warps;
-    long long spread = (a.rows + sms - 1) / sms;
-    if (groups > spread) groups = static_cast<int>(spread);
-    const int threads = 32 * warps * groups;
-    long long grid = (a.rows + groups - 1) / groups;
-    const long long most = static_cast<long long>(sms) * (threads <= 256 ? 2 : 1);
-    if (grid > most) grid = most;
-    if (grid > kLnMaxParts) grid = kLnMaxParts;
-    parts = static_cast<int>(grid);
-    size_t smem = static_cast<size_t>(DEPTH) * 2 * NCH * 16 * threads;
-    const size_t sums = groups > 1 ? static_cast<size_t>(2) * NCH * VEC * 32 * warps * sizeof(float) : 0;
-    if (smem < sums) smem = sums;
-    const auto k = ln_backward_fused<DT, VEC, NCH, DEPTH>;
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    return launch_after(k, dim3(static_cast<unsigned>(grid)), dim3(threads), smem, st, a, warps, groups);
 }
 
 template <int DT>
 cudaError_t backward_of(const LnArgs& a, cudaStream_t st)
 {
-    constexpr int V = DT == ZERO_FP32 ? 4 : 8;
-    constexpr int N = DT == ZERO_FP32 ? 4 : 2;    // chunks a thread when a row takes several warps: 16 columns
+    constexpr int V = kV<DT>;
     const int sms = sms_of_device();
     if (sms == 0) return cudaErrorInvalidDevice;
     int parts = static_cast<int>(a.rows < kLnMaxParts ? a.rows : kLnMaxParts);
     if (a.rows > 0) {
-        const bool vec = a.cols % V == 0 && a.x_stride % V == 0 && a.dy_stride % V == 0 && a.out_stride % V == 0 &&
-                         wide(a.x) && wide(a.dy) && wide(a.out) && wide(a.gain);
-        const int chunks = a.cols / V;
-        cudaError_t e = cudaSuccess;
-        if (vec && chunks <= 32) {
-            e = backward_fused<DT, V, 1, 4>(a, 1, sms, st, parts);
-        } else if (vec && chunks <= 64) {
-            e = backward_fused<DT, V, 2, 4>(a, 1, sms, st, parts);
-        } else if (vec && chunks <= 96) {
-            e = backward_fused<DT, V, 3, 4>(a, 1, sms, st, parts);
-        } else if (vec && chunks <= 512 * N) {
-            e = backward_fused<DT, V, N, N == 4 ? 3 : 4>(a, (chunks + 32 * N - 1) / (32 * N), sms, st, parts);
-        } else if (!vec && a.cols <= 16 * 32 * 8) {
-            e = backward_fused<DT, 1, 8, 0>(a, (a.cols + 255) / 256, sms, st, parts);
-        } else if (!vec && a.cols <= 16 * 32 * 16) {
-            e = backward_fused<DT, 1, 16, 0>(a, (a.cols + 511) / 512, sms, st, parts);
+        const bool al = a.cols % V == 0 && a.x_stride % V == 0 && a.dy_stride % V == 0 && a.out_stride % V == 0 &&
+                        wide(a.x) && wide(a.dy) && wide(a.out);
+        const int chunks = (a.cols + V - 1) / V;
+        constexpr int N = kNch<DT>;
+        cudaError_t e;
+        if (chunks <= 32) {
+            e = al ? backward_as<DT, 1, 2, 3, 1, true>(a, sms, st, parts) : backward_as<DT, 1, 2, 3, 1, false>(a, sms, st, parts);
+        } else if (a.cols <= kMaxCols) {
+            if (al)
+                e = backward_as<DT, N, 1, 3, 1, true>(a, sms, st, parts);
+            else if (a.cols <= kDeepCols<DT>)
+                e = backward_as<DT, N, 1, 5, 1, false>(a, sms, st, parts);
+            else
+                e = backward_as<DT, N, 1, 2, 1, false>(a, sms, st, parts);
         } else {
             const long long grid = a.rows < (1 << 30) ? a.rows : (1 << 30);
             e = launch_after(ln_backward_rows<DT>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, a);
