@@ -21,6 +21,7 @@
 // lo*hi + hi*lo + hi*hi: 3e-7 to 4e-6 off, for results kept in more than bf16.
 #include <cuda_fp16.h>
 
+#include <climits>
 #include <cstring>
 
 #include "zk_common.cuh"
@@ -39,6 +40,7 @@ constexpr int kBox = 64;       // TMA boxes are 64 x 64 values, 8 KB, whichever 
 constexpr int kBoxBytes = kBox * kBK * 2;
 constexpr int kMmThreads = 320;   // producer, MMA, eight epilogue warps
 constexpr int kMaxNsParts = 1024;
+constexpr int kStrip = 16;
 
 // how an operand lies in memory: its depth contiguous (K-major), its rows
 // contiguous (MN-major), or a symmetric matrix of which only the blocks of
@@ -53,7 +55,7 @@ struct MmArgs {
     int sb;
     int products;
     int lower;                    // only blocks on and under the diagonal
-    int tiles_n, tiles_per_matrix, tiles;
+    int tiles_m, tiles_n, tiles_per_matrix, tiles;
     // result: alpha * sum + beta * addend
     float alpha, beta;
     const __half* add_hi;
@@ -84,8 +86,13 @@ __device__ __forceinline__ Tile tile_of(const MmArgs& a, int t)
     r.b = t / a.tiles_per_matrix;
     t -= r.b * a.tiles_per_matrix;
     if (!a.lower) {
-        r.m0 = t / a.tiles_n * kBM;
-        r.n0 = t % a.tiles_n * BN;
+        // strips of kStrip row tiles, column by column: the tiles in flight at a
+        // time form a near-square block, whose operands stay in L2
+        const int strip = t / (kStrip * a.tiles_n), first = strip * kStrip;
+        const int rows = a.tiles_m - first < kStrip ? a.tiles_m - first : kStrip;
+        t -= first * a.tiles_n;
+        r.m0 = (first + t % rows) * kBM;
+        r.n0 = t / rows * BN;
         return r;
     }
     constexpr int SB = BN > kBM ? BN : kBM;
@@ -100,18 +107,30 @@ __device__ __forceinline__ Tile tile_of(const MmArgs& a, int t)
     return r;
 }
 
-__device__ __forceinline__ bool mn_major(int mode, int sb, int mn0, int k0)
+// the depth from which an operand's tile at mn0 is read MN-major
+__device__ __forceinline__ int mn_from(int mode, int sb, int mn0)
 {
-    return mode == kMajorMN || (mode == kSymLower && k0 / sb > mn0 / sb);
+    return mode == kMajorK ? INT_MAX : mode == kMajorMN ? 0 : (mn0 & -sb) + sb;
 }
 
-__device__ __forceinline__ void load_operand(unsigned char* dst, const CUtensorMap* map, int mode, int sb, int mn0,
-                                             int k0, int b, int boxes, uint64_t* bar)
+template <int BOXES>
+__device__ __forceinline__ void load_operand(unsigned char* dst, const CUtensorMap* map, bool mn, int mn0, int k0, int b,
+                                             uint64_t* bar)
 {
-    const bool mn = mn_major(mode, sb, mn0, k0);
-    for (int h = 0; h < boxes; ++h)
+#pragma unroll
+    for (int h = 0; h < BOXES; ++h)
         tma_load_3d(dst + h * kBoxBytes, map, mn ? mn0 + h * kBox : k0, mn ? k0 : mn0 + h * kBox, b, bar);
 }
+
+// a place in the ring of stages: the slot, and the parity of its current use
+template <int N>
+struct Slot {
+    uint32_t i = 0, parity = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++i == N) i = 0, parity ^= 1;
+    }
+};
 
 // ------------------------------------------------------------- epilogues
 __device__ __forceinline__ float2 half2_up(uint32_t w)
@@ -120,21 +139,35 @@ __device__ __forceinline__ float2 half2_up(uint32_t w)
     return __half22float2(h);
 }
 
-// acc[0..7] = beta * (hi + lo) + acc, from 16-byte aligned planes
-__device__ __forceinline__ void add_planes8(float* v, float beta, const __half* hi, const __half* lo)
-{
-    const uint4 h = *reinterpret_cast<const uint4*>(hi);
-    const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
-    uint4 l = make_uint4(0, 0, 0, 0);
-    if (lo != nullptr) l = *reinterpret_cast<const uint4*>(lo);
-    const uint32_t lw[4] = {l.x, l.y, l.z, l.w};
+// 32 consecutive values of a row of a pair of planes (lo may be null: zeros),
+// all loads issued together, from L2 (another SM wrote them)
+struct Addend {
+    uint4 h[4], l[4];
+    __device__ __forceinline__ void load(const __half* hi, const __half* lo, int n)
+    {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 p = half2_up(hw[i]), q = half2_up(lw[i]);
-        v[2 * i] = fmaf(beta, p.x + q.x, v[2 * i]);
-        v[2 * i + 1] = fmaf(beta, p.y + q.y, v[2 * i + 1]);
+        for (int c = 0; c < 4; ++c) {
+            h[c] = l[c] = make_uint4(0, 0, 0, 0);
+            if (8 * c < n) h[c] = __ldcg(reinterpret_cast<const uint4*>(hi) + c);
+            if (8 * c < n && lo != nullptr) l[c] = __ldcg(reinterpret_cast<const uint4*>(lo) + c);
+        }
     }
-}
+    // v = alpha * v + beta * (hi + lo)
+    __device__ __forceinline__ void into(float (&v)[32], float alpha, float beta) const
+    {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const uint32_t hw[4] = {h[c].x, h[c].y, h[c].z, h[c].w}, lw[4] = {l[c].x, l[c].y, l[c].z, l[c].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 p = half2_up(hw[i]), q = half2_up(lw[i]);
+                float* o = v + 8 * c + 2 * i;
+                o[0] = fmaf(beta, p.x + q.x, alpha * o[0]);
+                o[1] = fmaf(beta, p.y + q.y, alpha * o[1]);
+            }
+        }
+    }
+};
 
 __device__ __forceinline__ void put_planes8(const float* v, __half* hi, __half* lo)
 {
@@ -186,43 +219,56 @@ __device__ __forceinline__ void put_row8(void* base, int dt, long long i, const 
     }
 }
 
-// 32 consecutive sums of one output row, from column `col`
+// 32 consecutive sums of one output row, from column `col`; what the result
+// needs besides them is loaded before the sums arrive
 template <int EPI>
-__device__ __forceinline__ void epilogue(const MmArgs& a, int b, int row, int col, float (&v)[32])
+__device__ __forceinline__ void epilogue(const MmArgs& a, int b, int row, int col, uint32_t tmem)
 {
     const int n = a.n - col;
+    const bool in = row < a.m;
+    Addend x;
+    if (EPI != EPI_PLANES && in) {
+        const long long at = b * a.add_stride + row * a.add_ld + col;
+        x.load(a.add_hi + at, a.add_lo != nullptr ? a.add_lo + at : nullptr, n);
+    }
+    float v[32];
+    tmem_load32(tmem, v);
+    if (!in) return;
+    if (EPI == EPI_PLANES) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] *= a.alpha;
-    const long long at = b * a.add_stride + row * a.add_ld + col;
+        for (int i = 0; i < 32; ++i) v[i] *= a.alpha;
+    } else {
+        x.into(v, a.alpha, a.beta);
+    }
+    const long long o = b * a.out_stride + row * a.out_ld + col;
+    if (EPI == EPI_PLANES || EPI == EPI_ADD) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        if (8 * c >= n) break;
-        if (EPI != EPI_PLANES)
-            add_planes8(v + 8 * c, a.beta, a.add_hi + at + 8 * c, a.add_lo != nullptr ? a.add_lo + at + 8 * c : nullptr);
-        if (EPI == EPI_PLANES || EPI == EPI_ADD) {
-            const long long o = b * a.out_stride + row * a.out_ld + col + 8 * c;
-            put_planes8(v + 8 * c, a.out_hi + o, a.out_lo != nullptr ? a.out_lo + o : nullptr);
-        } else if (EPI == EPI_OUT) {
-            put_row8(a.out, a.out_dtype, b * a.out_stride + row * a.out_ld + col + 8 * c, v + 8 * c, n - 8 * c, a.out_vec);
-        } else {
-            // w <- w * (1 - lr wd) - step * o, rounded to the master's fp32, then its 16-bit cast
-            const long long o = b * a.out_stride + row * a.out_ld + col + 8 * c;
-            float* w = a.master + o;
-            float r[8];
+        for (int c = 0; c < 4; ++c)
+            if (8 * c < n) put_planes8(v + 8 * c, a.out_hi + o + 8 * c, a.out_lo != nullptr ? a.out_lo + o + 8 * c : nullptr);
+    } else if (EPI == EPI_OUT) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) r[e] = 0.0f;
-            if (a.out_vec && n - 8 * c >= 8) {
-                const float4 p = *reinterpret_cast<const float4*>(w), q = *reinterpret_cast<const float4*>(w + 4);
-                r[0] = p.x, r[1] = p.y, r[2] = p.z, r[3] = p.w, r[4] = q.x, r[5] = q.y, r[6] = q.z, r[7] = q.w;
-            } else {
+        for (int c = 0; c < 4; ++c)
+            if (8 * c < n) put_row8(a.out, a.out_dtype, o + 8 * c, v + 8 * c, n - 8 * c, a.out_vec);
+    } else {
+        // w <- w * (1 - lr wd) - step * o, rounded to the master's fp32, then its 16-bit cast
+        float w[32];
+        if (a.out_vec && n >= 32) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (8 * c + e < n) r[e] = w[e];
+            for (int c = 0; c < 8; ++c) {
+                const float4 p = *reinterpret_cast<const float4*>(a.master + o + 4 * c);
+                w[4 * c] = p.x, w[4 * c + 1] = p.y, w[4 * c + 2] = p.z, w[4 * c + 3] = p.w;
             }
+        } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) r[e] = fmaf(-a.step, v[8 * c + e], r[e] * a.decay);
-            put_row8(a.master, ZERO_FP32, o, r, n - 8 * c, a.out_vec);
-            if (a.lp != nullptr) put_row8(a.lp, a.out_dtype, o, r, n - 8 * c, a.out_vec);
+            for (int e = 0; e < 32; ++e) w[e] = e < n ? a.master[o + e] : 0.0f;
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = fmaf(-a.step, v[e], w[e] * a.decay);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            if (8 * c >= n) break;
+            put_row8(a.master, ZERO_FP32, o + 8 * c, v + 8 * c, n - 8 * c, a.out_vec);
+            if (a.lp != nullptr) put_row8(a.lp, a.out_dtype, o + 8 * c, v + 8 * c, n - 8 * c, a.out_vec);
         }
     }
 }
@@ -271,75 +317,82 @@ __global__ void __launch_bounds__(kMmThreads, 1) mm_kernel(const __grid_constant
     pdl_wait();
     pdl_launch();
 
-    const int depth = (a.k + kBK - 1) / kBK;
-    const int iters = depth * a.products;
-
     if (warp == 0) {
       if (lane == 0) {
         fence_proxy_async_global();   // the previous kernel's plain stores, before our TMA loads
-        uint32_t it = 0;
+        Slot<S::kStages> s;
+        uint32_t issued = 0;
         bool ok = true;
         for (int t = blockIdx.x; ok && t < a.tiles; t += gridDim.x) {
             const Tile tl = tile_of<BN>(a, t);
-            for (int i = 0; i < iters; ++i, ++it) {
-                const int s = it % S::kStages;
-                if (it >= S::kStages &&
-                    !mbar_wait_bounded(&empty[s], ((it / S::kStages) & 1) ^ 1, &abort_flag, a.timeout_ns)) {
-                    abort_flag = 1;
-                    ok = false;
-                    break;
+            const int am = mn_from(a.a_mode, a.sb, tl.m0), bm = mn_from(a.b_mode, a.sb, tl.n0);
+            // small products first: lo*hi, hi*lo, then hi*hi
+            for (int pass = 3 - a.products; ok && pass < 3; ++pass) {
+                const CUtensorMap* ma = &a.a[pass == 0];
+                const CUtensorMap* mb = &a.b[pass == 1];
+                for (int k0 = 0; k0 < a.k; k0 += kBK) {
+                    if (issued >= S::kStages && !mbar_wait_bounded(&empty[s.i], s.parity ^ 1, &abort_flag, a.timeout_ns)) {
+                        abort_flag = 1;
+                        ok = false;
+                        break;
+                    }
+                    if (!a.starve) {
+                        unsigned char* p = ring + s.i * S::kStageBytes;
+                        mbar_arrive_expect_tx(&full[s.i], S::kStageBytes);
+                        load_operand<kBM / kBox>(p, ma, k0 >= am, tl.m0, k0, tl.b, &full[s.i]);
+                        load_operand<BN / kBox>(p + kBM * kBK * 2, mb, k0 >= bm, tl.n0, k0, tl.b, &full[s.i]);
+                    }
+                    s.next();
+                    ++issued;
                 }
-                if (a.starve) continue;
-                // small products first: lo*hi, hi*lo, then hi*hi
-                const int pass = a.products == 3 ? i / depth : 2;
-                const int k0 = (a.products == 3 ? i % depth : i) * kBK;
-                unsigned char* p = ring + s * S::kStageBytes;
-                mbar_arrive_expect_tx(&full[s], S::kStageBytes);
-                load_operand(p, &a.a[pass == 0], a.a_mode, a.sb, tl.m0, k0, tl.b, kBM / kBox, &full[s]);
-                load_operand(p + kBM * kBK * 2, &a.b[pass == 1], a.b_mode, a.sb, tl.n0, k0, tl.b, BN / kBox, &full[s]);
             }
         }
         if (!ok && !a.starve) {
             // nothing of ours may still be landing when the CTA's memory goes away
-            const uint32_t first = it > S::kStages ? it - S::kStages : 0;
-            for (uint32_t i = first; i < it; ++i)
+            for (uint32_t i = issued > S::kStages ? issued - S::kStages : 0; i < issued; ++i)
                 mbar_wait_bounded(&full[i % S::kStages], (i / S::kStages) & 1, nullptr, 1000000000ull);
         }
       }
       __syncwarp();
     } else if (warp == 1) {
       if (lane == 0) {
-        uint32_t it = 0, n_tile = 0;
+        Slot<S::kStages> s;
+        Slot<2> acc;
+        uint32_t n_tile = 0;
         bool ok = true;
         for (int t = blockIdx.x; ok && t < a.tiles; t += gridDim.x, ++n_tile) {
             const Tile tl = tile_of<BN>(a, t);
-            const int acc = n_tile & 1;
-            if (n_tile >= 2 && !mbar_wait_bounded(&acc_empty[acc], ((n_tile >> 1) & 1) ^ 1, &abort_flag, a.timeout_ns)) {
+            const int am = mn_from(a.a_mode, a.sb, tl.m0), bm = mn_from(a.b_mode, a.sb, tl.n0);
+            if (n_tile >= 2 && !mbar_wait_bounded(&acc_empty[acc.i], acc.parity ^ 1, &abort_flag, a.timeout_ns)) {
                 abort_flag = 1;
                 break;
             }
             tc_fence_after();
-            for (int i = 0; i < iters; ++i, ++it) {
-                const int s = it % S::kStages;
-                if (!mbar_wait_bounded(&full[s], (it / S::kStages) & 1, &abort_flag, a.timeout_ns)) {
-                    abort_flag = 1;
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const int k0 = i % depth * kBK;
-                const bool a_mn = mn_major(a.a_mode, a.sb, tl.m0, k0), b_mn = mn_major(a.b_mode, a.sb, tl.n0, k0);
-                const uint32_t idesc = instr_desc(kBM, BN, a_mn, b_mn);
-                const uint32_t p = smem_u32(ring + s * S::kStageBytes);
-                const uint64_t da = smem_desc(p), db = smem_desc(p + kBM * kBK * 2);
-                // sixteen values of depth: 32 bytes along a line, or sixteen lines
-                const uint32_t sa = a_mn ? 2048 >> 4 : 32 >> 4, sbb = b_mn ? 2048 >> 4 : 32 >> 4;
+            bool more = false;   // false: the accumulator starts anew
+            for (int pass = 3 - a.products; ok && pass < 3; ++pass) {
+                for (int k0 = 0; k0 < a.k; k0 += kBK) {
+                    if (!mbar_wait_bounded(&full[s.i], s.parity, &abort_flag, a.timeout_ns)) {
+                        abort_flag = 1;
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const bool a_mn = k0 >= am, b_mn = k0 >= bm;
+                    const uint32_t idesc = instr_desc(kBM, BN, a_mn, b_mn);
+                    const uint32_t p = smem_u32(ring + s.i * S::kStageBytes);
+                    const uint64_t da = smem_desc(p), db = smem_desc(p + kBM * kBK * 2);
+                    // sixteen values of depth: 32 bytes along a line, or sixteen lines
+                    const uint32_t sa = a_mn ? 2048 >> 4 : 32 >> 4, sbb = b_mn ? 2048 >> 4 : 32 >> 4;
 #pragma unroll
-                for (int k = 0; k < kBK / 16; ++k)
-                    mma_f16(tmem + acc * BN, da + k * sa, db + k * sbb, idesc, i > 0 || k > 0);
-                mma_commit(&empty[s]);
+                    for (int k = 0; k < kBK / 16; ++k)
+                        mma_f16(tmem + acc.i * BN, da + k * sa, db + k * sbb, idesc, more || k > 0);
+                    more = true;
+                    mma_commit(&empty[s.i]);
+                    s.next();
+                }
             }
-            if (ok) mma_commit(&acc_full[acc]);
+            if (ok) mma_commit(&acc_full[acc.i]);
+            acc.next();
         }
         mma_commit(&drain);   // TMEM is given back only after the last MMA
         mbar_wait_bounded(&drain, 0, nullptr, 1000000000ull);
@@ -361,9 +414,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) mm_kernel(const __grid_constant
 #pragma unroll 1
             for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 32) {
                 if (tl.n0 + c >= a.n) break;
-                float v[32];
-                tmem_load32(tmem + acc * BN + c + (static_cast<uint32_t>(quarter * 32) << 16), v);
-                if (row < a.m) epilogue<EPI>(a, tl.b, row, tl.n0 + c, v);
+                epilogue<EPI>(a, tl.b, row, tl.n0 + c, tmem + acc * BN + c + (static_cast<uint32_t>(quarter * 32) << 16));
             }
             tc_fence_before();
             __syncwarp();
@@ -667,11 +718,12 @@ cudaError_t launch_mm(int bn, MmArgs& a, int batch, int sms, cudaStream_t st)
     const int sb = bn > kBM ? bn : kBM;
     a.sb = sb;
     a.tiles_n = (a.n + bn - 1) / bn;
+    a.tiles_m = (a.m + kBM - 1) / kBM;
     if (a.lower) {
         const int blocks = (a.m + sb - 1) / sb;
         a.tiles_per_matrix = (sb / kBM) * (sb / bn) * (blocks * (blocks + 1) / 2);
     } else {
-        a.tiles_per_matrix = a.tiles_n * ((a.m + kBM - 1) / kBM);
+        a.tiles_per_matrix = a.tiles_n * a.tiles_m;
     }
     a.tiles = a.tiles_per_matrix * batch;
     if (bn == 256) return launch_mm_as<256, EPI>(a, sms, st);
