@@ -38,56 +38,89 @@ constexpr int kBM = 128;       // output rows of a CTA's tile (TMEM lanes)
 constexpr int kBK = 64;        // depth of a pipeline stage: 128 bytes, one swizzle line
 constexpr int kBox = 64;       // TMA boxes are 64 x 64 values, 8 KB, whichever side is the depth
 constexpr int kBoxBytes = kBox * kBK * 2;
-constexpr int kMmThreads = 320;   // producer, MMA, eight epilogue warps
+constexpr int kThreads = 320;  // producer warp, MMA warp, eight epilogue warps
+constexpr int kEpiWarps = 8;
 constexpr int kMaxNsParts = 1024;
-constexpr int kStrip = 16;
+constexpr int kStrip = 16;     // row tiles of a strip (see tile_of)
+constexpr int kBarStride = 32; // words between the groups' barrier counters: a line each
+constexpr unsigned kPoison = 0x80000000u;
 
 // how an operand lies in memory: its depth contiguous (K-major), its rows
 // contiguous (MN-major), or a symmetric matrix of which only the blocks of
 // `sb` x `sb` on and under the diagonal are stored
 enum { kMajorK = 0, kMajorMN = 1, kSymLower = 2 };
-enum { EPI_PLANES = 0, EPI_ADD = 1, EPI_OUT = 2, EPI_MUON = 3 };
+// what becomes of the sums: a pair of fp16 planes, the result, or the weights
+enum { EPI_PLANES = 0, EPI_OUT = 1, EPI_MUON = 2 };
 
-struct MmArgs {
-    CUtensorMap a[2], b[2];       // hi and lo planes
-    int a_mode, b_mode;
-    int m, n, k;
-    int sb;
-    int products;
-    int lower;                    // only blocks on and under the diagonal
-    int tiles_m, tiles_n, tiles_per_matrix, tiles;
-    // result: alpha * sum + beta * addend
-    float alpha, beta;
-    const __half* add_hi;
-    const __half* add_lo;         // may be null
-    __half* out_hi;
-    __half* out_lo;               // may be null
-    long long add_ld, add_stride, out_ld, out_stride;   // elements
-    void* out;                    // EPI_OUT
+struct DevPlanes {
+    __half* hi;
+    __half* lo;                  // may be null
+    long long ld, stride;        // elements
+};
+
+struct NsKernelArgs {
+    CUtensorMap xmap[2][2], gmap[2], pmap[2];   // hi and lo planes
+    DevPlanes x[2], g, p;
+    int rows, cols, m, wide, batch;
+    int steps, products;
+    int groups, ctas;            // CTAs of a group; a group takes every groups-th matrix
+    int split[3];                // CTAs that share a tile's depth: for G, P and x
+    float coef[kNsMaxSteps][3];
+    // x_0
+    const void* in;
+    int in_dtype, in_vec, chunks;
+    long long in_ld, in_stride;
+    float eps;
+    const double* parts;         // [batch][parts_n] sums of squares
+    int parts_n;
+    // the result
+    int epi;
+    void* out;
     int out_dtype, out_vec;
-    float* master;                // EPI_MUON
+    long long out_ld, out_stride;
+    float* master;
     void* lp;
     float decay, step;
+    // exchange between CTAs
+    unsigned* group_bar;         // [groups] counters, kBarStride words apart
+    unsigned* tile_bar;          // [groups][ctas]
+    float* partial;              // [groups * ctas][128 * BN]
     zero_dev_scalars* sc;
-    int starve;                   // issue no copy, so that every wait runs out
+    int starve;                  // issue no copy, so that every wait runs out
     unsigned long long timeout_ns;
 };
 
-struct Tile {
-    int b, m0, n0;
+// One product: alpha * A B^T + beta * addend over an m x n result.
+struct Phase {
+    const CUtensorMap* a;        // hi; lo follows
+    const CUtensorMap* b;
+    int a_mode, b_mode;
+    int m, n, k;
+    int lower;                   // only blocks on and under the diagonal
+    int tiles_m, tiles_n, tiles, split;
+    int stop;                    // a wait has run out somewhere
+    unsigned tile_target;        // tile_bar's count once all parts of a tile of this phase are there
+    int epi;
+    float alpha, beta;
+    const __half* add_hi;        // this matrix's; null: no addend
+    const __half* add_lo;
+    long long add_ld;
+    DevPlanes out;               // EPI_PLANES: this matrix's
 };
 
-// Tile t of the launch.  Lower-triangle launches number the tiles of block row
-// I (sb rows, (I + 1) * sb columns) after those of the rows above.
+struct Tile {
+    int m0, n0;
+};
+
+// Tile t of a phase.  Lower-triangle phases number the tiles of block row I
+// (sb rows, (I + 1) * sb columns) after those of the rows above.  Others go in
+// strips of kStrip row tiles, column by column: the tiles in flight at a time
+// form a near-square block, whose operands stay in L2.
 template <int BN>
-__device__ __forceinline__ Tile tile_of(const MmArgs& a, int t)
+__device__ __forceinline__ Tile tile_of(const Phase& a, int t)
 {
     Tile r;
-    r.b = t / a.tiles_per_matrix;
-    t -= r.b * a.tiles_per_matrix;
     if (!a.lower) {
-        // strips of kStrip row tiles, column by column: the tiles in flight at a
-        // time form a near-square block, whose operands stay in L2
         const int strip = t / (kStrip * a.tiles_n), first = strip * kStrip;
         const int rows = a.tiles_m - first < kStrip ? a.tiles_m - first : kStrip;
         t -= first * a.tiles_n;
@@ -139,32 +172,24 @@ __device__ __forceinline__ float2 half2_up(uint32_t w)
     return __half22float2(h);
 }
 
-// 32 consecutive values of a row of a pair of planes (lo may be null: zeros),
-// all loads issued together, from L2 (another SM wrote them)
+// eight consecutive values of a pair of planes (lo may be null: zeros), from
+// L2: another SM may have written them a moment ago
 struct Addend {
-    uint4 h[4], l[4];
-    __device__ __forceinline__ void load(const __half* hi, const __half* lo, int n)
+    uint4 h, l;
+    __device__ __forceinline__ void load(const __half* hi, const __half* lo)
     {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            h[c] = l[c] = make_uint4(0, 0, 0, 0);
-            if (8 * c < n) h[c] = __ldcg(reinterpret_cast<const uint4*>(hi) + c);
-            if (8 * c < n && lo != nullptr) l[c] = __ldcg(reinterpret_cast<const uint4*>(lo) + c);
-        }
+        h = __ldcg(reinterpret_cast<const uint4*>(hi));
+        l = lo != nullptr ? __ldcg(reinterpret_cast<const uint4*>(lo)) : make_uint4(0, 0, 0, 0);
     }
     // v = alpha * v + beta * (hi + lo)
-    __device__ __forceinline__ void into(float (&v)[32], float alpha, float beta) const
+    __device__ __forceinline__ void into(float* v, float alpha, float beta) const
     {
+        const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const uint32_t hw[4] = {h[c].x, h[c].y, h[c].z, h[c].w}, lw[4] = {l[c].x, l[c].y, l[c].z, l[c].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 p = half2_up(hw[i]), q = half2_up(lw[i]);
-                float* o = v + 8 * c + 2 * i;
-                o[0] = fmaf(beta, p.x + q.x, alpha * o[0]);
-                o[1] = fmaf(beta, p.y + q.y, alpha * o[1]);
-            }
+        for (int i = 0; i < 4; ++i) {
+            const float2 p = half2_up(hw[i]), q = half2_up(lw[i]);
+            v[2 * i] = fmaf(beta, p.x + q.x, alpha * v[2 * i]);
+            v[2 * i + 1] = fmaf(beta, p.y + q.y, alpha * v[2 * i + 1]);
         }
     }
 };
@@ -219,213 +244,83 @@ __device__ __forceinline__ void put_row8(void* base, int dt, long long i, const 
     }
 }
 
-// 32 consecutive sums of one output row, from column `col`; what the result
-// needs besides them is loaded before the sums arrive
-template <int EPI>
-__device__ __forceinline__ void epilogue(const MmArgs& a, int b, int row, int col, uint32_t tmem)
+// the addend of U groups of eight columns from column `col` of a row
+template <int U>
+__device__ __forceinline__ void load_addends(const Phase& ph, int row, int col, Addend (&x)[U])
 {
-    const int n = a.n - col;
-    const bool in = row < a.m;
-    Addend x;
-    if (EPI != EPI_PLANES && in) {
-        const long long at = b * a.add_stride + row * a.add_ld + col;
-        x.load(a.add_hi + at, a.add_lo != nullptr ? a.add_lo + at : nullptr, n);
-    }
-    float v[32];
-    tmem_load32(tmem, v);
-    if (!in) return;
-    if (EPI == EPI_PLANES) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] *= a.alpha;
-    } else {
-        x.into(v, a.alpha, a.beta);
-    }
-    const long long o = b * a.out_stride + row * a.out_ld + col;
-    if (EPI == EPI_PLANES || EPI == EPI_ADD) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-            if (8 * c < n) put_planes8(v + 8 * c, a.out_hi + o + 8 * c, a.out_lo != nullptr ? a.out_lo + o + 8 * c : nullptr);
-    } else if (EPI == EPI_OUT) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-            if (8 * c < n) put_row8(a.out, a.out_dtype, o + 8 * c, v + 8 * c, n - 8 * c, a.out_vec);
-    } else {
-        // w <- w * (1 - lr wd) - step * o, rounded to the master's fp32, then its 16-bit cast
-        float w[32];
-        if (a.out_vec && n >= 32) {
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const float4 p = *reinterpret_cast<const float4*>(a.master + o + 4 * c);
-                w[4 * c] = p.x, w[4 * c + 1] = p.y, w[4 * c + 2] = p.z, w[4 * c + 3] = p.w;
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) w[e] = e < n ? a.master[o + e] : 0.0f;
-        }
-#pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = fmaf(-a.step, v[e], w[e] * a.decay);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            if (8 * c >= n) break;
-            put_row8(a.master, ZERO_FP32, o + 8 * c, v + 8 * c, n - 8 * c, a.out_vec);
-            if (a.lp != nullptr) put_row8(a.lp, a.out_dtype, o + 8 * c, v + 8 * c, n - 8 * c, a.out_vec);
-        }
+    for (int c = 0; c < U; ++c) {
+        x[c].h = x[c].l = make_uint4(0, 0, 0, 0);
+        if (ph.add_hi == nullptr || row >= ph.m || col + 8 * c >= ph.n) continue;
+        const long long at = row * ph.add_ld + col + 8 * c;
+        x[c].load(ph.add_hi + at, ph.add_lo != nullptr ? ph.add_lo + at : nullptr);
     }
 }
 
-template <int BN>
-struct MmShape {
-    static constexpr int kStageBytes = (kBM + BN) * kBK * 2;
-    static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 6 : 8;
-    static constexpr int kSmem = kStages * kStageBytes + 1024;   // + alignment of the ring
-};
-
-// One persistent CTA per SM walks the tiles: a producer thread keeps a ring of
-// 64-deep operand tiles full by TMA, one thread issues the MMAs into one of
-// two TMEM accumulators, and eight warps turn the other one into results.
-template <int BN, int EPI>
-__global__ void __launch_bounds__(kMmThreads, 1) mm_kernel(const __grid_constant__ MmArgs a)
+// U groups of eight sums of one row, from column `col`, to where they belong
+template <int U>
+__device__ __forceinline__ void finish(const NsKernelArgs& a, const Phase& ph, int b, int row, int col,
+                                       const Addend (&x)[U], float (&v)[8 * U])
 {
-    using S = MmShape<BN>;
-    extern __shared__ unsigned char smem_raw[];
-    __shared__ uint64_t full[S::kStages], empty[S::kStages], acc_full[2], acc_empty[2], drain;
-    __shared__ uint32_t tmem_base;
-    __shared__ volatile int abort_flag;
-    unsigned char* ring = smem_raw + (1024 - (smem_u32(smem_raw) & 1023u)) % 1024;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < S::kStages; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], 8);
-        }
-        mbar_init(&drain, 1);
-        abort_flag = 0;
-        fence_barrier_init();
-        prefetch_tmap(&a.a[0]);
-        prefetch_tmap(&a.b[0]);
-    }
-    if (warp == 1) tmem_alloc(&tmem_base, 2 * BN);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = tmem_base;
-    pdl_wait();
-    pdl_launch();
-
-    if (warp == 0) {
-      if (lane == 0) {
-        fence_proxy_async_global();   // the previous kernel's plain stores, before our TMA loads
-        Slot<S::kStages> s;
-        uint32_t issued = 0;
-        bool ok = true;
-        for (int t = blockIdx.x; ok && t < a.tiles; t += gridDim.x) {
-            const Tile tl = tile_of<BN>(a, t);
-            const int am = mn_from(a.a_mode, a.sb, tl.m0), bm = mn_from(a.b_mode, a.sb, tl.n0);
-            // small products first: lo*hi, hi*lo, then hi*hi
-            for (int pass = 3 - a.products; ok && pass < 3; ++pass) {
-                const CUtensorMap* ma = &a.a[pass == 0];
-                const CUtensorMap* mb = &a.b[pass == 1];
-                for (int k0 = 0; k0 < a.k; k0 += kBK) {
-                    if (issued >= S::kStages && !mbar_wait_bounded(&empty[s.i], s.parity ^ 1, &abort_flag, a.timeout_ns)) {
-                        abort_flag = 1;
-                        ok = false;
-                        break;
-                    }
-                    if (!a.starve) {
-                        unsigned char* p = ring + s.i * S::kStageBytes;
-                        mbar_arrive_expect_tx(&full[s.i], S::kStageBytes);
-                        load_operand<kBM / kBox>(p, ma, k0 >= am, tl.m0, k0, tl.b, &full[s.i]);
-                        load_operand<BN / kBox>(p + kBM * kBK * 2, mb, k0 >= bm, tl.n0, k0, tl.b, &full[s.i]);
-                    }
-                    s.next();
-                    ++issued;
-                }
-            }
-        }
-        if (!ok && !a.starve) {
-            // nothing of ours may still be landing when the CTA's memory goes away
-            for (uint32_t i = issued > S::kStages ? issued - S::kStages : 0; i < issued; ++i)
-                mbar_wait_bounded(&full[i % S::kStages], (i / S::kStages) & 1, nullptr, 1000000000ull);
-        }
-      }
-      __syncwarp();
-    } else if (warp == 1) {
-      if (lane == 0) {
-        Slot<S::kStages> s;
-        Slot<2> acc;
-        uint32_t n_tile = 0;
-        bool ok = true;
-        for (int t = blockIdx.x; ok && t < a.tiles; t += gridDim.x, ++n_tile) {
-            const Tile tl = tile_of<BN>(a, t);
-            const int am = mn_from(a.a_mode, a.sb, tl.m0), bm = mn_from(a.b_mode, a.sb, tl.n0);
-            if (n_tile >= 2 && !mbar_wait_bounded(&acc_empty[acc.i], acc.parity ^ 1, &abort_flag, a.timeout_ns)) {
-                abort_flag = 1;
-                break;
-            }
-            tc_fence_after();
-            bool more = false;   // false: the accumulator starts anew
-            for (int pass = 3 - a.products; ok && pass < 3; ++pass) {
-                for (int k0 = 0; k0 < a.k; k0 += kBK) {
-                    if (!mbar_wait_bounded(&full[s.i], s.parity, &abort_flag, a.timeout_ns)) {
-                        abort_flag = 1;
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const bool a_mn = k0 >= am, b_mn = k0 >= bm;
-                    const uint32_t idesc = instr_desc(kBM, BN, a_mn, b_mn);
-                    const uint32_t p = smem_u32(ring + s.i * S::kStageBytes);
-                    const uint64_t da = smem_desc(p), db = smem_desc(p + kBM * kBK * 2);
-                    // sixteen values of depth: 32 bytes along a line, or sixteen lines
-                    const uint32_t sa = a_mn ? 2048 >> 4 : 32 >> 4, sbb = b_mn ? 2048 >> 4 : 32 >> 4;
+    const int n = ph.n - col;
+    if (row >= ph.m || n <= 0) return;
 #pragma unroll
-                    for (int k = 0; k < kBK / 16; ++k)
-                        mma_f16(tmem + acc.i * BN, da + k * sa, db + k * sbb, idesc, more || k > 0);
-                    more = true;
-                    mma_commit(&empty[s.i]);
-                    s.next();
-                }
-            }
-            if (ok) mma_commit(&acc_full[acc.i]);
-            acc.next();
-        }
-        mma_commit(&drain);   // TMEM is given back only after the last MMA
-        mbar_wait_bounded(&drain, 0, nullptr, 1000000000ull);
-      }
-      __syncwarp();
-    } else {
-        const int quarter = warp & 3;         // the TMEM lanes this warp may read
-        const int half = (warp - 2) >> 2;     // its half of the columns
-        uint32_t n_tile = 0;
-        for (int t = blockIdx.x; t < a.tiles; t += gridDim.x, ++n_tile) {
-            const Tile tl = tile_of<BN>(a, t);
-            const int acc = n_tile & 1;
-            if (!mbar_wait_bounded(&acc_full[acc], (n_tile >> 1) & 1, &abort_flag, a.timeout_ns)) {
-                abort_flag = 1;
-                break;
-            }
-            tc_fence_after();
-            const int row = tl.m0 + quarter * 32 + lane;
-#pragma unroll 1
-            for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 32) {
-                if (tl.n0 + c >= a.n) break;
-                epilogue<EPI>(a, tl.b, row, tl.n0 + c, tmem + acc * BN + c + (static_cast<uint32_t>(quarter * 32) << 16));
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[acc]);
-        }
+    for (int c = 0; c < U; ++c) x[c].into(v + 8 * c, ph.alpha, ph.beta);
+    if (ph.epi == EPI_PLANES) {
+        const long long o = row * ph.out.ld + col;
+#pragma unroll
+        for (int c = 0; c < U; ++c)
+            if (8 * c < n) put_planes8(v + 8 * c, ph.out.hi + o + 8 * c, ph.out.lo != nullptr ? ph.out.lo + o + 8 * c : nullptr);
+        return;
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (warp == 1) tmem_free(tmem, 2 * BN);
-    if (threadIdx.x == 0 && abort_flag && a.sc != nullptr) atomicOr(&a.sc->status, ZERO_DEV_TIMEOUT);
+    const long long o = b * a.out_stride + row * a.out_ld + col;
+    if (ph.epi == EPI_OUT) {
+#pragma unroll
+        for (int c = 0; c < U; ++c)
+            if (8 * c < n) put_row8(a.out, a.out_dtype, o + 8 * c, v + 8 * c, n - 8 * c, a.out_vec);
+        return;
+    }
+    // w <- w * (1 - lr wd) - step * o, rounded to the master's fp32, then its 16-bit cast
+    float w[8 * U];
+    if (a.out_vec && n >= 8 * U) {
+#pragma unroll
+        for (int c = 0; c < 2 * U; ++c) {
+            const float4 q = *reinterpret_cast<const float4*>(a.master + o + 4 * c);
+            w[4 * c] = q.x, w[4 * c + 1] = q.y, w[4 * c + 2] = q.z, w[4 * c + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8 * U; ++e) w[e] = e < n ? a.master[o + e] : 0.0f;
+    }
+#pragma unroll
+    for (int e = 0; e < 8 * U; ++e) v[e] = fmaf(-a.step, v[e], w[e] * a.decay);
+#pragma unroll
+    for (int c = 0; c < U; ++c) {
+        if (8 * c >= n) break;
+        put_row8(a.master, ZERO_FP32, o + 8 * c, v + 8 * c, n - 8 * c, a.out_vec);
+        if (a.lp != nullptr) put_row8(a.lp, a.out_dtype, o + 8 * c, v + 8 * c, n - 8 * c, a.out_vec);
+    }
+}
+
+// Wait until *count, which others raise, reaches target; false (and an abort)
+// when the limit ran out or one of them gave up.
+__device__ __forceinline__ bool wait_count(unsigned* count, unsigned target, volatile int* abort_flag,
+                                           unsigned long long timeout_ns)
+{
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 0; it < (1u << 30); ++it) {
+        unsigned v;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(count) : "memory");
+        if (v & kPoison) break;
+        if (v >= target) return true;
+        if ((it & 63u) == 63u && (*abort_flag || globaltimer_ns() - t0 > timeout_ns)) break;
+    }
+    *abort_flag = 1;
+    return false;
+}
+__device__ __forceinline__ void raise_count(unsigned* count)
+{
+    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(count) : "memory");
 }
 
 // ------------------------------------------------- norms and first operands
@@ -434,21 +329,19 @@ struct PrepArgs {
     int dtype, vec;
     long long ld, stride;
     int rows, cols, chunks;      // chunks: groups of eight columns in a row
-    float eps;
     double* parts;               // [batch][gridDim.x]
-    __half* hi;
-    __half* lo;
-    long long out_ld, out_stride;
+    unsigned* counters;          // cleared for the products' kernel
+    int n_counters;
 };
 
 // eight consecutive elements from column 8 * ch of a row, zeros past its end
-__device__ __forceinline__ void load_row8(const PrepArgs& a, long long base, int row, int ch, float (&v)[8])
+__device__ __forceinline__ void load_row8(const void* in, int dtype, bool vec, long long row_at, int cols, int ch, float (&v)[8])
 {
-    const long long i = base + row * a.ld + 8 * ch;
-    const int n = a.cols - 8 * ch;
-    if (a.dtype == ZERO_FP32) {
-        const float* p = static_cast<const float*>(a.in) + i;
-        if (a.vec && n >= 8) {
+    const long long i = row_at + 8 * ch;
+    const int n = cols - 8 * ch;
+    if (dtype == ZERO_FP32) {
+        const float* p = static_cast<const float*>(in) + i;
+        if (vec && n >= 8) {
             const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + 4);
             v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
         } else {
@@ -457,9 +350,9 @@ __device__ __forceinline__ void load_row8(const PrepArgs& a, long long base, int
         }
         return;
     }
-    const uint16_t* p = static_cast<const uint16_t*>(a.in) + i;
+    const uint16_t* p = static_cast<const uint16_t*>(in) + i;
     uint32_t w[4];
-    if (a.vec && n >= 8) {
+    if (vec && n >= 8) {
         const uint4 x = *reinterpret_cast<const uint4*>(p);
         w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
     } else {
@@ -469,8 +362,8 @@ __device__ __forceinline__ void load_row8(const PrepArgs& a, long long base, int
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        v[2 * e] = a.dtype == ZERO_BF16 ? Lp<ZERO_BF16>::lo(w[e]) : Lp<ZERO_FP16>::lo(w[e]);
-        v[2 * e + 1] = a.dtype == ZERO_BF16 ? Lp<ZERO_BF16>::hi(w[e]) : Lp<ZERO_FP16>::hi(w[e]);
+        v[2 * e] = dtype == ZERO_BF16 ? Lp<ZERO_BF16>::lo(w[e]) : Lp<ZERO_FP16>::lo(w[e]);
+        v[2 * e + 1] = dtype == ZERO_BF16 ? Lp<ZERO_BF16>::hi(w[e]) : Lp<ZERO_FP16>::hi(w[e]);
     }
 }
 
@@ -487,7 +380,7 @@ __device__ __forceinline__ double squares8(const float (&v)[8])
     return d;
 }
 
-// sum over a block of 256 threads, in every thread; red: 8 doubles
+// sum over a block, in every thread; red: a double for each warp
 __device__ __forceinline__ double block_sum_f64(double v, double* red)
 {
     v = warp_sum_f64(v);
@@ -495,50 +388,32 @@ __device__ __forceinline__ double block_sum_f64(double v, double* red)
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
     double s = 0.0;
-    for (int i = 0; i < 8; ++i) s += red[i];
+    for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) s += red[i];
     return s;
+}
+
+__device__ __forceinline__ void clear_counters(unsigned* c, int n)
+{
+    if (blockIdx.x == 0 && blockIdx.y == 0)
+        for (int i = threadIdx.x; i < n; i += blockDim.x) c[i] = 0;
 }
 
 __global__ void __launch_bounds__(256) ns_sqnorm(const __grid_constant__ PrepArgs a)
 {
     __shared__ double red[8];
     pdl_wait();
-    pdl_launch();
+    clear_counters(a.counters, a.n_counters);
     const uint32_t total = static_cast<uint32_t>(a.rows) * a.chunks;
     const long long base = blockIdx.y * a.stride;
     double s = 0.0;
     for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < total; i += gridDim.x * 256) {
         const uint32_t row = i / static_cast<uint32_t>(a.chunks);
         float v[8];
-        load_row8(a, base, row, i - row * a.chunks, v);
+        load_row8(a.in, a.dtype, a.vec, base + row * a.ld, a.cols, i - row * a.chunks, v);
         s += squares8(v);
     }
     s = block_sum_f64(s, red);
     if (threadIdx.x == 0) a.parts[blockIdx.y * static_cast<long long>(gridDim.x) + blockIdx.x] = s;
-}
-
-// x_0 = g / (|g| + eps) as a scaled hi/lo pair; parts_n partial sums a matrix
-__global__ void __launch_bounds__(256) ns_scale(const __grid_constant__ PrepArgs a, int parts_n)
-{
-    __shared__ double red[8];
-    pdl_wait();
-    pdl_launch();
-    double s = 0.0;
-    for (int i = threadIdx.x; i < parts_n; i += 256) s += a.parts[blockIdx.y * static_cast<long long>(parts_n) + i];
-    s = block_sum_f64(s, red);
-    const float f = static_cast<float>(static_cast<double>(kScale) / (sqrt(s) + static_cast<double>(a.eps)));
-    const uint32_t total = static_cast<uint32_t>(a.rows) * a.chunks;
-    const long long base = blockIdx.y * a.stride;
-    for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < total; i += gridDim.x * 256) {
-        const uint32_t row = i / static_cast<uint32_t>(a.chunks);
-        const int ch = i - row * a.chunks;
-        float v[8];
-        load_row8(a, base, row, ch, v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = 8 * ch + e < a.cols ? v[e] * f : 0.0f;
-        const long long o = blockIdx.y * a.out_stride + row * a.out_ld + 8 * ch;
-        put_planes8(v, a.hi + o, a.lo + o);
-    }
 }
 
 struct MuonArgs {
@@ -550,6 +425,8 @@ struct MuonArgs {
     long long stride, u_stride;
     uint32_t elems;              // of one matrix
     double* parts;
+    unsigned* counters;
+    int n_counters;
 };
 
 // Rank mean (rank order, fp32), momentum, and the update direction u with its
@@ -558,7 +435,7 @@ __global__ void __launch_bounds__(256) muon_direction(const __grid_constant__ Mu
 {
     __shared__ double red[8];
     pdl_wait();
-    pdl_launch();
+    clear_counters(a.counters, a.n_counters);
     double s = 0.0;
     for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i * 8u < a.elems; i += gridDim.x * 256) {
         const int n = a.elems - 8 * i < 8 ? static_cast<int>(a.elems - 8 * i) : 8;
@@ -612,6 +489,367 @@ __global__ void __launch_bounds__(256) muon_direction(const __grid_constant__ Mu
     if (threadIdx.x == 0) a.parts[blockIdx.y * static_cast<long long>(gridDim.x) + blockIdx.x] = s;
 }
 
+// ------------------------------------------------------------ the products
+// JOINT (three products): a stage holds both planes of both operands, and the
+// small products lo*hi + hi*lo have an accumulator of their own, so that the
+// large one is added to no more often than with one product (each addition
+// drops low bits).  Otherwise a stage holds one plane of each, and three
+// products are three passes over the depth, the small ones first.
+template <int BN, bool JOINT>
+struct MmShape {
+    static constexpr int kABytes = kBM * kBK * 2, kBBytes = BN * kBK * 2;
+    static constexpr int kStageBytes = (kABytes + kBBytes) * (JOINT ? 2 : 1);
+    static constexpr int kStages = JOINT ? 3 : BN == 256 ? 4 : 6;
+    static constexpr int kAccCols = BN * (JOINT ? 2 : 1);   // of one of the two TMEM buffers
+    static constexpr int kSmem = kStages * kStageBytes + 1024;   // + alignment of the ring
+    static constexpr int kSb = BN > kBM ? BN : kBM;
+};
+
+// Phase `kind` (0: G = x x^T, 1: P = b G + c G G, 2: x <- a x + P x) of step s
+// of matrix b.
+template <int BN>
+__device__ __forceinline__ void set_phase(Phase& ph, const NsKernelArgs& a, int s, int kind, int b, const unsigned (&done)[3])
+{
+    const DevPlanes& xi = a.x[s & 1];
+    const DevPlanes& xo = a.x[(s & 1) ^ 1];
+    const CUtensorMap* xm = a.xmap[s & 1];
+    constexpr int SB = MmShape<BN, false>::kSb;
+    const bool last = s + 1 == a.steps;
+    ph.lower = kind < 2;
+    ph.epi = EPI_PLANES;
+    ph.alpha = kInvScale;
+    ph.beta = 0.0f;
+    ph.add_hi = ph.add_lo = nullptr;
+    ph.add_ld = 0;
+    if (kind == 0) {
+        ph.a = ph.b = xm;
+        ph.a_mode = ph.b_mode = a.wide ? kMajorK : kMajorMN;
+        ph.m = ph.n = a.m;
+        ph.k = a.wide ? a.cols : a.rows;
+        ph.out = a.g;
+    } else if (kind == 1) {
+        ph.a = ph.b = a.gmap;
+        ph.a_mode = ph.b_mode = kSymLower;
+        ph.m = ph.n = ph.k = a.m;
+        ph.alpha = a.coef[s][2] * kInvScale;
+        ph.beta = a.coef[s][1];
+        ph.add_hi = a.g.hi + b * a.g.stride;
+        ph.add_lo = a.g.lo != nullptr ? a.g.lo + b * a.g.stride : nullptr;
+        ph.add_ld = a.g.ld;
+        ph.out = a.p;
+    } else {
+        ph.a = a.wide ? a.pmap : xm;
+        ph.b = a.wide ? xm : a.pmap;
+        ph.a_mode = a.wide ? kSymLower : kMajorK;
+        ph.b_mode = a.wide ? kMajorMN : kSymLower;
+        ph.m = a.rows;
+        ph.n = a.cols;
+        ph.k = a.m;
+        ph.beta = a.coef[s][0];
+        ph.add_hi = xi.hi + b * xi.stride;
+        ph.add_lo = xi.lo + b * xi.stride;
+        ph.add_ld = xi.ld;
+        ph.out = xo;
+        if (last) {   // x itself leaves: scaled back
+            ph.epi = a.epi;
+            ph.alpha *= kInvScale;
+            ph.beta *= kInvScale;
+        }
+    }
+    ph.out.hi += b * ph.out.stride;
+    if (ph.out.lo != nullptr) ph.out.lo += b * ph.out.stride;
+    ph.tiles_m = (ph.m + kBM - 1) / kBM;
+    ph.tiles_n = (ph.n + BN - 1) / BN;
+    const int blocks = (a.m + SB - 1) / SB;
+    const int sym = (SB / kBM) * (SB / BN) * (blocks * (blocks + 1) / 2);
+    const int up = ((a.rows + kBM - 1) / kBM) * ((a.cols + BN - 1) / BN);
+    ph.tiles = ph.lower ? sym : up;
+    ph.split = a.split[kind];
+    // a tile's counter has been raised by every earlier phase that had the tile
+    const int t = blockIdx.x % a.ctas / ph.split;
+    ph.tile_target = ph.split;
+    for (int q = 0; q < 3; ++q)
+        if (a.split[q] > 1 && t < (q < 2 ? sym : up)) ph.tile_target += done[q] * a.split[q];
+}
+
+// The whole iteration in one launch.  The grid is `groups` of `ctas` CTAs, all
+// resident (a cooperative launch); a group takes its matrices one after the
+// other and meets at a counter in memory between products.  Within a product
+// the CTAs share the tiles, or, where there are fewer tiles than CTAs, each
+// tile's depth (its parts meet at a counter of the tile and each adds up its
+// share of the columns, in order).  Within a CTA a producer thread keeps a
+// ring of 64-deep operand tiles full by TMA, one thread issues the MMAs into
+// one of two TMEM accumulators, and eight warps turn the other one into
+// results.
+template <int BN, bool JOINT>
+__global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__ NsKernelArgs a)
+{
+    using S = MmShape<BN, JOINT>;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ uint64_t full[S::kStages], empty[S::kStages], acc_full[2], acc_empty[2], drain;
+    __shared__ uint32_t tmem_base;
+    __shared__ volatile int abort_flag;
+    __shared__ Phase ph;
+    __shared__ double red[kThreads / 32];
+    unsigned char* ring = smem_raw + (1024 - (smem_u32(smem_raw) & 1023u)) % 1024;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int group = blockIdx.x / a.ctas, cta = blockIdx.x % a.ctas;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], kEpiWarps);
+        }
+        mbar_init(&drain, 1);
+        abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) tmem_alloc(&tmem_base, 2 * S::kAccCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+
+    // where the roles are in the ring and the accumulators, over all phases
+    Slot<S::kStages> slot;
+    Slot<2> acc;
+    uint32_t count = 0;          // producer: stages issued; MMA: accumulators begun
+    unsigned met = 0, done[3] = {0, 0, 0};   // thread 0's: meetings, phases of each kind
+    bool stop = false;
+
+    for (int b = group; b < a.batch && !stop; b += a.groups) {
+        {   // x_0 = g / (|g| + eps), scaled
+            double q = 0.0;
+            for (int i = threadIdx.x; i < a.parts_n; i += kThreads) q += a.parts[static_cast<long long>(b) * a.parts_n + i];
+            q = block_sum_f64(q, red);
+            const float f = static_cast<float>(static_cast<double>(kScale) / (sqrt(q) + static_cast<double>(a.eps)));
+            const uint32_t total = static_cast<uint32_t>(a.rows) * a.chunks;
+            for (uint32_t i = cta * kThreads + threadIdx.x; i < total; i += a.ctas * kThreads) {
+                const uint32_t row = i / static_cast<uint32_t>(a.chunks);
+                const int ch = i - row * a.chunks;
+                float v[8];
+                load_row8(a.in, a.in_dtype, a.in_vec, b * a.in_stride + row * a.in_ld, a.cols, ch, v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = 8 * ch + e < a.cols ? v[e] * f : 0.0f;
+                const long long o = b * a.x[0].stride + row * a.x[0].ld + 8 * ch;
+                put_planes8(v, a.x[0].hi + o, a.x[0].lo + o);
+            }
+        }
+        for (int phase = 0; phase < 3 * a.steps; ++phase) {
+            // the group's results of the phase before, for everyone's TMA loads
+            fence_proxy_async_global();
+            __threadfence();
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                met += a.ctas;
+                if (a.ctas > 1) {
+                    if (abort_flag) {
+                        atomicOr(a.group_bar + group * kBarStride, kPoison);
+                    } else {
+                        raise_count(a.group_bar + group * kBarStride);
+                        wait_count(a.group_bar + group * kBarStride, met, &abort_flag, a.timeout_ns);
+                    }
+                }
+                set_phase<BN>(ph, a, phase / 3, phase % 3, b, done);
+                ++done[phase % 3];
+                ph.stop = abort_flag;
+            }
+            __syncthreads();
+            if (ph.stop) {
+                stop = true;
+                break;
+            }
+
+            const int first = ph.split > 1 ? cta / ph.split : cta, step = ph.split > 1 ? INT_MAX / 2 : a.ctas;
+            const int part = ph.split > 1 ? cta % ph.split : 0;
+            const int stages = (ph.k + kBK - 1) / kBK;
+            const int k_from = stages * part / ph.split * kBK, k_to = stages * (part + 1) / ph.split * kBK;
+            const int pass0 = JOINT ? 2 : 3 - a.products;
+
+            if (warp == 0) {
+                if (lane == 0) {
+                    fence_proxy_async_global();
+                    bool ok = true;
+                    for (int t = first; ok && t < ph.tiles; t += step) {
+                        const Tile tl = tile_of<BN>(ph, t);
+                        const int am = mn_from(ph.a_mode, S::kSb, tl.m0), bm = mn_from(ph.b_mode, S::kSb, tl.n0);
+                        for (int pass = pass0; ok && pass < 3; ++pass) {
+                            const CUtensorMap* ma = ph.a + (pass == 0);
+                            const CUtensorMap* mb = ph.b + (pass == 1);
+                            for (int k0 = k_from; k0 < k_to; k0 += kBK) {
+                                if (count >= S::kStages && !mbar_wait_bounded(&empty[slot.i], slot.parity ^ 1, &abort_flag, a.timeout_ns)) {
+                                    abort_flag = 1;
+                                    ok = false;
+                                    break;
+                                }
+                                if (!a.starve) {
+                                    unsigned char* p = ring + slot.i * S::kStageBytes;
+                                    uint64_t* bar = &full[slot.i];
+                                    mbar_arrive_expect_tx(bar, S::kStageBytes);
+                                    load_operand<kBM / kBox>(p, ma, k0 >= am, tl.m0, k0, b, bar);
+                                    load_operand<BN / kBox>(p + S::kABytes, mb, k0 >= bm, tl.n0, k0, b, bar);
+                                    if (JOINT) {
+                                        p += S::kABytes + S::kBBytes;
+                                        load_operand<kBM / kBox>(p, ma + 1, k0 >= am, tl.m0, k0, b, bar);
+                                        load_operand<BN / kBox>(p + S::kABytes, mb + 1, k0 >= bm, tl.n0, k0, b, bar);
+                                    }
+                                }
+                                slot.next();
+                                ++count;
+                            }
+                        }
+                    }
+                }
+                __syncwarp();
+            } else if (warp == 1) {
+                if (lane == 0) {
+                    bool ok = true;
+                    for (int t = first; ok && t < ph.tiles; t += step) {
+                        const Tile tl = tile_of<BN>(ph, t);
+                        const int am = mn_from(ph.a_mode, S::kSb, tl.m0), bm = mn_from(ph.b_mode, S::kSb, tl.n0);
+                        if (count >= 2 && !mbar_wait_bounded(&acc_empty[acc.i], acc.parity ^ 1, &abort_flag, a.timeout_ns)) {
+                            abort_flag = 1;
+                            break;
+                        }
+                        ++count;
+                        tc_fence_after();
+                        const uint32_t d = tmem + acc.i * S::kAccCols;
+                        bool more = false;   // false: the accumulator starts anew
+                        for (int pass = pass0; ok && pass < 3; ++pass) {
+                            for (int k0 = k_from; k0 < k_to; k0 += kBK) {
+                                if (!mbar_wait_bounded(&full[slot.i], slot.parity, &abort_flag, a.timeout_ns)) {
+                                    abort_flag = 1;
+                                    ok = false;
+                                    break;
+                                }
+                                tc_fence_after();
+                                const bool a_mn = k0 >= am, b_mn = k0 >= bm;
+                                const uint32_t idesc = instr_desc(kBM, BN, a_mn, b_mn);
+                                const uint32_t p = smem_u32(ring + slot.i * S::kStageBytes);
+                                const uint64_t da = smem_desc(p), db = smem_desc(p + S::kABytes);
+                                // sixteen values of depth: 32 bytes along a line, or sixteen lines
+                                const uint32_t sa = a_mn ? 2048 >> 4 : 32 >> 4, sbb = b_mn ? 2048 >> 4 : 32 >> 4;
+#pragma unroll
+                                for (int k = 0; k < kBK / 16; ++k) {
+                                    mma_f16(d, da + k * sa, db + k * sbb, idesc, more || k > 0);
+                                    if (JOINT) {
+                                        constexpr uint32_t kLo = (S::kABytes + S::kBBytes) >> 4;
+                                        mma_f16(d + BN, da + kLo + k * sa, db + k * sbb, idesc, more || k > 0);
+                                        mma_f16(d + BN, da + k * sa, db + kLo + k * sbb, idesc, true);
+                                    }
+                                }
+                                more = true;
+                                mma_commit(&empty[slot.i]);
+                                slot.next();
+                            }
+                        }
+                        if (ok) mma_commit(&acc_full[acc.i]);
+                        acc.next();
+                    }
+                }
+                __syncwarp();
+            } else {
+                const int quarter = warp & 3;         // the TMEM lanes this warp may read
+                const int half = (warp - 2) >> 2;     // its half of the columns
+                for (int t = first; t < ph.tiles; t += step) {
+                    const Tile tl = tile_of<BN>(ph, t);
+                    if (!mbar_wait_bounded(&acc_full[acc.i], acc.parity, &abort_flag, a.timeout_ns)) {
+                        abort_flag = 1;
+                        if (ph.split == 1) break;
+                        // the other warps of the CTA still meet below
+                    }
+                    tc_fence_after();
+                    const int row = tl.m0 + quarter * 32 + lane;
+                    const uint32_t d = tmem + acc.i * S::kAccCols + (static_cast<uint32_t>(quarter * 32) << 16);
+                    // [unit of eight columns][row][8] of this CTA
+                    float* mine = a.partial + static_cast<long long>(blockIdx.x) * (kBM * BN) + (quarter * 32 + lane) * 8;
+#pragma unroll 1
+                    for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 32) {
+                        const int col = tl.n0 + c;
+                        if (col >= ph.n) break;
+                        Addend x[4];
+                        if (ph.split == 1) load_addends<4>(ph, row, col, x);
+                        float v[32];
+                        tmem_load32(d + c, v);
+                        if (JOINT) {
+                            float w[32];
+                            tmem_load32(d + BN + c, w);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] += w[i];
+                        }
+                        if (ph.split == 1) {
+                            finish<4>(a, ph, b, row, col, x, v);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                __stcg(reinterpret_cast<float4*>(mine + (c / 8 + i / 2) * (kBM * 8)) + (i & 1),
+                                       make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&acc_empty[acc.i]);
+                    acc.next();
+                    if (ph.split == 1) continue;
+                    // all parts of the tile are there: add up this one's columns, part by part
+                    __threadfence();
+                    named_bar_sync(1, kEpiWarps * 32);
+                    if (threadIdx.x == 64 && !abort_flag) {
+                        unsigned* bar = a.tile_bar + group * a.ctas + t;
+                        raise_count(bar);
+                        wait_count(bar, ph.tile_target, &abort_flag, a.timeout_ns);
+                    }
+                    named_bar_sync(1, kEpiWarps * 32);
+                    if (abort_flag) break;
+                    const float* parts = mine - static_cast<long long>(part) * (kBM * BN);
+#pragma unroll 1
+                    for (int u = 2 * part + half; u < BN / 8; u += 2 * ph.split) {
+                        const int col = tl.n0 + 8 * u;
+                        if (col >= ph.n) break;
+                        Addend x[1];
+                        load_addends<1>(ph, row, col, x);
+                        float v[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+#pragma unroll 4
+                        for (int q = 0; q < ph.split; ++q) {
+                            const float4* p = reinterpret_cast<const float4*>(parts + static_cast<long long>(q) * (kBM * BN) + u * (kBM * 8));
+                            const float4 y = __ldcg(p), z = __ldcg(p + 1);
+                            v[0] += y.x, v[1] += y.y, v[2] += y.z, v[3] += y.w;
+                            v[4] += z.x, v[5] += z.y, v[6] += z.z, v[7] += z.w;
+                        }
+                        finish<1>(a, ph, b, row, col, x, v);
+                    }
+                }
+            }
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {
+        if (lane == 0 && abort_flag && !a.starve) {
+            // nothing of ours may still be landing when the CTA's memory goes away
+            for (uint32_t i = count > S::kStages ? count - S::kStages : 0; i < count; ++i)
+                mbar_wait_bounded(&full[i % S::kStages], (i / S::kStages) & 1, nullptr, 1000000000ull);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            mma_commit(&drain);   // TMEM is given back only after the last MMA
+            mbar_wait_bounded(&drain, 0, nullptr, 1000000000ull);
+        }
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_free(tmem, 2 * S::kAccCols);
+    if (threadIdx.x == 0 && abort_flag && a.sc != nullptr) atomicOr(&a.sc->status, ZERO_DEV_TIMEOUT);
+}
+
 // ------------------------------------------------------------------- host
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -654,11 +892,93 @@ bool encode(CUtensorMap* map, const Planes& p, const __half* plane, int batch)
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// How a call is cut up.
+struct Plan {
+    int bn, joint;
+    int groups, ctas;
+    int split[3];
+    double us;
+};
+
+// Times of a CTA, in us, that the choice goes by (measured): a 64-deep stage
+// of 128 x 256 (48 KB of operands) and of 128 x 128 (32 KB; both planes: 64),
+// a tile's results after its last MMA, the exchange of partial sums, the
+// meeting of a group.
+constexpr double kStage256 = 0.39, kStage128 = 0.25, kStageJoint = 0.46;
+constexpr double kTileEnd = 2.0, kSplitEnd = 3.0, kMeet = 1.5, kMeetAlone = 0.5;
+
+long long sym_tiles(int m, int bn)
+{
+    const int sb = bn > kBM ? bn : kBM;
+    const long long blocks = (m + sb - 1) / sb;
+    return static_cast<long long>(sb / kBM) * (sb / bn) * (blocks * (blocks + 1) / 2);
+}
+
+// the time of one product with `tiles` tiles and `stages` stages each on
+// `ctas` CTAs, and how many of them share a tile
+double phase_us(long long tiles, int stages, int passes, double stage_us, int ctas, int& split)
+{
+    split = 1;
+    double best = static_cast<double>((tiles + ctas - 1) / ctas) * stages * passes * stage_us + kTileEnd;
+    if (tiles < ctas) {
+        int most = static_cast<int>(ctas / tiles);
+        if (most > stages) most = stages;
+        if (most > 16) most = 16;
+        for (int q = 2; q <= most; ++q) {
+            const double us = static_cast<double>((stages + q - 1) / q) * passes * stage_us + kTileEnd + kSplitEnd;
+            if (us < best) best = us, split = q;
+        }
+    }
+    return best;
+}
+
+Plan plan_of(int rows, int cols, int batch, int products, int sms)
+{
+    const int m = rows < cols ? rows : cols, n = rows < cols ? cols : rows;
+    Plan best;
+    std::memset(&best, 0, sizeof(best));
+    for (int bn = 128; bn <= 256; bn += 128) {
+        const int joint = bn == 128 && products == 3, passes = joint ? 1 : products;
+        const double st = joint ? kStageJoint : bn == 128 ? kStage128 : kStage256;
+        const long long sym = sym_tiles(m, bn);
+        const long long up = static_cast<long long>((rows + kBM - 1) / kBM) * ((cols + bn - 1) / bn);
+        int last = 0;
+        for (int groups = 1; groups <= batch && groups <= sms; ++groups) {
+            Plan p;
+            p.bn = bn;
+            p.joint = joint;
+            p.groups = groups;
+            p.ctas = sms / groups;
+            const int turns = (batch + groups - 1) / groups;
+            if (turns == last) continue;   // the same with smaller groups
+            last = turns;
+            for (int pass = 0; pass < 2; ++pass) {
+                // as they are, then alone: without the meetings
+                if (pass == 1) p.ctas = 1;
+                const double us = phase_us(sym, (n + kBK - 1) / kBK, passes, st, p.ctas, p.split[0]) +
+                                  phase_us(sym, (m + kBK - 1) / kBK, passes, st, p.ctas, p.split[1]) +
+                                  phase_us(up, (m + kBK - 1) / kBK, passes, st, p.ctas, p.split[2]);
+                p.us = turns * (us + 3 * (p.ctas > 1 ? kMeet : kMeetAlone));
+                if (best.bn == 0 || p.us < best.us) best = p;
+            }
+        }
+    }
+    long long most = 0;
+    for (int q = 0; q < 3; ++q) {
+        const long long tiles = q < 2 ? sym_tiles(m, best.bn) : static_cast<long long>((rows + kBM - 1) / kBM) * ((cols + best.bn - 1) / best.bn);
+        if (most < tiles * best.split[q]) most = tiles * best.split[q];
+    }
+    if (most < best.ctas) best.ctas = static_cast<int>(most);   // CTAs that would only wait
+    return best;
+}
+
 struct Layout {
-    size_t parts, u, x[2], g, p, end;
+    size_t parts, counters, partial, u, x[2], g, p, end;
     long long x_plane, s_plane;   // elements of one plane
     int planes;
 };
+
+constexpr int kMaxSms = 160;      // GB300 has 152
 
 Layout layout_of(int rows, int cols, int batch, int products, bool muon)
 {
@@ -668,8 +988,12 @@ Layout layout_of(int rows, int cols, int batch, int products, bool muon)
     l.x_plane = static_cast<long long>(batch) * rows * up64(cols);
     l.s_plane = static_cast<long long>(batch) * m * up64(m);
     size_t at = 0;
+    l.counters = at;
+    at += up256(static_cast<size_t>(kMaxSms) * (kBarStride + 1) * sizeof(unsigned));
     l.parts = at;
     at += up256(static_cast<size_t>(batch) * kMaxNsParts * sizeof(double));
+    l.partial = at;
+    at += static_cast<size_t>(kMaxSms) * kBM * 256 * sizeof(float);
     l.u = at;
     if (muon) at += up256(static_cast<size_t>(batch) * ((static_cast<size_t>(rows) * cols + 7) / 8 * 8) * sizeof(float));
     for (int i = 0; i < 2; ++i) {
@@ -701,60 +1025,44 @@ int sm_count()
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return 0;
-    return n;
+    return n < kMaxSms ? n : kMaxSms;
 }
 
-template <int BN, int EPI>
-cudaError_t launch_mm_as(const MmArgs& a, int sms, cudaStream_t st)
+template <int BN, bool JOINT>
+cudaError_t launch_ns_as(const NsKernelArgs& a, cudaStream_t st)
 {
-    const cudaError_t e = cudaFuncSetAttribute(mm_kernel<BN, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize, MmShape<BN>::kSmem);
+    constexpr int smem = MmShape<BN, JOINT>::kSmem;
+    const auto k = ns_kernel<BN, JOINT>;
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return launch_after(mm_kernel<BN, EPI>, dim3(a.tiles < sms ? a.tiles : sms), dim3(kMmThreads), MmShape<BN>::kSmem, st, a);
+    cudaLaunchConfig_t c;
+    std::memset(&c, 0, sizeof(c));
+    c.gridDim = dim3(a.groups * a.ctas);
+    c.blockDim = dim3(kThreads);
+    c.dynamicSmemBytes = smem;
+    c.stream = st;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeCooperative;   // CTAs that wait for one another are resident together
+    at.val.cooperative = 1;
+    c.attrs = &at;
+    c.numAttrs = a.ctas > 1 ? 1 : 0;
+    count_launch();
+    return cudaLaunchKernelEx(&c, k, a);
 }
 
-template <int EPI>
-cudaError_t launch_mm(int bn, MmArgs& a, int batch, int sms, cudaStream_t st)
+cudaError_t launch_products(const Plan& p, const NsKernelArgs& a, cudaStream_t st)
 {
-    const int sb = bn > kBM ? bn : kBM;
-    a.sb = sb;
-    a.tiles_n = (a.n + bn - 1) / bn;
-    a.tiles_m = (a.m + kBM - 1) / kBM;
-    if (a.lower) {
-        const int blocks = (a.m + sb - 1) / sb;
-        a.tiles_per_matrix = (sb / kBM) * (sb / bn) * (blocks * (blocks + 1) / 2);
-    } else {
-        a.tiles_per_matrix = a.tiles_n * a.tiles_m;
-    }
-    a.tiles = a.tiles_per_matrix * batch;
-    if (bn == 256) return launch_mm_as<256, EPI>(a, sms, st);
-    if (bn == 128) return launch_mm_as<128, EPI>(a, sms, st);
-    return launch_mm_as<64, EPI>(a, sms, st);
+    if (p.bn == 256) return launch_ns_as<256, false>(a, st);
+    return p.joint ? launch_ns_as<128, true>(a, st) : launch_ns_as<128, false>(a, st);
 }
 
-bool set_operands(MmArgs& m, const Planes& a, int a_mode, const Planes& b, int b_mode, int products, int batch)
+bool set_planes(DevPlanes& d, CUtensorMap* maps, const Planes& p, int batch)
 {
-    m.a_mode = a_mode;
-    m.b_mode = b_mode;
-    m.products = products;
-    bool ok = encode(&m.a[0], a, a.hi, batch) && encode(&m.b[0], b, b.hi, batch);
-    if (products == 3) ok = ok && encode(&m.a[1], a, a.lo, batch) && encode(&m.b[1], b, b.lo, batch);
-    return ok;
-}
-
-void set_addend(MmArgs& m, const Planes& p)
-{
-    m.add_hi = p.hi;
-    m.add_lo = p.lo;
-    m.add_ld = p.ld;
-    m.add_stride = p.stride;
-}
-
-void set_result(MmArgs& m, const Planes& p)
-{
-    m.out_hi = p.hi;
-    m.out_lo = p.lo;
-    m.out_ld = p.ld;
-    m.out_stride = p.stride;
+    d.hi = p.hi;
+    d.lo = p.lo;
+    d.ld = p.ld;
+    d.stride = p.stride;
+    return encode(&maps[0], p, p.hi, batch) && (p.lo == nullptr || encode(&maps[1], p, p.lo, batch));
 }
 
 }  // namespace
@@ -772,17 +1080,22 @@ size_t ns_workspace_bytes(int rows, int cols, int batch, int products, bool muon
 
 cudaError_t launch_mm_starved(void* scratch, zero_dev_scalars* sc, unsigned long long timeout_ns, cudaStream_t st)
 {
-    const Planes p = planes_at(scratch, 0, 64 * 64, 64, 64, false);
-    const Planes r = planes_at(scratch, 64 * 64 * 2, 64 * 64, 64, 64, false);
-    MmArgs k;
+    // one 64 x 64 matrix: its planes in the scratch are never read or written
+    // (the input is empty)
+    NsKernelArgs k;
     std::memset(&k, 0, sizeof(k));
-    k.m = k.n = k.k = 64;
+    const Planes p = planes_at(scratch, 0, 64 * 64, 64, 64, false);
+    k.rows = k.cols = k.m = 64;
+    k.wide = k.batch = k.steps = k.products = k.groups = k.ctas = k.split[0] = k.split[1] = k.split[2] = 1;
+    k.eps = 1.0f;
     k.sc = sc;
-    k.timeout_ns = timeout_ns;
     k.starve = 1;
-    if (!set_operands(k, p, kMajorK, p, kMajorK, 1, 1)) return cudaErrorInvalidValue;
-    set_result(k, r);
-    return launch_mm<EPI_PLANES>(64, k, 1, 1, st);
+    k.timeout_ns = timeout_ns;
+    if (!set_planes(k.x[0], k.xmap[0], p, 1) || !set_planes(k.g, k.gmap, p, 1)) return cudaErrorInvalidValue;
+    Plan plan;
+    std::memset(&plan, 0, sizeof(plan));
+    plan.bn = 128;
+    return launch_products(plan, k, st);
 }
 
 cudaError_t launch_ns(const NsArgs& a, cudaStream_t st)
@@ -792,27 +1105,44 @@ cudaError_t launch_ns(const NsArgs& a, cudaStream_t st)
     const bool muon = a.out == nullptr, wide = a.rows <= a.cols;
     const int m = wide ? a.rows : a.cols;
     const Layout l = layout_of(a.rows, a.cols, a.batch, a.products, muon);
-    Planes x[2] = {planes_at(a.ws, l.x[0], l.x_plane, a.rows, a.cols, true), planes_at(a.ws, l.x[1], l.x_plane, a.rows, a.cols, true)};
-    const Planes g = planes_at(a.ws, l.g, l.s_plane, m, m, a.products == 3);
-    const Planes p = planes_at(a.ws, l.p, l.s_plane, m, m, a.products == 3);
+    const Plan plan = plan_of(a.rows, a.cols, a.batch, a.products, sms);
+    char* ws = static_cast<char*>(a.ws);
+    unsigned* counters = reinterpret_cast<unsigned*>(ws + l.counters);
 
-    // the norm and x_0
-    PrepArgs pr;
-    std::memset(&pr, 0, sizeof(pr));
-    pr.rows = a.rows;
-    pr.cols = a.cols;
-    pr.chunks = (a.cols + 7) / 8;
-    pr.eps = a.eps;
-    pr.parts = reinterpret_cast<double*>(static_cast<char*>(a.ws) + l.parts);
-    pr.hi = x[0].hi;
-    pr.lo = x[0].lo;
-    pr.out_ld = x[0].ld;
-    pr.out_stride = x[0].stride;
-    // CTAs a matrix: four chunks a thread, eight CTAs an SM over the batch
-    const long long chunks = static_cast<long long>(a.rows) * pr.chunks;
+    NsKernelArgs k;
+    std::memset(&k, 0, sizeof(k));
+    bool ok = true;
+    for (int i = 0; i < 2; ++i) ok = ok && set_planes(k.x[i], k.xmap[i], planes_at(ws, l.x[i], l.x_plane, a.rows, a.cols, true), a.batch);
+    ok = ok && set_planes(k.g, k.gmap, planes_at(ws, l.g, l.s_plane, m, m, a.products == 3), a.batch);
+    ok = ok && set_planes(k.p, k.pmap, planes_at(ws, l.p, l.s_plane, m, m, a.products == 3), a.batch);
+    if (!ok) return cudaErrorInvalidValue;
+    k.rows = a.rows;
+    k.cols = a.cols;
+    k.m = m;
+    k.wide = wide;
+    k.batch = a.batch;
+    k.steps = a.steps;
+    k.products = a.products;
+    k.groups = plan.groups;
+    k.ctas = plan.ctas;
+    std::memcpy(k.split, plan.split, sizeof(k.split));
+    std::memcpy(k.coef, a.coef, sizeof(k.coef));
+    k.chunks = (a.cols + 7) / 8;
+    k.eps = a.eps;
+    double* parts = reinterpret_cast<double*>(ws + l.parts);
+    k.parts = parts;
+    k.group_bar = counters;
+    k.tile_bar = counters + kMaxSms * kBarStride;
+    k.partial = reinterpret_cast<float*>(ws + l.partial);
+    k.sc = a.sc;
+    k.timeout_ns = kDefaultTimeoutNs;
+
+    // the norm: CTAs a matrix, four chunks a thread, eight CTAs an SM over the batch
+    const long long chunks = static_cast<long long>(a.rows) * k.chunks;
     long long per = (chunks + 1023) / 1024, most = (8LL * sms + a.batch - 1) / a.batch;
     if (per > most) per = most;
     if (per > kMaxNsParts) per = kMaxNsParts;
+    k.parts_n = static_cast<int>(per);
     const dim3 grid(static_cast<unsigned>(per), a.batch);
     if (muon) {
         MuonArgs mu;
@@ -824,98 +1154,57 @@ cudaError_t launch_ns(const NsArgs& a, cudaStream_t st)
         mu.divisor = a.divisor;
         mu.mu = a.mu;
         mu.momentum = a.momentum;
-        mu.u = reinterpret_cast<float*>(static_cast<char*>(a.ws) + l.u);
+        mu.u = reinterpret_cast<float*>(ws + l.u);
         mu.stride = a.flat_stride;
         mu.elems = static_cast<uint32_t>(a.rows) * static_cast<uint32_t>(a.cols);
         mu.u_stride = (static_cast<long long>(mu.elems) + 7) / 8 * 8;
-        mu.parts = pr.parts;
-        pr.in = mu.u;
-        pr.dtype = ZERO_FP32;
-        pr.ld = a.cols;
-        pr.stride = mu.u_stride;
-        pr.vec = a.cols % 4 == 0;
+        mu.parts = parts;
+        mu.counters = counters;
+        mu.n_counters = kMaxSms * (kBarStride + 1);
+        k.in = mu.u;
+        k.in_dtype = ZERO_FP32;
+        k.in_ld = a.cols;
+        k.in_stride = mu.u_stride;
+        k.in_vec = a.cols % 4 == 0;
+        k.epi = EPI_MUON;
+        k.master = a.master;
+        k.lp = a.lp;
+        k.out_dtype = a.lp_dtype;
+        k.out_ld = a.cols;
+        k.out_stride = a.flat_stride;
+        k.out_vec = a.cols % 8 == 0;
+        k.decay = a.decay;
+        k.step = a.step;
         ZK_GO(launch_after(muon_direction, grid, dim3(256), 0, st, mu));
     } else {
-        const int v = 16 / dtype_bytes(a.in_dtype);
-        pr.in = a.in;
-        pr.dtype = a.in_dtype;
-        pr.ld = a.in_ld;
-        pr.stride = a.in_stride;
-        pr.vec = reinterpret_cast<uintptr_t>(a.in) % 16 == 0 && a.in_ld % v == 0 && a.in_stride % v == 0;
+        const int v = 16 / dtype_bytes(a.in_dtype), w = 16 / dtype_bytes(a.out_dtype);
+        k.in = a.in;
+        k.in_dtype = a.in_dtype;
+        k.in_ld = a.in_ld;
+        k.in_stride = a.in_stride;
+        k.in_vec = reinterpret_cast<uintptr_t>(a.in) % 16 == 0 && a.in_ld % v == 0 && a.in_stride % v == 0;
+        k.epi = EPI_OUT;
+        k.out = a.out;
+        k.out_dtype = a.out_dtype;
+        k.out_ld = a.out_ld;
+        k.out_stride = a.out_stride;
+        k.out_vec = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.out_ld % w == 0 && a.out_stride % w == 0;
+        PrepArgs pr;
+        std::memset(&pr, 0, sizeof(pr));
+        pr.in = k.in;
+        pr.dtype = k.in_dtype;
+        pr.vec = k.in_vec;
+        pr.ld = k.in_ld;
+        pr.stride = k.in_stride;
+        pr.rows = a.rows;
+        pr.cols = a.cols;
+        pr.chunks = k.chunks;
+        pr.parts = parts;
+        pr.counters = counters;
+        pr.n_counters = kMaxSms * (kBarStride + 1);
         ZK_GO(launch_after(ns_sqnorm, grid, dim3(256), 0, st, pr));
     }
-    ZK_GO(launch_after(ns_scale, grid, dim3(256), 0, st, pr, static_cast<int>(per)));
-
-    // one tile width for the call (the stored triangle's blocks go by it)
-    const long long wide_tiles = static_cast<long long>(a.batch) * ((a.rows + kBM - 1) / kBM) * ((a.cols + 255) / 256);
-    const int bn = wide_tiles >= sms ? 256 : 2 * wide_tiles >= sms ? 128 : 64;
-
-    MmArgs base;
-    std::memset(&base, 0, sizeof(base));
-    base.sc = a.sc;
-    base.timeout_ns = kDefaultTimeoutNs;
-    for (int s = 0; s < a.steps; ++s) {
-        const Planes& xi = x[s & 1];
-        const Planes& xo = x[(s & 1) ^ 1];
-        const float ca = a.coef[s][0], cb = a.coef[s][1], cc = a.coef[s][2];
-        MmArgs k = base;   // G = x x^T
-        k.m = k.n = m;
-        k.k = wide ? a.cols : a.rows;
-        k.lower = 1;
-        k.alpha = kInvScale;
-        if (!set_operands(k, xi, wide ? kMajorK : kMajorMN, xi, wide ? kMajorK : kMajorMN, a.products, a.batch)) return cudaErrorInvalidValue;
-        set_result(k, g);
-        ZK_GO(launch_mm<EPI_PLANES>(bn, k, a.batch, sms, st));
-
-        k = base;          // P = b G + c G G
-        k.m = k.n = k.k = m;
-        k.lower = 1;
-        k.alpha = cc * kInvScale;
-        k.beta = cb;
-        if (!set_operands(k, g, kSymLower, g, kSymLower, a.products, a.batch)) return cudaErrorInvalidValue;
-        set_addend(k, g);
-        set_result(k, p);
-        ZK_GO(launch_mm<EPI_ADD>(bn, k, a.batch, sms, st));
-
-        k = base;          // x <- a x + P x, or a x + x P
-        k.m = a.rows;
-        k.n = a.cols;
-        k.k = m;
-        k.alpha = kInvScale;
-        k.beta = ca;
-        if (!(wide ? set_operands(k, p, kSymLower, xi, kMajorMN, a.products, a.batch)
-                   : set_operands(k, xi, kMajorK, p, kSymLower, a.products, a.batch)))
-            return cudaErrorInvalidValue;
-        set_addend(k, xi);
-        if (s + 1 < a.steps) {
-            set_result(k, xo);
-            ZK_GO(launch_mm<EPI_ADD>(bn, k, a.batch, sms, st));
-            continue;
-        }
-        // the last step leaves x itself: scaled back, in its own type
-        k.alpha *= kInvScale;
-        k.beta *= kInvScale;
-        if (!muon) {
-            const int v = 16 / dtype_bytes(a.out_dtype);
-            k.out = a.out;
-            k.out_dtype = a.out_dtype;
-            k.out_ld = a.out_ld;
-            k.out_stride = a.out_stride;
-            k.out_vec = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.out_ld % v == 0 && a.out_stride % v == 0;
-            ZK_GO(launch_mm<EPI_OUT>(bn, k, a.batch, sms, st));
-        } else {
-            k.master = a.master;
-            k.lp = a.lp;
-            k.out_dtype = a.lp_dtype;
-            k.out_ld = a.cols;
-            k.out_stride = a.flat_stride;
-            k.out_vec = a.cols % 8 == 0;
-            k.decay = a.decay;
-            k.step = a.step;
-            ZK_GO(launch_mm<EPI_MUON>(bn, k, a.batch, sms, st));
-        }
-    }
-    return cudaSuccess;
+    return launch_products(plan, k, st);
 }
 
 }  // namespace zk
