@@ -38,8 +38,9 @@ constexpr int kBM = 128;       // output rows of a CTA's tile (TMEM lanes)
 constexpr int kBK = 64;        // depth of a pipeline stage: 128 bytes, one swizzle line
 constexpr int kBox = 64;       // TMA boxes are 64 x 64 values, 8 KB, whichever side is the depth
 constexpr int kBoxBytes = kBox * kBK * 2;
-constexpr int kThreads = 320;  // producer warp, MMA warp, eight epilogue warps
+constexpr int kThreads = 352;  // producer, MMA, eight epilogue warps, one that plans the next phase
 constexpr int kEpiWarps = 8;
+constexpr int kTurnBytes = 32 * 32 * 4;   // of an epilogue warp's 32 x 32 turning buffer
 constexpr int kMaxNsParts = 1024;
 constexpr int kStrip = 16;     // row tiles of a strip (see tile_of)
 constexpr int kBarStride = 32; // words between the groups' barrier counters: a line each
@@ -49,9 +50,6 @@ constexpr unsigned kPoison = 0x80000000u;
 // contiguous (MN-major), or a symmetric matrix of which only the blocks of
 // `sb` x `sb` on and under the diagonal are stored
 enum { kMajorK = 0, kMajorMN = 1, kSymLower = 2 };
-// what becomes of the sums: a pair of fp16 planes, the result, or the weights
-enum { EPI_PLANES = 0, EPI_OUT = 1, EPI_MUON = 2 };
-
 struct DevPlanes {
     __half* hi;
     __half* lo;                  // may be null
@@ -74,7 +72,7 @@ struct NsKernelArgs {
     const double* parts;         // [batch][parts_n] sums of squares
     int parts_n;
     // the result
-    int epi;
+    int res;                     // RES_OUT or RES_MUON
     void* out;
     int out_dtype, out_vec;
     long long out_ld, out_stride;
@@ -90,6 +88,10 @@ struct NsKernelArgs {
     unsigned long long timeout_ns;
 };
 
+struct Tile {
+    int m0, n0;
+};
+
 // One product: alpha * A B^T + beta * addend over an m x n result.
 struct Phase {
     const CUtensorMap* a;        // hi; lo follows
@@ -98,18 +100,19 @@ struct Phase {
     int m, n, k;
     int lower;                   // only blocks on and under the diagonal
     int tiles_m, tiles_n, tiles, split;
-    int stop;                    // a wait has run out somewhere
+    Tile first;                  // this CTA's first tile
     unsigned tile_target;        // tile_bar's count once all parts of a tile of this phase are there
-    int epi;
+    int res;
     float alpha, beta;
-    const __half* add_hi;        // this matrix's; null: no addend
+    const __half* add_hi;        // this matrix's
     const __half* add_lo;
     long long add_ld;
-    DevPlanes out;               // EPI_PLANES: this matrix's
-};
-
-struct Tile {
-    int m0, n0;
+    DevPlanes out;               // RES_PLANES*: this matrix's
+    void* res_out;               // RES_OUT, RES_MUON: this matrix's result, or master and 16-bit weights
+    float* master;
+    int res_dtype, res_vec;
+    long long res_ld;
+    float decay, step;
 };
 
 // Tile t of a phase.  Lower-triangle phases number the tiles of block row I
@@ -176,34 +179,57 @@ __device__ __forceinline__ float2 half2_up(uint32_t w)
 // L2: another SM may have written them a moment ago
 struct Addend {
     uint4 h, l;
+    __device__ __forceinline__ void zero() { h = l = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void load(const __half* hi, const __half* lo)
     {
         h = __ldcg(reinterpret_cast<const uint4*>(hi));
         l = lo != nullptr ? __ldcg(reinterpret_cast<const uint4*>(lo)) : make_uint4(0, 0, 0, 0);
     }
-    // v = alpha * v + beta * (hi + lo)
-    __device__ __forceinline__ void into(float* v, float alpha, float beta) const
+};
+
+// eight fp32 values in register pairs
+struct Eight {
+    f32x2 v[4];
+    __device__ __forceinline__ void set(const float4& p, const float4& q)
     {
-        const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
+        v[0] = pack2(p.x, p.y), v[1] = pack2(p.z, p.w), v[2] = pack2(q.x, q.y), v[3] = pack2(q.z, q.w);
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) unpack2(v[i], f[2 * i], f[2 * i + 1]);
+    }
+    __device__ __forceinline__ void scale(f32x2 alpha)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], alpha);
+    }
+    // alpha * v + beta * (hi + lo)
+    __device__ __forceinline__ void combine(f32x2 alpha, f32x2 beta, const Addend& x)
+    {
+        const uint32_t hw[4] = {x.h.x, x.h.y, x.h.z, x.h.w}, lw[4] = {x.l.x, x.l.y, x.l.z, x.l.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 p = half2_up(hw[i]), q = half2_up(lw[i]);
-            v[2 * i] = fmaf(beta, p.x + q.x, alpha * v[2 * i]);
-            v[2 * i + 1] = fmaf(beta, p.y + q.y, alpha * v[2 * i + 1]);
+            v[i] = fma2(beta, add2(pack2(p.x, p.y), pack2(q.x, q.y)), mul2(alpha, v[i]));
         }
     }
 };
 
-__device__ __forceinline__ void put_planes8(const float* v, __half* hi, __half* lo)
+__device__ __forceinline__ void put_planes8(const Eight& x, __half* hi, __half* lo)
 {
     uint32_t hw[4], lw[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-        const float2 f = __half22float2(h);
-        const __half2 l = __floats2half2_rn(v[2 * i] - f.x, v[2 * i + 1] - f.y);
+        float a, b;
+        unpack2(x.v[i], a, b);
+        const __half2 h = __floats2half2_rn(a, b);
         hw[i] = *reinterpret_cast<const uint32_t*>(&h);
-        lw[i] = *reinterpret_cast<const uint32_t*>(&l);
+        if (lo != nullptr) {
+            const float2 f = __half22float2(h);
+            const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
+            lw[i] = *reinterpret_cast<const uint32_t*>(&l);
+        }
     }
     *reinterpret_cast<uint4*>(hi) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
     if (lo != nullptr) *reinterpret_cast<uint4*>(lo) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
@@ -244,61 +270,156 @@ __device__ __forceinline__ void put_row8(void* base, int dt, long long i, const 
     }
 }
 
-// the addend of U groups of eight columns from column `col` of a row
-template <int U>
-__device__ __forceinline__ void load_addends(const Phase& ph, int row, int col, Addend (&x)[U])
-{
-#pragma unroll
-    for (int c = 0; c < U; ++c) {
-        x[c].h = x[c].l = make_uint4(0, 0, 0, 0);
-        if (ph.add_hi == nullptr || row >= ph.m || col + 8 * c >= ph.n) continue;
-        const long long at = row * ph.add_ld + col + 8 * c;
-        x[c].load(ph.add_hi + at, ph.add_lo != nullptr ? ph.add_lo + at : nullptr);
-    }
-}
+// what becomes of a phase's sums: a pair of fp16 planes, the result, or the weights
+enum { RES_PLANES = 0, RES_OUT = 1, RES_MUON = 2 };
 
-// U groups of eight sums of one row, from column `col`, to where they belong
-template <int U>
-__device__ __forceinline__ void finish(const NsKernelArgs& a, const Phase& ph, int b, int row, int col,
-                                       const Addend (&x)[U], float (&v)[8 * U])
-{
-    const int n = ph.n - col;
-    if (row >= ph.m || n <= 0) return;
-#pragma unroll
-    for (int c = 0; c < U; ++c) x[c].into(v + 8 * c, ph.alpha, ph.beta);
-    if (ph.epi == EPI_PLANES) {
-        const long long o = row * ph.out.ld + col;
-#pragma unroll
-        for (int c = 0; c < U; ++c)
-            if (8 * c < n) put_planes8(v + 8 * c, ph.out.hi + o + 8 * c, ph.out.lo != nullptr ? ph.out.lo + o + 8 * c : nullptr);
-        return;
+// What the results of a phase need, in registers.
+struct Results {
+    int m, n, res;
+    float alpha, beta;
+    const __half* add_hi;
+    const __half* add_lo;
+    int add_ld;
+    __half* hi;
+    __half* lo;
+    int ld;
+
+    __device__ __forceinline__ explicit Results(const Phase& ph)
+        : m(ph.m), n(ph.n), res(ph.res), alpha(ph.alpha), beta(ph.beta), add_hi(ph.add_hi), add_lo(ph.add_lo),
+          add_ld(static_cast<int>(ph.add_ld)), hi(ph.out.hi), lo(ph.out.lo), ld(static_cast<int>(ph.out.ld))
+    {
     }
-    const long long o = b * a.out_stride + row * a.out_ld + col;
-    if (ph.epi == EPI_OUT) {
-#pragma unroll
-        for (int c = 0; c < U; ++c)
-            if (8 * c < n) put_row8(a.out, a.out_dtype, o + 8 * c, v + 8 * c, n - 8 * c, a.out_vec);
+    __device__ __forceinline__ void load(int row, int col, Addend& x) const
+    {
+        x.zero();
+        if (add_hi == nullptr || row >= m || col >= n) return;
+        const long long at = static_cast<long long>(row) * add_ld + col;
+        x.load(add_hi + at, add_lo != nullptr ? add_lo + at : nullptr);
+    }
+};
+
+// The last phase: x itself, to the result or into the weights; n of the eight
+// values exist.  Once a call, so kept out of the other phases' way.
+__device__ __noinline__ void put_last(const Phase* ph, int row, int col, Eight u)
+{
+    const int n = ph->n - col;
+    const long long o = row * ph->res_ld + col;
+    const bool vec = ph->res_vec;
+    float v[8];
+    u.get(v);
+    if (ph->res == RES_OUT) {
+        put_row8(ph->res_out, ph->res_dtype, o, v, n, vec);
         return;
     }
     // w <- w * (1 - lr wd) - step * o, rounded to the master's fp32, then its 16-bit cast
-    float w[8 * U];
-    if (a.out_vec && n >= 8 * U) {
-#pragma unroll
-        for (int c = 0; c < 2 * U; ++c) {
-            const float4 q = *reinterpret_cast<const float4*>(a.master + o + 4 * c);
-            w[4 * c] = q.x, w[4 * c + 1] = q.y, w[4 * c + 2] = q.z, w[4 * c + 3] = q.w;
-        }
+    float* master = ph->master;
+    const float decay = ph->decay, step = ph->step;
+    float w[8];
+    if (vec && n >= 8) {
+        const float4 p = *reinterpret_cast<const float4*>(master + o), q = *reinterpret_cast<const float4*>(master + o + 4);
+        w[0] = p.x, w[1] = p.y, w[2] = p.z, w[3] = p.w, w[4] = q.x, w[5] = q.y, w[6] = q.z, w[7] = q.w;
     } else {
 #pragma unroll
-        for (int e = 0; e < 8 * U; ++e) w[e] = e < n ? a.master[o + e] : 0.0f;
+        for (int e = 0; e < 8; ++e) w[e] = e < n ? master[o + e] : 0.0f;
     }
 #pragma unroll
-    for (int e = 0; e < 8 * U; ++e) v[e] = fmaf(-a.step, v[e], w[e] * a.decay);
+    for (int e = 0; e < 8; ++e) v[e] = fmaf(-step, v[e], w[e] * decay);
+    put_row8(master, ZERO_FP32, o, v, n, vec);
+    if (ph->res_out != nullptr) put_row8(ph->res_out, ph->res_dtype, o, v, n, vec);
+}
+
+// eight sums of one row from column `col`, to where they belong
+__device__ __forceinline__ void put_results(const Results& r, const Phase& ph, int row, int col, const Addend& x, Eight& u)
+{
+    if (row >= r.m || col >= r.n) return;
+    u.combine(pack2(r.alpha, r.alpha), pack2(r.beta, r.beta), x);
+    if (r.res == RES_PLANES) {
+        const long long o = static_cast<long long>(row) * r.ld + col;
+        put_planes8(u, r.hi + o, r.lo != nullptr ? r.lo + o : nullptr);
+    } else {
+        put_last(&ph, row, col, u);
+    }
+}
+
+// 32 columns of this warp's 32 rows of sums, one row a thread
+template <int BN, bool JOINT>
+__device__ __forceinline__ void load_sums(uint32_t tmem, float (&v)[32])
+{
+    tmem_load32(tmem, v);
+    if (JOINT) {
+        float w[32];
+        tmem_load32(tmem + BN, w);
 #pragma unroll
-    for (int c = 0; c < U; ++c) {
-        if (8 * c >= n) break;
-        put_row8(a.master, ZERO_FP32, o + 8 * c, v + 8 * c, n - 8 * c, a.out_vec);
-        if (a.lp != nullptr) put_row8(a.lp, a.out_dtype, o + 8 * c, v + 8 * c, n - 8 * c, a.out_vec);
+        for (int i = 0; i < 32; ++i) v[i] += w[i];
+    }
+}
+
+// The results of a whole tile, by eight warps: `quarter` the 32 TMEM lanes
+// (rows) this one may read, `half` its half of the columns.  A lane of TMEM is
+// a row; memory wants whole rows side by side.  32 x 32 sums at a time turn in
+// shared memory (16-byte chunks, swizzled by the row): lane l then has the
+// columns 8 (l % 4) + .. of the rows l / 4 + 8 i.  What the results need from
+// memory is loaded before the sums.
+template <int BN, bool JOINT>
+__device__ __forceinline__ void tile_results(const Results& r, const Phase& ph, const Tile& tl, uint32_t tmem, int quarter,
+                                             int half, int lane, unsigned char* turn)
+{
+    const int row0 = tl.m0 + quarter * 32 + lane / 4;
+#pragma unroll 1
+    for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 32) {
+        if (tl.n0 + c >= r.n) break;
+        const int col = tl.n0 + c + lane % 4 * 8;
+        Addend x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.load(row0 + 8 * i, col, x[i]);
+        float v[32];
+        load_sums<BN, JOINT>(tmem + c, v);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4*>(turn + lane * 128 + ((i ^ (lane & 7)) * 16)) =
+                make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int k = lane / 4 + 8 * i, ch = lane % 4 * 2;
+            Eight u;
+            u.set(*reinterpret_cast<const float4*>(turn + k * 128 + ((ch ^ (k & 7)) * 16)),
+                  *reinterpret_cast<const float4*>(turn + k * 128 + (((ch + 1) ^ (k & 7)) * 16)));
+            put_results(r, ph, row0 + 8 * i, col, x[i], u);
+        }
+    }
+}
+
+// One part's share of a tile whose depth is split: the sums of all parts, in
+// their order, for BN / 8 / split groups of eight columns.  `parts` is the
+// first part's [group][row][8]; t: this thread of 256.
+constexpr int kMaxSplit = 8;
+template <int BN>
+__device__ __forceinline__ void split_results(const Results& r, const Phase& ph, const Tile& tl, const float* parts, int part,
+                                              int split, int t)
+{
+    const int units = BN / 8 / split;
+#pragma unroll 1
+    for (int i = t; i < units * kBM; i += kEpiWarps * 32) {
+        const int unit = part * units + i % units, k = i / units;
+        const int row = tl.m0 + k, col = tl.n0 + 8 * unit;
+        if (row >= r.m || col >= r.n) continue;
+        Addend x;
+        r.load(row, col, x);
+        const float4* p = reinterpret_cast<const float4*>(parts + unit * (kBM * 8) + k * 8);
+        Eight u;
+        u.set(make_float4(0.0f, 0.0f, 0.0f, 0.0f), make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+        for (int q = 0; q < split; q += 2) {   // an even number of parts
+            Eight y, z;
+            y.set(__ldcg(p), __ldcg(p + 1));
+            p += kBM * BN / 4;
+            z.set(__ldcg(p), __ldcg(p + 1));
+            p += kBM * BN / 4;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u.v[e] = add2(add2(u.v[e], y.v[e]), z.v[e]);
+        }
+        put_results(r, ph, row, col, x, u);
     }
 }
 
@@ -501,7 +622,7 @@ struct MmShape {
     static constexpr int kStageBytes = (kABytes + kBBytes) * (JOINT ? 2 : 1);
     static constexpr int kStages = JOINT ? 3 : BN == 256 ? 4 : 6;
     static constexpr int kAccCols = BN * (JOINT ? 2 : 1);   // of one of the two TMEM buffers
-    static constexpr int kSmem = kStages * kStageBytes + 1024;   // + alignment of the ring
+    static constexpr int kSmem = kStages * kStageBytes + kEpiWarps * kTurnBytes + 1024;   // + alignment of the ring
     static constexpr int kSb = BN > kBM ? BN : kBM;
 };
 
@@ -516,7 +637,7 @@ __device__ __forceinline__ void set_phase(Phase& ph, const NsKernelArgs& a, int 
     constexpr int SB = MmShape<BN, false>::kSb;
     const bool last = s + 1 == a.steps;
     ph.lower = kind < 2;
-    ph.epi = EPI_PLANES;
+    ph.res = RES_PLANES;
     ph.alpha = kInvScale;
     ph.beta = 0.0f;
     ph.add_hi = ph.add_lo = nullptr;
@@ -551,9 +672,21 @@ __device__ __forceinline__ void set_phase(Phase& ph, const NsKernelArgs& a, int 
         ph.add_ld = xi.ld;
         ph.out = xo;
         if (last) {   // x itself leaves: scaled back
-            ph.epi = a.epi;
+            ph.res = a.res;
             ph.alpha *= kInvScale;
             ph.beta *= kInvScale;
+            ph.res_dtype = a.out_dtype;
+            ph.res_vec = a.out_vec;
+            ph.res_ld = a.out_ld;
+            ph.decay = a.decay;
+            ph.step = a.step;
+            const long long at = b * a.out_stride;
+            if (a.res == RES_MUON) {
+                ph.master = a.master + at;
+                ph.res_out = a.lp != nullptr ? static_cast<uint16_t*>(a.lp) + at : nullptr;
+            } else {
+                ph.res_out = static_cast<char*>(a.out) + at * (a.out_dtype == ZERO_FP32 ? 4 : 2);
+            }
         }
     }
     ph.out.hi += b * ph.out.stride;
@@ -570,6 +703,8 @@ __device__ __forceinline__ void set_phase(Phase& ph, const NsKernelArgs& a, int 
     ph.tile_target = ph.split;
     for (int q = 0; q < 3; ++q)
         if (a.split[q] > 1 && t < (q < 2 ? sym : up)) ph.tile_target += done[q] * a.split[q];
+    const int first = ph.split > 1 ? t : blockIdx.x % a.ctas;
+    if (first < ph.tiles) ph.first = tile_of<BN>(ph, first);
 }
 
 // The whole iteration in one launch.  The grid is `groups` of `ctas` CTAs, all
@@ -589,7 +724,8 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
     __shared__ uint64_t full[S::kStages], empty[S::kStages], acc_full[2], acc_empty[2], drain;
     __shared__ uint32_t tmem_base;
     __shared__ volatile int abort_flag;
-    __shared__ Phase ph;
+    __shared__ Phase plan[2];
+    __shared__ int stop_flag;
     __shared__ double red[kThreads / 32];
     unsigned char* ring = smem_raw + (1024 - (smem_u32(smem_raw) & 1023u)) % 1024;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -614,12 +750,20 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
     tc_fence_after();
     const uint32_t tmem = tmem_base;
 
+    unsigned char* turn = ring + S::kStages * S::kStageBytes + (warp - 2) * kTurnBytes;   // of the epilogue warps
+
     // where the roles are in the ring and the accumulators, over all phases
     Slot<S::kStages> slot;
     Slot<2> acc;
     uint32_t count = 0;          // producer: stages issued; MMA: accumulators begun
-    unsigned met = 0, done[3] = {0, 0, 0};   // thread 0's: meetings, phases of each kind
+    unsigned met = 0;            // thread 0's: arrivals at the group's meetings
+    unsigned done[3] = {0, 0, 0};   // the planning thread's: phases of each kind
     bool stop = false;
+    int turn_of = 0;             // which of the two plans is the phase's
+    if (threadIdx.x == kThreads - 32) {
+        set_phase<BN>(plan[0], a, 0, 0, group, done);
+        ++done[0];
+    }
 
     for (int b = group; b < a.batch && !stop; b += a.groups) {
         {   // x_0 = g / (|g| + eps), scaled
@@ -633,10 +777,11 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
                 const int ch = i - row * a.chunks;
                 float v[8];
                 load_row8(a.in, a.in_dtype, a.in_vec, b * a.in_stride + row * a.in_ld, a.cols, ch, v);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = 8 * ch + e < a.cols ? v[e] * f : 0.0f;
+                Eight u;
+                u.set(make_float4(v[0], v[1], v[2], v[3]), make_float4(v[4], v[5], v[6], v[7]));
+                u.scale(pack2(f, f));
                 const long long o = b * a.x[0].stride + row * a.x[0].ld + 8 * ch;
-                put_planes8(v, a.x[0].hi + o, a.x[0].lo + o);
+                put_planes8(u, a.x[0].hi + o, a.x[0].lo + o);
             }
         }
         for (int phase = 0; phase < 3 * a.steps; ++phase) {
@@ -654,15 +799,15 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
                         wait_count(a.group_bar + group * kBarStride, met, &abort_flag, a.timeout_ns);
                     }
                 }
-                set_phase<BN>(ph, a, phase / 3, phase % 3, b, done);
-                ++done[phase % 3];
-                ph.stop = abort_flag;
+                stop_flag = abort_flag;
             }
             __syncthreads();
-            if (ph.stop) {
+            if (stop_flag) {   // the same for every thread
                 stop = true;
                 break;
             }
+            const Phase& ph = plan[turn_of];
+            turn_of ^= 1;
 
             const int first = ph.split > 1 ? cta / ph.split : cta, step = ph.split > 1 ? INT_MAX / 2 : a.ctas;
             const int part = ph.split > 1 ? cta % ph.split : 0;
@@ -670,12 +815,20 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
             const int k_from = stages * part / ph.split * kBK, k_to = stages * (part + 1) / ph.split * kBK;
             const int pass0 = JOINT ? 2 : 3 - a.products;
 
-            if (warp == 0) {
+            if (warp == kThreads / 32 - 1) {
+                // the next phase, of this matrix or of the group's next one
+                if (lane == 0) {
+                    const int next = phase + 1 < 3 * a.steps ? phase + 1 : 0;
+                    set_phase<BN>(plan[turn_of], a, next / 3, next % 3, next > 0 ? b : b + a.groups, done);
+                    ++done[next % 3];
+                }
+                __syncwarp();
+            } else if (warp == 0) {
                 if (lane == 0) {
                     fence_proxy_async_global();
                     bool ok = true;
                     for (int t = first; ok && t < ph.tiles; t += step) {
-                        const Tile tl = tile_of<BN>(ph, t);
+                        const Tile tl = t == first ? ph.first : tile_of<BN>(ph, t);
                         const int am = mn_from(ph.a_mode, S::kSb, tl.m0), bm = mn_from(ph.b_mode, S::kSb, tl.n0);
                         for (int pass = pass0; ok && pass < 3; ++pass) {
                             const CUtensorMap* ma = ph.a + (pass == 0);
@@ -709,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
                 if (lane == 0) {
                     bool ok = true;
                     for (int t = first; ok && t < ph.tiles; t += step) {
-                        const Tile tl = tile_of<BN>(ph, t);
+                        const Tile tl = t == first ? ph.first : tile_of<BN>(ph, t);
                         const int am = mn_from(ph.a_mode, S::kSb, tl.m0), bm = mn_from(ph.b_mode, S::kSb, tl.n0);
                         if (count >= 2 && !mbar_wait_bounded(&acc_empty[acc.i], acc.parity ^ 1, &abort_flag, a.timeout_ns)) {
                             abort_flag = 1;
@@ -755,35 +908,26 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
             } else {
                 const int quarter = warp & 3;         // the TMEM lanes this warp may read
                 const int half = (warp - 2) >> 2;     // its half of the columns
+                const Results res(ph);
+#pragma unroll 1
                 for (int t = first; t < ph.tiles; t += step) {
-                    const Tile tl = tile_of<BN>(ph, t);
+                    const Tile tl = t == first ? ph.first : tile_of<BN>(ph, t);
                     if (!mbar_wait_bounded(&acc_full[acc.i], acc.parity, &abort_flag, a.timeout_ns)) {
                         abort_flag = 1;
                         if (ph.split == 1) break;
                         // the other warps of the CTA still meet below
                     }
                     tc_fence_after();
-                    const int row = tl.m0 + quarter * 32 + lane;
                     const uint32_t d = tmem + acc.i * S::kAccCols + (static_cast<uint32_t>(quarter * 32) << 16);
-                    // [unit of eight columns][row][8] of this CTA
-                    float* mine = a.partial + static_cast<long long>(blockIdx.x) * (kBM * BN) + (quarter * 32 + lane) * 8;
+                    if (ph.split == 1) {
+                        tile_results<BN, JOINT>(res, ph, tl, d, quarter, half, lane, turn);
+                    } else {
+                        // this part's sums, [group of eight columns][row][8]
+                        float* mine = a.partial + static_cast<long long>(blockIdx.x) * (kBM * BN) + (quarter * 32 + lane) * 8;
 #pragma unroll 1
-                    for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 32) {
-                        const int col = tl.n0 + c;
-                        if (col >= ph.n) break;
-                        Addend x[4];
-                        if (ph.split == 1) load_addends<4>(ph, row, col, x);
-                        float v[32];
-                        tmem_load32(d + c, v);
-                        if (JOINT) {
-                            float w[32];
-                            tmem_load32(d + BN + c, w);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] += w[i];
-                        }
-                        if (ph.split == 1) {
-                            finish<4>(a, ph, b, row, col, x, v);
-                        } else {
+                        for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 32) {
+                            float v[32];
+                            load_sums<BN, JOINT>(d + c, v);
 #pragma unroll
                             for (int i = 0; i < 8; ++i)
                                 __stcg(reinterpret_cast<float4*>(mine + (c / 8 + i / 2) * (kBM * 8)) + (i & 1),
@@ -795,7 +939,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
                     if (lane == 0) mbar_arrive(&acc_empty[acc.i]);
                     acc.next();
                     if (ph.split == 1) continue;
-                    // all parts of the tile are there: add up this one's columns, part by part
+                    // the tile's parts meet, then each adds up its columns
                     __threadfence();
                     named_bar_sync(1, kEpiWarps * 32);
                     if (threadIdx.x == 64 && !abort_flag) {
@@ -805,25 +949,8 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
                     }
                     named_bar_sync(1, kEpiWarps * 32);
                     if (abort_flag) break;
-                    const float* parts = mine - static_cast<long long>(part) * (kBM * BN);
-#pragma unroll 1
-                    for (int u = 2 * part + half; u < BN / 8; u += 2 * ph.split) {
-                        const int col = tl.n0 + 8 * u;
-                        if (col >= ph.n) break;
-                        Addend x[1];
-                        load_addends<1>(ph, row, col, x);
-                        float v[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-#pragma unroll 4
-                        for (int q = 0; q < ph.split; ++q) {
-                            const float4* p = reinterpret_cast<const float4*>(parts + static_cast<long long>(q) * (kBM * BN) + u * (kBM * 8));
-                            const float4 y = __ldcg(p), z = __ldcg(p + 1);
-                            v[0] += y.x, v[1] += y.y, v[2] += y.z, v[3] += y.w;
-                            v[4] += z.x, v[5] += z.y, v[6] += z.z, v[7] += z.w;
-                        }
-                        finish<1>(a, ph, b, row, col, x, v);
-                    }
+                    split_results<BN>(res, ph, tl, a.partial + static_cast<long long>(blockIdx.x - part) * (kBM * BN), part,
+                                      ph.split, threadIdx.x - 64);
                 }
             }
         }
@@ -923,8 +1050,8 @@ double phase_us(long long tiles, int stages, int passes, double stage_us, int ct
     if (tiles < ctas) {
         int most = static_cast<int>(ctas / tiles);
         if (most > stages) most = stages;
-        if (most > 16) most = 16;
-        for (int q = 2; q <= most; ++q) {
+        if (most > kMaxSplit) most = kMaxSplit;
+        for (int q = 2; q <= most; q *= 2) {
             const double us = static_cast<double>((stages + q - 1) / q) * passes * stage_us + kTileEnd + kSplitEnd;
             if (us < best) best = us, split = q;
         }
@@ -1166,7 +1293,7 @@ cudaError_t launch_ns(const NsArgs& a, cudaStream_t st)
         k.in_ld = a.cols;
         k.in_stride = mu.u_stride;
         k.in_vec = a.cols % 4 == 0;
-        k.epi = EPI_MUON;
+        k.res = RES_MUON;
         k.master = a.master;
         k.lp = a.lp;
         k.out_dtype = a.lp_dtype;
@@ -1183,7 +1310,7 @@ cudaError_t launch_ns(const NsArgs& a, cudaStream_t st)
         k.in_ld = a.in_ld;
         k.in_stride = a.in_stride;
         k.in_vec = reinterpret_cast<uintptr_t>(a.in) % 16 == 0 && a.in_ld % v == 0 && a.in_stride % v == 0;
-        k.epi = EPI_OUT;
+        k.res = RES_OUT;
         k.out = a.out;
         k.out_dtype = a.out_dtype;
         k.out_ld = a.out_ld;
