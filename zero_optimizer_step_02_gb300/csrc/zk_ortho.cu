@@ -36,7 +36,7 @@ constexpr float kScale = 4096.0f;
 constexpr float kInvScale = 1.0f / 4096.0f;
 constexpr int kBM = 128;       // output rows of a CTA's tile (TMEM lanes)
 constexpr int kBK = 64;        // depth of a pipeline stage: 128 bytes, one swizzle line
-constexpr int kBox = 64;       // TMA boxes are 64 x 64 values, 8 KB, whichever side is the depth
+constexpr int kBox = 128;      // rows (columns) of an operand that one TMA copy brings, 16 KB
 constexpr int kBoxBytes = kBox * kBK * 2;
 constexpr int kThreads = 352;  // producer, MMA, eight epilogue warps, one that plans the next phase
 constexpr int kEpiWarps = 8;
@@ -50,6 +50,14 @@ constexpr unsigned kPoison = 0x80000000u;
 // contiguous (MN-major), or a symmetric matrix of which only the blocks of
 // `sb` x `sb` on and under the diagonal are stored
 enum { kMajorK = 0, kMajorMN = 1, kSymLower = 2 };
+// The maps of one plane.  `k`: {column, row, matrix} in boxes of 64 columns of
+// depth by 128 rows.  `mn`: {column of a panel, row, panel of 64 columns,
+// matrix} in boxes of two panels by 64 rows of depth (what a last panel holds
+// past the matrix only reaches result columns that do not exist).
+struct Maps {
+    CUtensorMap k, mn;
+};
+
 struct DevPlanes {
     __half* hi;
     __half* lo;                  // may be null
@@ -57,7 +65,7 @@ struct DevPlanes {
 };
 
 struct NsKernelArgs {
-    CUtensorMap xmap[2][2], gmap[2], pmap[2];   // hi and lo planes
+    Maps xmap[2][2], gmap[2], pmap[2];   // hi and lo planes
     DevPlanes x[2], g, p;
     int rows, cols, m, wide, batch;
     int steps, products;
@@ -94,8 +102,8 @@ struct Tile {
 
 // One product: alpha * A B^T + beta * addend over an m x n result.
 struct Phase {
-    const CUtensorMap* a;        // hi; lo follows
-    const CUtensorMap* b;
+    const Maps* a;               // hi; lo follows
+    const Maps* b;
     int a_mode, b_mode;
     int m, n, k;
     int lower;                   // only blocks on and under the diagonal
@@ -150,12 +158,15 @@ __device__ __forceinline__ int mn_from(int mode, int sb, int mn0)
 }
 
 template <int BOXES>
-__device__ __forceinline__ void load_operand(unsigned char* dst, const CUtensorMap* map, bool mn, int mn0, int k0, int b,
-                                             uint64_t* bar)
+__device__ __forceinline__ void load_operand(unsigned char* dst, const Maps* map, bool mn, int mn0, int k0, int b, uint64_t* bar)
 {
 #pragma unroll
-    for (int h = 0; h < BOXES; ++h)
-        tma_load_3d(dst + h * kBoxBytes, map, mn ? mn0 + h * kBox : k0, mn ? k0 : mn0 + h * kBox, b, bar);
+    for (int h = 0; h < BOXES; ++h) {
+        if (mn)
+            tma_load_4d(dst + h * kBoxBytes, &map->mn, 0, k0, mn0 / 64 + 2 * h, b, bar);
+        else
+            tma_load_3d(dst + h * kBoxBytes, &map->k, k0, mn0 + h * kBox, b, bar);
+    }
 }
 
 // a place in the ring of stages: the slot, and the parity of its current use
@@ -633,7 +644,7 @@ __device__ __forceinline__ void set_phase(Phase& ph, const NsKernelArgs& a, int 
 {
     const DevPlanes& xi = a.x[s & 1];
     const DevPlanes& xo = a.x[(s & 1) ^ 1];
-    const CUtensorMap* xm = a.xmap[s & 1];
+    const Maps* xm = a.xmap[s & 1];
     constexpr int SB = MmShape<BN, false>::kSb;
     const bool last = s + 1 == a.steps;
     ph.lower = kind < 2;
@@ -824,87 +835,91 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
                 }
                 __syncwarp();
             } else if (warp == 0) {
-                if (lane == 0) {
-                    fence_proxy_async_global();
-                    bool ok = true;
-                    for (int t = first; ok && t < ph.tiles; t += step) {
-                        const Tile tl = t == first ? ph.first : tile_of<BN>(ph, t);
-                        const int am = mn_from(ph.a_mode, S::kSb, tl.m0), bm = mn_from(ph.b_mode, S::kSb, tl.n0);
-                        for (int pass = pass0; ok && pass < 3; ++pass) {
-                            const CUtensorMap* ma = ph.a + (pass == 0);
-                            const CUtensorMap* mb = ph.b + (pass == 1);
-                            for (int k0 = k_from; k0 < k_to; k0 += kBK) {
-                                if (count >= S::kStages && !mbar_wait_bounded(&empty[slot.i], slot.parity ^ 1, &abort_flag, a.timeout_ns)) {
-                                    abort_flag = 1;
-                                    ok = false;
-                                    break;
-                                }
-                                if (!a.starve) {
-                                    unsigned char* p = ring + slot.i * S::kStageBytes;
-                                    uint64_t* bar = &full[slot.i];
-                                    mbar_arrive_expect_tx(bar, S::kStageBytes);
-                                    load_operand<kBM / kBox>(p, ma, k0 >= am, tl.m0, k0, b, bar);
-                                    load_operand<BN / kBox>(p + S::kABytes, mb, k0 >= bm, tl.n0, k0, b, bar);
-                                    if (JOINT) {
-                                        p += S::kABytes + S::kBBytes;
-                                        load_operand<kBM / kBox>(p, ma + 1, k0 >= am, tl.m0, k0, b, bar);
-                                        load_operand<BN / kBox>(p + S::kABytes, mb + 1, k0 >= bm, tl.n0, k0, b, bar);
-                                    }
-                                }
-                                slot.next();
-                                ++count;
+                // Whole warps walk these two loops, one lane of them issues: what
+                // the issued instructions need is then the same in all lanes and
+                // stays in uniform registers.
+                fence_proxy_async_global();
+                bool ok = true;
+                for (int t = first; ok && t < ph.tiles; t += step) {
+                    const Tile tl = t == first ? ph.first : tile_of<BN>(ph, t);
+                    const int am = mn_from(ph.a_mode, S::kSb, tl.m0), bm = mn_from(ph.b_mode, S::kSb, tl.n0);
+                    for (int pass = pass0; ok && pass < 3; ++pass) {
+                        const Maps* ma = ph.a + (pass == 0);
+                        const Maps* mb = ph.b + (pass == 1);
+                        for (int k0 = k_from; k0 < k_to; k0 += kBK) {
+                            if (count >= S::kStages &&
+                                !__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&empty[slot.i], slot.parity ^ 1, &abort_flag, a.timeout_ns))) {
+                                abort_flag = 1;
+                                ok = false;
+                                break;
                             }
+                            if (!a.starve && elect_one()) {
+                                unsigned char* p = ring + slot.i * S::kStageBytes;
+                                uint64_t* bar = &full[slot.i];
+                                mbar_arrive_expect_tx(bar, S::kStageBytes);
+                                load_operand<kBM / kBox>(p, ma, k0 >= am, tl.m0, k0, b, bar);
+                                load_operand<BN / kBox>(p + S::kABytes, mb, k0 >= bm, tl.n0, k0, b, bar);
+                                if (JOINT) {
+                                    p += S::kABytes + S::kBBytes;
+                                    load_operand<kBM / kBox>(p, ma + 1, k0 >= am, tl.m0, k0, b, bar);
+                                    load_operand<BN / kBox>(p + S::kABytes, mb + 1, k0 >= bm, tl.n0, k0, b, bar);
+                                }
+                            }
+                            __syncwarp();
+                            slot.next();
+                            ++count;
                         }
                     }
                 }
-                __syncwarp();
             } else if (warp == 1) {
-                if (lane == 0) {
-                    bool ok = true;
-                    for (int t = first; ok && t < ph.tiles; t += step) {
-                        const Tile tl = t == first ? ph.first : tile_of<BN>(ph, t);
-                        const int am = mn_from(ph.a_mode, S::kSb, tl.m0), bm = mn_from(ph.b_mode, S::kSb, tl.n0);
-                        if (count >= 2 && !mbar_wait_bounded(&acc_empty[acc.i], acc.parity ^ 1, &abort_flag, a.timeout_ns)) {
-                            abort_flag = 1;
-                            break;
-                        }
-                        ++count;
-                        tc_fence_after();
-                        const uint32_t d = tmem + acc.i * S::kAccCols;
-                        bool more = false;   // false: the accumulator starts anew
-                        for (int pass = pass0; ok && pass < 3; ++pass) {
-                            for (int k0 = k_from; k0 < k_to; k0 += kBK) {
-                                if (!mbar_wait_bounded(&full[slot.i], slot.parity, &abort_flag, a.timeout_ns)) {
-                                    abort_flag = 1;
-                                    ok = false;
-                                    break;
-                                }
-                                tc_fence_after();
-                                const bool a_mn = k0 >= am, b_mn = k0 >= bm;
-                                const uint32_t idesc = instr_desc(kBM, BN, a_mn, b_mn);
-                                const uint32_t p = smem_u32(ring + slot.i * S::kStageBytes);
-                                const uint64_t da = smem_desc(p), db = smem_desc(p + S::kABytes);
-                                // sixteen values of depth: 32 bytes along a line, or sixteen lines
-                                const uint32_t sa = a_mn ? 2048 >> 4 : 32 >> 4, sbb = b_mn ? 2048 >> 4 : 32 >> 4;
+                const uint32_t ring_at = smem_u32(ring);
+                bool ok = true;
+                for (int t = first; ok && t < ph.tiles; t += step) {
+                    const Tile tl = t == first ? ph.first : tile_of<BN>(ph, t);
+                    const int am = mn_from(ph.a_mode, S::kSb, tl.m0), bm = mn_from(ph.b_mode, S::kSb, tl.n0);
+                    if (count >= 2 && !__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&acc_empty[acc.i], acc.parity ^ 1, &abort_flag, a.timeout_ns))) {
+                        abort_flag = 1;
+                        break;
+                    }
+                    ++count;
+                    tc_fence_after();
+                    const uint32_t d = tmem + acc.i * S::kAccCols;
+                    uint32_t more = 0;   // 0: the accumulator starts anew
+                    for (int pass = pass0; ok && pass < 3; ++pass) {
+                        for (int k0 = k_from; k0 < k_to; k0 += kBK) {
+                            if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[slot.i], slot.parity, &abort_flag, a.timeout_ns))) {
+                                abort_flag = 1;
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            const bool a_mn = k0 >= am, b_mn = k0 >= bm;
+                            const uint32_t idesc = instr_desc(kBM, BN, a_mn, b_mn);
+                            const uint32_t p = ring_at + slot.i * S::kStageBytes;
+                            const uint32_t da = smem_desc_lo(p), db = smem_desc_lo(p + S::kABytes);
+                            // sixteen values of depth: 32 bytes along a line, or sixteen lines
+                            const uint32_t sa = a_mn ? 2048 >> 4 : 32 >> 4, sb = b_mn ? 2048 >> 4 : 32 >> 4;
+                            if (elect_one()) {
 #pragma unroll
                                 for (int k = 0; k < kBK / 16; ++k) {
-                                    mma_f16(d, da + k * sa, db + k * sbb, idesc, more || k > 0);
+                                    mma_f16(d, da + k * sa, db + k * sb, idesc, k > 0 ? 1u : more);
                                     if (JOINT) {
                                         constexpr uint32_t kLo = (S::kABytes + S::kBBytes) >> 4;
-                                        mma_f16(d + BN, da + kLo + k * sa, db + k * sbb, idesc, more || k > 0);
-                                        mma_f16(d + BN, da + k * sa, db + kLo + k * sbb, idesc, true);
+                                        mma_f16(d + BN, da + kLo + k * sa, db + k * sb, idesc, k > 0 ? 1u : more);
+                                        mma_f16(d + BN, da + k * sa, db + kLo + k * sb, idesc, 1u);
                                     }
                                 }
-                                more = true;
                                 mma_commit(&empty[slot.i]);
-                                slot.next();
                             }
+                            __syncwarp();
+                            more = 1;
+                            slot.next();
                         }
-                        if (ok) mma_commit(&acc_full[acc.i]);
-                        acc.next();
                     }
+                    if (ok && elect_one()) mma_commit(&acc_full[acc.i]);
+                    __syncwarp();
+                    acc.next();
                 }
-                __syncwarp();
             } else {
                 const int quarter = warp & 3;         // the TMEM lanes this warp may read
                 const int half = (warp - 2) >> 2;     // its half of the columns
@@ -964,7 +979,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
             mma_commit(&drain);   // TMEM is given back only after the last MMA
             mbar_wait_bounded(&drain, 0, nullptr, 1000000000ull);
         }
@@ -1007,16 +1022,22 @@ struct Planes {
     long long ld = 0, stride = 0;
 };
 
-bool encode(CUtensorMap* map, const Planes& p, const __half* plane, int batch)
+bool encode(Maps* map, const Planes& p, const __half* plane, int batch)
 {
     const EncodeFn fn = encoder();
     if (fn == nullptr) return false;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.cols), static_cast<cuuint64_t>(p.rows), static_cast<cuuint64_t>(batch)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(p.ld) * 2, static_cast<cuuint64_t>(p.stride) * 2};
-    const cuuint32_t box[3] = {kBox, kBox, 1}, unit[3] = {1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<__half*>(plane), dims, strides, box, unit,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint64_t rows = static_cast<cuuint64_t>(p.rows), cols = static_cast<cuuint64_t>(p.cols), n = static_cast<cuuint64_t>(batch);
+    const cuuint64_t ld = static_cast<cuuint64_t>(p.ld) * 2, stride = static_cast<cuuint64_t>(p.stride) * 2;
+    const cuuint32_t unit[4] = {1, 1, 1, 1};
+    const cuuint64_t kdims[3] = {cols, rows, n}, kstrides[2] = {ld, stride};
+    const cuuint32_t kbox[3] = {kBK, kBox, 1};
+    const cuuint64_t mdims[4] = {64, rows, (cols + 63) / 64, n}, mstrides[3] = {ld, 128, stride};
+    const cuuint32_t mbox[4] = {64, kBK, kBox / 64, 1};
+    void* at = const_cast<__half*>(plane);
+    return fn(&map->k, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, at, kdims, kstrides, kbox, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS &&
+           fn(&map->mn, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, at, mdims, mstrides, mbox, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // How a call is cut up.
@@ -1029,10 +1050,12 @@ struct Plan {
 
 // Times of a CTA, in us, that the choice goes by (measured): a 64-deep stage
 // of 128 x 256 (48 KB of operands) and of 128 x 128 (32 KB; both planes: 64),
-// a tile's results after its last MMA, the exchange of partial sums, the
-// meeting of a group.
+// the results of a tile (beside the next tile's products), the exchange of
+// partial sums, the meeting of a group and the first copies after it.
 constexpr double kStage256 = 0.39, kStage128 = 0.25, kStageJoint = 0.46;
-constexpr double kTileEnd = 2.0, kSplitEnd = 3.0, kMeet = 1.5, kMeetAlone = 0.5;
+constexpr double kResults256 = 4.8, kResults128 = 2.4;
+constexpr double kSplit256 = 8.4, kSplit128 = 4.7;
+constexpr double kMeet = 3.2, kMeetAlone = 2.2;
 
 long long sym_tiles(int m, int bn)
 {
@@ -1043,18 +1066,16 @@ long long sym_tiles(int m, int bn)
 
 // the time of one product with `tiles` tiles and `stages` stages each on
 // `ctas` CTAs, and how many of them share a tile
-double phase_us(long long tiles, int stages, int passes, double stage_us, int ctas, int& split)
+double phase_us(long long tiles, int stages, int passes, double stage_us, int bn, int ctas, int& split)
 {
+    const double end = bn == 256 ? kResults256 : kResults128, join = bn == 256 ? kSplit256 : kSplit128;
+    const double mma = stages * passes * stage_us;
+    const long long rounds = (tiles + ctas - 1) / ctas;
+    double best = mma + (rounds - 1) * (mma > end ? mma : end) + end;
     split = 1;
-    double best = static_cast<double>((tiles + ctas - 1) / ctas) * stages * passes * stage_us + kTileEnd;
-    if (tiles < ctas) {
-        int most = static_cast<int>(ctas / tiles);
-        if (most > stages) most = stages;
-        if (most > kMaxSplit) most = kMaxSplit;
-        for (int q = 2; q <= most; q *= 2) {
-            const double us = static_cast<double>((stages + q - 1) / q) * passes * stage_us + kTileEnd + kSplitEnd;
-            if (us < best) best = us, split = q;
-        }
+    for (int q = 2; q <= kMaxSplit && q <= stages && tiles * q <= ctas; q *= 2) {
+        const double us = static_cast<double>((stages + q - 1) / q) * passes * stage_us + join + end / q;
+        if (us < best) best = us, split = q;
     }
     return best;
 }
@@ -1082,9 +1103,9 @@ Plan plan_of(int rows, int cols, int batch, int products, int sms)
             for (int pass = 0; pass < 2; ++pass) {
                 // as they are, then alone: without the meetings
                 if (pass == 1) p.ctas = 1;
-                const double us = phase_us(sym, (n + kBK - 1) / kBK, passes, st, p.ctas, p.split[0]) +
-                                  phase_us(sym, (m + kBK - 1) / kBK, passes, st, p.ctas, p.split[1]) +
-                                  phase_us(up, (m + kBK - 1) / kBK, passes, st, p.ctas, p.split[2]);
+                const double us = phase_us(sym, (n + kBK - 1) / kBK, passes, st, bn, p.ctas, p.split[0]) +
+                                  phase_us(sym, (m + kBK - 1) / kBK, passes, st, bn, p.ctas, p.split[1]) +
+                                  phase_us(up, (m + kBK - 1) / kBK, passes, st, bn, p.ctas, p.split[2]);
                 p.us = turns * (us + 3 * (p.ctas > 1 ? kMeet : kMeetAlone));
                 if (best.bn == 0 || p.us < best.us) best = p;
             }
@@ -1183,7 +1204,7 @@ cudaError_t launch_products(const Plan& p, const NsKernelArgs& a, cudaStream_t s
     return p.joint ? launch_ns_as<128, true>(a, st) : launch_ns_as<128, false>(a, st);
 }
 
-bool set_planes(DevPlanes& d, CUtensorMap* maps, const Planes& p, int batch)
+bool set_planes(DevPlanes& d, Maps* maps, const Planes& p, int batch)
 {
     d.hi = p.hi;
     d.lo = p.lo;

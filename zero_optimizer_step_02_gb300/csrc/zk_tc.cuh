@@ -18,7 +18,7 @@ __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* m)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
 }
 
-// One box of a rank-3 tensor {x, y, z} into this CTA's shared memory, counted
+// One box of a rank-3 (rank-4) tensor at {x, y, z} ({x, y, z, w}) into this CTA's shared memory, counted
 // on `bar`.  x * element size must be a multiple of 16 bytes; what lies
 // outside the tensor arrives as zeros (and is counted in full).
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, int x, int y, int z, uint64_t* bar)
@@ -27,6 +27,15 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, int
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, int x, int y, int z, int w, uint64_t* bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
         : "memory");
 }
 
@@ -95,11 +104,9 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32])
 // of 64 16-bit values (128 bytes), eight-row groups 1024 bytes apart; an
 // MN-major tile is panels of 64 rows/columns, one K index per 128-byte line,
 // eight K indices per 1024 bytes (stride), panels 8192 bytes apart (leading).
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr)
-{
-    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(8192 >> 4) << 16) |
-           (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
+// Low word: address and leading offset; high word: stride, version, swizzle.
+__device__ __forceinline__ uint32_t smem_desc_lo(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | ((8192u >> 4) << 16); }
+constexpr uint32_t kSmemDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 
 // kind::f16 instruction descriptor: fp16 operands, fp32 accumulator
 __host__ __device__ constexpr uint32_t instr_desc(int m, int n, bool a_mn, bool b_mn)
@@ -108,14 +115,29 @@ __host__ __device__ constexpr uint32_t instr_desc(int m, int n, bool a_mn, bool 
            (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate)
+// a, b: low words of the operands' descriptors
+__device__ __forceinline__ void mma_f16(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %5};\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
         "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kSmemDescHi)
         : "memory");
+}
+
+// one lane of the (converged) warp
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok));
+    return ok != 0;
 }
 
 // arrive on `bar` once every MMA this thread has issued so far is complete
