@@ -34,15 +34,15 @@ namespace {
 
 constexpr float kScale = 4096.0f;
 constexpr float kInvScale = 1.0f / 4096.0f;
-constexpr int kBM = 128;       // output rows of a CTA's tile (TMEM lanes)
+constexpr int kBM = 128;       // output rows of a CTA (TMEM lanes); a pair of CTAs shares tiles of twice as many
 constexpr int kBK = 64;        // depth of a pipeline stage: 128 bytes, one swizzle line
-constexpr int kBox = 128;      // rows (columns) of an operand that one TMA copy brings, 16 KB
+constexpr int kBox = 64;       // rows (columns) of an operand that one TMA copy brings, 8 KB
 constexpr int kBoxBytes = kBox * kBK * 2;
 constexpr int kThreads = 352;  // producer, MMA, eight epilogue warps, one that plans the next phase
 constexpr int kEpiWarps = 8;
 constexpr int kTurnBytes = 32 * 32 * 4;   // of an epilogue warp's 32 x 32 turning buffer
 constexpr int kMaxNsParts = 1024;
-constexpr int kStrip = 16;     // row tiles of a strip (see tile_of)
+constexpr int kStrip = 16;     // 128-row tiles of a strip (see tile_of)
 constexpr int kBarStride = 32; // words between the groups' barrier counters: a line each
 constexpr unsigned kPoison = 0x80000000u;
 
@@ -50,14 +50,6 @@ constexpr unsigned kPoison = 0x80000000u;
 // contiguous (MN-major), or a symmetric matrix of which only the blocks of
 // `sb` x `sb` on and under the diagonal are stored
 enum { kMajorK = 0, kMajorMN = 1, kSymLower = 2 };
-// The maps of one plane.  `k`: {column, row, matrix} in boxes of 64 columns of
-// depth by 128 rows.  `mn`: {column of a panel, row, panel of 64 columns,
-// matrix} in boxes of two panels by 64 rows of depth (what a last panel holds
-// past the matrix only reaches result columns that do not exist).
-struct Maps {
-    CUtensorMap k, mn;
-};
-
 struct DevPlanes {
     __half* hi;
     __half* lo;                  // may be null
@@ -65,11 +57,11 @@ struct DevPlanes {
 };
 
 struct NsKernelArgs {
-    Maps xmap[2][2], gmap[2], pmap[2];   // hi and lo planes
+    CUtensorMap xmap[2][2], gmap[2], pmap[2];   // hi and lo planes
     DevPlanes x[2], g, p;
     int rows, cols, m, wide, batch;
     int steps, products;
-    int groups, ctas;            // CTAs of a group; a group takes every groups-th matrix
+    int groups, ctas;            // CTAs of a group (CG = 2: pairs); a group takes every groups-th matrix
     int split[3];                // CTAs that share a tile's depth: for G, P and x
     float coef[kNsMaxSteps][3];
     // x_0
@@ -102,8 +94,8 @@ struct Tile {
 
 // One product: alpha * A B^T + beta * addend over an m x n result.
 struct Phase {
-    const Maps* a;               // hi; lo follows
-    const Maps* b;
+    const CUtensorMap* a;               // hi; lo follows
+    const CUtensorMap* b;
     int a_mode, b_mode;
     int m, n, k;
     int lower;                   // only blocks on and under the diagonal
@@ -123,30 +115,34 @@ struct Phase {
     float decay, step;
 };
 
+// side of the blocks in which a symmetric matrix is stored
+__host__ __device__ constexpr int sym_block(int cg, int bn) { return bn > kBM * cg ? bn : kBM * cg; }
+
 // Tile t of a phase.  Lower-triangle phases number the tiles of block row I
 // (sb rows, (I + 1) * sb columns) after those of the rows above.  Others go in
 // strips of kStrip row tiles, column by column: the tiles in flight at a time
 // form a near-square block, whose operands stay in L2.
-template <int BN>
+template <int CG, int BN>
 __device__ __forceinline__ Tile tile_of(const Phase& a, int t)
 {
+    constexpr int BM = kBM * CG, kStripTiles = kStrip / CG;
     Tile r;
     if (!a.lower) {
-        const int strip = t / (kStrip * a.tiles_n), first = strip * kStrip;
-        const int rows = a.tiles_m - first < kStrip ? a.tiles_m - first : kStrip;
+        const int strip = t / (kStripTiles * a.tiles_n), first = strip * kStripTiles;
+        const int rows = a.tiles_m - first < kStripTiles ? a.tiles_m - first : kStripTiles;
         t -= first * a.tiles_n;
-        r.m0 = (first + t % rows) * kBM;
+        r.m0 = (first + t % rows) * BM;
         r.n0 = t / rows * BN;
         return r;
     }
-    constexpr int SB = BN > kBM ? BN : kBM;
-    constexpr int kRows = SB / kBM, kCols = SB / BN;
+    constexpr int SB = sym_block(CG, BN);
+    constexpr int kRows = SB / BM, kCols = SB / BN;
     int i = static_cast<int>((sqrtf(1.0f + 8.0f * static_cast<float>(t / (kRows * kCols))) - 1.0f) * 0.5f);
     while (kRows * kCols * ((i + 1) * (i + 2) / 2) <= t) ++i;
     while (i > 0 && kRows * kCols * (i * (i + 1) / 2) > t) --i;
     t -= kRows * kCols * (i * (i + 1) / 2);
     const int width = (i + 1) * kCols;
-    r.m0 = (i * kRows + t / width) * kBM;
+    r.m0 = (i * kRows + t / width) * BM;
     r.n0 = t % width * BN;
     return r;
 }
@@ -157,16 +153,12 @@ __device__ __forceinline__ int mn_from(int mode, int sb, int mn0)
     return mode == kMajorK ? INT_MAX : mode == kMajorMN ? 0 : (mn0 & -sb) + sb;
 }
 
-template <int BOXES>
-__device__ __forceinline__ void load_operand(unsigned char* dst, const Maps* map, bool mn, int mn0, int k0, int b, uint64_t* bar)
+template <int CG, int BOXES>
+__device__ __forceinline__ void load_operand(unsigned char* dst, const CUtensorMap* map, bool mn, int mn0, int k0, int b, uint64_t* bar)
 {
 #pragma unroll
-    for (int h = 0; h < BOXES; ++h) {
-        if (mn)
-            tma_load_4d(dst + h * kBoxBytes, &map->mn, 0, k0, mn0 / 64 + 2 * h, b, bar);
-        else
-            tma_load_3d(dst + h * kBoxBytes, &map->k, k0, mn0 + h * kBox, b, bar);
-    }
+    for (int h = 0; h < BOXES; ++h)
+        tma_load_3d<CG>(dst + h * kBoxBytes, map, mn ? mn0 + h * kBox : k0, mn ? k0 : mn0 + h * kBox, b, bar);
 }
 
 // a place in the ring of stages: the slot, and the parity of its current use
@@ -404,11 +396,12 @@ __device__ __forceinline__ void tile_results(const Results& r, const Phase& ph, 
 
 // One part's share of a tile whose depth is split: the sums of all parts, in
 // their order, for BN / 8 / split groups of eight columns.  `parts` is the
-// first part's [group][row][8]; t: this thread of 256.
+// first part's [group][row][8], the next one lies `apart` of those further on;
+// t: this thread of 256.
 constexpr int kMaxSplit = 8;
 template <int BN>
 __device__ __forceinline__ void split_results(const Results& r, const Phase& ph, const Tile& tl, const float* parts, int part,
-                                              int split, int t)
+                                              int split, int apart, int t)
 {
     const int units = BN / 8 / split;
 #pragma unroll 1
@@ -424,9 +417,9 @@ __device__ __forceinline__ void split_results(const Results& r, const Phase& ph,
         for (int q = 0; q < split; q += 2) {   // an even number of parts
             Eight y, z;
             y.set(__ldcg(p), __ldcg(p + 1));
-            p += kBM * BN / 4;
+            p += apart * (kBM * BN / 4);
             z.set(__ldcg(p), __ldcg(p + 1));
-            p += kBM * BN / 4;
+            p += apart * (kBM * BN / 4);
 #pragma unroll
             for (int e = 0; e < 4; ++e) u.v[e] = add2(add2(u.v[e], y.v[e]), z.v[e]);
         }
@@ -627,25 +620,30 @@ __global__ void __launch_bounds__(256) muon_direction(const __grid_constant__ Mu
 // large one is added to no more often than with one product (each addition
 // drops low bits).  Otherwise a stage holds one plane of each, and three
 // products are three passes over the depth, the small ones first.
-template <int BN, bool JOINT>
+// CG = 2: a pair of CTAs shares a tile of 256 rows.  Each brings its 128 rows
+// of A and half of B's, and holds its rows' sums.  An SM takes 64 bytes a clock
+// from L2; alone, a 128 x 256 tile wants 96 to keep its tensor core busy, in a
+// pair 64.
+template <int CG, int BN, bool JOINT>
 struct MmShape {
-    static constexpr int kABytes = kBM * kBK * 2, kBBytes = BN * kBK * 2;
+    static constexpr int kABytes = kBM * kBK * 2, kBBytes = BN / CG * kBK * 2;
     static constexpr int kStageBytes = (kABytes + kBBytes) * (JOINT ? 2 : 1);
-    static constexpr int kStages = JOINT ? 3 : BN == 256 ? 4 : 6;
+    static constexpr int kRing = 192 * 1024;
+    static constexpr int kStages = kRing / kStageBytes;
     static constexpr int kAccCols = BN * (JOINT ? 2 : 1);   // of one of the two TMEM buffers
     static constexpr int kSmem = kStages * kStageBytes + kEpiWarps * kTurnBytes + 1024;   // + alignment of the ring
-    static constexpr int kSb = BN > kBM ? BN : kBM;
+    static constexpr int kSb = sym_block(CG, BN);
 };
 
 // Phase `kind` (0: G = x x^T, 1: P = b G + c G G, 2: x <- a x + P x) of step s
 // of matrix b.
-template <int BN>
+template <int CG, int BN>
 __device__ __forceinline__ void set_phase(Phase& ph, const NsKernelArgs& a, int s, int kind, int b, const unsigned (&done)[3])
 {
     const DevPlanes& xi = a.x[s & 1];
     const DevPlanes& xo = a.x[(s & 1) ^ 1];
-    const Maps* xm = a.xmap[s & 1];
-    constexpr int SB = MmShape<BN, false>::kSb;
+    const CUtensorMap* xm = a.xmap[s & 1];
+    constexpr int SB = sym_block(CG, BN), BM = kBM * CG;
     const bool last = s + 1 == a.steps;
     ph.lower = kind < 2;
     ph.res = RES_PLANES;
@@ -702,35 +700,35 @@ __device__ __forceinline__ void set_phase(Phase& ph, const NsKernelArgs& a, int 
     }
     ph.out.hi += b * ph.out.stride;
     if (ph.out.lo != nullptr) ph.out.lo += b * ph.out.stride;
-    ph.tiles_m = (ph.m + kBM - 1) / kBM;
+    ph.tiles_m = (ph.m + BM - 1) / BM;
     ph.tiles_n = (ph.n + BN - 1) / BN;
     const int blocks = (a.m + SB - 1) / SB;
-    const int sym = (SB / kBM) * (SB / BN) * (blocks * (blocks + 1) / 2);
-    const int up = ((a.rows + kBM - 1) / kBM) * ((a.cols + BN - 1) / BN);
+    const int sym = (SB / BM) * (SB / BN) * (blocks * (blocks + 1) / 2);
+    const int up = ((a.rows + BM - 1) / BM) * ((a.cols + BN - 1) / BN);
     ph.tiles = ph.lower ? sym : up;
     ph.split = a.split[kind];
     // a tile's counter has been raised by every earlier phase that had the tile
-    const int t = blockIdx.x % a.ctas / ph.split;
+    const int unit = blockIdx.x % a.ctas / CG, t = unit / ph.split;
     ph.tile_target = ph.split;
     for (int q = 0; q < 3; ++q)
         if (a.split[q] > 1 && t < (q < 2 ? sym : up)) ph.tile_target += done[q] * a.split[q];
-    const int first = ph.split > 1 ? t : blockIdx.x % a.ctas;
-    if (first < ph.tiles) ph.first = tile_of<BN>(ph, first);
+    const int first = ph.split > 1 ? t : unit;
+    if (first < ph.tiles) ph.first = tile_of<CG, BN>(ph, first);
 }
 
 // The whole iteration in one launch.  The grid is `groups` of `ctas` CTAs, all
 // resident (a cooperative launch); a group takes its matrices one after the
 // other and meets at a counter in memory between products.  Within a product
-// the CTAs share the tiles, or, where there are fewer tiles than CTAs, each
-// tile's depth (its parts meet at a counter of the tile and each adds up its
-// share of the columns, in order).  Within a CTA a producer thread keeps a
+// the CTAs (CG = 2: the pairs) share the tiles, or, where there are fewer
+// tiles than units, each tile's depth (its parts meet at a counter of the tile
+// and each adds up its share of the columns, in order).  Within a CTA a producer thread keeps a
 // ring of 64-deep operand tiles full by TMA, one thread issues the MMAs into
 // one of two TMEM accumulators, and eight warps turn the other one into
 // results.
-template <int BN, bool JOINT>
+template <int CG, int BN, bool JOINT>
 __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__ NsKernelArgs a)
 {
-    using S = MmShape<BN, JOINT>;
+    using S = MmShape<CG, BN, JOINT>;
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint64_t full[S::kStages], empty[S::kStages], acc_full[2], acc_empty[2], drain;
     __shared__ uint32_t tmem_base;
@@ -741,6 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
     unsigned char* ring = smem_raw + (1024 - (smem_u32(smem_raw) & 1023u)) % 1024;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = blockIdx.x / a.ctas, cta = blockIdx.x % a.ctas;
+    const int rank = CG == 2 ? static_cast<int>(cluster_rank()) : 0, unit = cta / CG, units = a.ctas / CG;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kStages; ++i) {
@@ -749,15 +748,16 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], kEpiWarps);
+            mbar_init(&acc_empty[i], kEpiWarps * CG);
         }
         mbar_init(&drain, 1);
         abort_flag = 0;
         fence_barrier_init();
     }
-    if (warp == 1) tmem_alloc(&tmem_base, 2 * S::kAccCols);
+    if (warp == 1) tmem_alloc<CG>(&tmem_base, 2 * S::kAccCols);
     tc_fence_before();
     __syncthreads();
+    if (CG == 2) pair_sync();   // the other CTA's barriers are there
     tc_fence_after();
     const uint32_t tmem = tmem_base;
 
@@ -772,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
     bool stop = false;
     int turn_of = 0;             // which of the two plans is the phase's
     if (threadIdx.x == kThreads - 32) {
-        set_phase<BN>(plan[0], a, 0, 0, group, done);
+        set_phase<CG, BN>(plan[0], a, 0, 0, group, done);
         ++done[0];
     }
 
@@ -820,8 +820,8 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
             const Phase& ph = plan[turn_of];
             turn_of ^= 1;
 
-            const int first = ph.split > 1 ? cta / ph.split : cta, step = ph.split > 1 ? INT_MAX / 2 : a.ctas;
-            const int part = ph.split > 1 ? cta % ph.split : 0;
+            const int first = ph.split > 1 ? unit / ph.split : unit, step = ph.split > 1 ? INT_MAX / 2 : units;
+            const int part = ph.split > 1 ? unit % ph.split : 0;
             const int stages = (ph.k + kBK - 1) / kBK;
             const int k_from = stages * part / ph.split * kBK, k_to = stages * (part + 1) / ph.split * kBK;
             const int pass0 = JOINT ? 2 : 3 - a.products;
@@ -830,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
                 // the next phase, of this matrix or of the group's next one
                 if (lane == 0) {
                     const int next = phase + 1 < 3 * a.steps ? phase + 1 : 0;
-                    set_phase<BN>(plan[turn_of], a, next / 3, next % 3, next > 0 ? b : b + a.groups, done);
+                    set_phase<CG, BN>(plan[turn_of], a, next / 3, next % 3, next > 0 ? b : b + a.groups, done);
                     ++done[next % 3];
                 }
                 __syncwarp();
@@ -841,14 +841,15 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
                 fence_proxy_async_global();
                 bool ok = true;
                 for (int t = first; ok && t < ph.tiles; t += step) {
-                    const Tile tl = t == first ? ph.first : tile_of<BN>(ph, t);
+                    const Tile tl = t == first ? ph.first : tile_of<CG, BN>(ph, t);
                     const int am = mn_from(ph.a_mode, S::kSb, tl.m0), bm = mn_from(ph.b_mode, S::kSb, tl.n0);
+                    const int m0 = tl.m0 + rank * kBM, n0 = tl.n0 + rank * (BN / CG);   // this CTA's share
                     for (int pass = pass0; ok && pass < 3; ++pass) {
-                        const Maps* ma = ph.a + (pass == 0);
-                        const Maps* mb = ph.b + (pass == 1);
+                        const CUtensorMap* ma = ph.a + (pass == 0);
+                        const CUtensorMap* mb = ph.b + (pass == 1);
                         for (int k0 = k_from; k0 < k_to; k0 += kBK) {
                             if (count >= S::kStages &&
-                                !__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&empty[slot.i], slot.parity ^ 1, &abort_flag, a.timeout_ns))) {
+                                !__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&empty[slot.i], slot.parity ^ 1, &abort_flag, a.timeout_ns))) {
                                 abort_flag = 1;
                                 ok = false;
                                 break;
@@ -856,13 +857,14 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
                             if (!a.starve && elect_one()) {
                                 unsigned char* p = ring + slot.i * S::kStageBytes;
                                 uint64_t* bar = &full[slot.i];
-                                mbar_arrive_expect_tx(bar, S::kStageBytes);
-                                load_operand<kBM / kBox>(p, ma, k0 >= am, tl.m0, k0, b, bar);
-                                load_operand<BN / kBox>(p + S::kABytes, mb, k0 >= bm, tl.n0, k0, b, bar);
+                                // the leader's barrier counts both CTAs' bytes
+                                if (rank == 0) mbar_arrive_expect_tx(bar, CG * S::kStageBytes);
+                                load_operand<CG, kBM / kBox>(p, ma, k0 >= am, m0, k0, b, bar);
+                                load_operand<CG, BN / CG / kBox>(p + S::kABytes, mb, k0 >= bm, n0, k0, b, bar);
                                 if (JOINT) {
                                     p += S::kABytes + S::kBBytes;
-                                    load_operand<kBM / kBox>(p, ma + 1, k0 >= am, tl.m0, k0, b, bar);
-                                    load_operand<BN / kBox>(p + S::kABytes, mb + 1, k0 >= bm, tl.n0, k0, b, bar);
+                                    load_operand<CG, kBM / kBox>(p, ma + 1, k0 >= am, m0, k0, b, bar);
+                                    load_operand<CG, BN / CG / kBox>(p + S::kABytes, mb + 1, k0 >= bm, n0, k0, b, bar);
                                 }
                             }
                             __syncwarp();
@@ -873,11 +875,11 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
                 }
             } else if (warp == 1) {
                 const uint32_t ring_at = smem_u32(ring);
-                bool ok = true;
+                bool ok = rank == 0;   // a pair's leader issues for both
                 for (int t = first; ok && t < ph.tiles; t += step) {
-                    const Tile tl = t == first ? ph.first : tile_of<BN>(ph, t);
+                    const Tile tl = t == first ? ph.first : tile_of<CG, BN>(ph, t);
                     const int am = mn_from(ph.a_mode, S::kSb, tl.m0), bm = mn_from(ph.b_mode, S::kSb, tl.n0);
-                    if (count >= 2 && !__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&acc_empty[acc.i], acc.parity ^ 1, &abort_flag, a.timeout_ns))) {
+                    if (count >= 2 && !__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&acc_empty[acc.i], acc.parity ^ 1, &abort_flag, a.timeout_ns))) {
                         abort_flag = 1;
                         break;
                     }
@@ -887,14 +889,14 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
                     uint32_t more = 0;   // 0: the accumulator starts anew
                     for (int pass = pass0; ok && pass < 3; ++pass) {
                         for (int k0 = k_from; k0 < k_to; k0 += kBK) {
-                            if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[slot.i], slot.parity, &abort_flag, a.timeout_ns))) {
+                            if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&full[slot.i], slot.parity, &abort_flag, a.timeout_ns))) {
                                 abort_flag = 1;
                                 ok = false;
                                 break;
                             }
                             tc_fence_after();
                             const bool a_mn = k0 >= am, b_mn = k0 >= bm;
-                            const uint32_t idesc = instr_desc(kBM, BN, a_mn, b_mn);
+                            const uint32_t idesc = instr_desc(kBM * CG, BN, a_mn, b_mn);
                             const uint32_t p = ring_at + slot.i * S::kStageBytes;
                             const uint32_t da = smem_desc_lo(p), db = smem_desc_lo(p + S::kABytes);
                             // sixteen values of depth: 32 bytes along a line, or sixteen lines
@@ -902,21 +904,21 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
                             if (elect_one()) {
 #pragma unroll
                                 for (int k = 0; k < kBK / 16; ++k) {
-                                    mma_f16(d, da + k * sa, db + k * sb, idesc, k > 0 ? 1u : more);
+                                    mma_f16<CG>(d, da + k * sa, db + k * sb, idesc, k > 0 ? 1u : more);
                                     if (JOINT) {
                                         constexpr uint32_t kLo = (S::kABytes + S::kBBytes) >> 4;
-                                        mma_f16(d + BN, da + kLo + k * sa, db + k * sb, idesc, k > 0 ? 1u : more);
-                                        mma_f16(d + BN, da + k * sa, db + kLo + k * sb, idesc, 1u);
+                                        mma_f16<CG>(d + BN, da + kLo + k * sa, db + k * sb, idesc, k > 0 ? 1u : more);
+                                        mma_f16<CG>(d + BN, da + k * sa, db + kLo + k * sb, idesc, 1u);
                                     }
                                 }
-                                mma_commit(&empty[slot.i]);
+                                mma_commit<CG>(&empty[slot.i]);
                             }
                             __syncwarp();
                             more = 1;
                             slot.next();
                         }
                     }
-                    if (ok && elect_one()) mma_commit(&acc_full[acc.i]);
+                    if (ok && elect_one()) mma_commit<CG>(&acc_full[acc.i]);
                     __syncwarp();
                     acc.next();
                 }
@@ -926,8 +928,9 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
                 const Results res(ph);
 #pragma unroll 1
                 for (int t = first; t < ph.tiles; t += step) {
-                    const Tile tl = t == first ? ph.first : tile_of<BN>(ph, t);
-                    if (!mbar_wait_bounded(&acc_full[acc.i], acc.parity, &abort_flag, a.timeout_ns)) {
+                    Tile tl = t == first ? ph.first : tile_of<CG, BN>(ph, t);
+                    tl.m0 += rank * kBM;
+                    if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&acc_full[acc.i], acc.parity, &abort_flag, a.timeout_ns))) {
                         abort_flag = 1;
                         if (ph.split == 1) break;
                         // the other warps of the CTA still meet below
@@ -951,44 +954,51 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
                     }
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&acc_empty[acc.i]);
+                    if (lane == 0) {
+                        if (CG == 2)
+                            mbar_arrive_leader(&acc_empty[acc.i]);
+                        else
+                            mbar_arrive(&acc_empty[acc.i]);
+                    }
                     acc.next();
                     if (ph.split == 1) continue;
                     // the tile's parts meet, then each adds up its columns
                     __threadfence();
                     named_bar_sync(1, kEpiWarps * 32);
                     if (threadIdx.x == 64 && !abort_flag) {
-                        unsigned* bar = a.tile_bar + group * a.ctas + t;
+                        unsigned* bar = a.tile_bar + group * a.ctas + t * CG + rank;
                         raise_count(bar);
                         wait_count(bar, ph.tile_target, &abort_flag, a.timeout_ns);
                     }
                     named_bar_sync(1, kEpiWarps * 32);
                     if (abort_flag) break;
-                    split_results<BN>(res, ph, tl, a.partial + static_cast<long long>(blockIdx.x - part) * (kBM * BN), part,
-                                      ph.split, threadIdx.x - 64);
+                    split_results<BN>(res, ph, tl, a.partial + static_cast<long long>(blockIdx.x - part * CG) * (kBM * BN), part,
+                                      ph.split, CG, threadIdx.x - 64);
                 }
             }
         }
     }
     __syncthreads();
+    if (CG == 2) pair_sync();   // neither issues anything any more
     if (warp == 0) {
-        if (lane == 0 && abort_flag && !a.starve) {
-            // nothing of ours may still be landing when the CTA's memory goes away
+        if (lane == 0 && rank == 0 && abort_flag && !a.starve) {
+            // nothing of ours (nor, counted here, of the other CTA's) may still
+            // be landing when the memory goes away
             for (uint32_t i = count > S::kStages ? count - S::kStages : 0; i < count; ++i)
                 mbar_wait_bounded(&full[i % S::kStages], (i / S::kStages) & 1, nullptr, 1000000000ull);
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (elect_one()) {
-            mma_commit(&drain);   // TMEM is given back only after the last MMA
-            mbar_wait_bounded(&drain, 0, nullptr, 1000000000ull);
-        }
+        // TMEM and the barriers are given up only after the last MMA
+        if (rank == 0 && elect_one()) mma_commit<CG>(&drain);
         __syncwarp();
+        mbar_wait_cluster(&drain, 0, nullptr, 1000000000ull);
     }
     tc_fence_before();
     __syncthreads();
+    if (CG == 2) pair_sync();
     tc_fence_after();
-    if (warp == 1) tmem_free(tmem, 2 * S::kAccCols);
+    if (warp == 1) tmem_free<CG>(tmem, 2 * S::kAccCols);
     if (threadIdx.x == 0 && abort_flag && a.sc != nullptr) atomicOr(&a.sc->status, ZERO_DEV_TIMEOUT);
 }
 
@@ -1022,59 +1032,61 @@ struct Planes {
     long long ld = 0, stride = 0;
 };
 
-bool encode(Maps* map, const Planes& p, const __half* plane, int batch)
+bool encode(CUtensorMap* map, const Planes& p, const __half* plane, int batch)
 {
     const EncodeFn fn = encoder();
     if (fn == nullptr) return false;
-    const cuuint64_t rows = static_cast<cuuint64_t>(p.rows), cols = static_cast<cuuint64_t>(p.cols), n = static_cast<cuuint64_t>(batch);
-    const cuuint64_t ld = static_cast<cuuint64_t>(p.ld) * 2, stride = static_cast<cuuint64_t>(p.stride) * 2;
-    const cuuint32_t unit[4] = {1, 1, 1, 1};
-    const cuuint64_t kdims[3] = {cols, rows, n}, kstrides[2] = {ld, stride};
-    const cuuint32_t kbox[3] = {kBK, kBox, 1};
-    const cuuint64_t mdims[4] = {64, rows, (cols + 63) / 64, n}, mstrides[3] = {ld, 128, stride};
-    const cuuint32_t mbox[4] = {64, kBK, kBox / 64, 1};
-    void* at = const_cast<__half*>(plane);
-    return fn(&map->k, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, at, kdims, kstrides, kbox, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS &&
-           fn(&map->mn, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, at, mdims, mstrides, mbox, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.cols), static_cast<cuuint64_t>(p.rows), static_cast<cuuint64_t>(batch)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(p.ld) * 2, static_cast<cuuint64_t>(p.stride) * 2};
+    const cuuint32_t box[3] = {kBox, kBox, 1}, unit[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<__half*>(plane), dims, strides, box, unit,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // How a call is cut up.
 struct Plan {
-    int bn, joint;
+    int cg, bn, joint;
     int groups, ctas;
     int split[3];
     double us;
 };
 
-// Times of a CTA, in us, that the choice goes by (measured): a 64-deep stage
-// of 128 x 256 (48 KB of operands) and of 128 x 128 (32 KB; both planes: 64),
-// the results of a tile (beside the next tile's products), the exchange of
-// partial sums, the meeting of a group and the first copies after it.
-constexpr double kStage256 = 0.39, kStage128 = 0.25, kStageJoint = 0.46;
+// Times of a CTA or a pair, in us, that the choice goes by (measured): a
+// 64-deep stage, the results of a tile (beside the next tile's products), the
+// exchange of partial sums, the meeting of a group and the first copies after
+// it.
+double stage_us(int cg, int bn, int joint)
+{
+    if (cg == 1) return joint ? 0.53 : 0.27;
+    return bn == 256 ? 0.29 : joint ? 0.41 : 0.21;
+}
 constexpr double kResults256 = 4.8, kResults128 = 2.4;
 constexpr double kSplit256 = 8.4, kSplit128 = 4.7;
 constexpr double kMeet = 3.2, kMeetAlone = 2.2;
 
-long long sym_tiles(int m, int bn)
+long long sym_tiles(int m, int cg, int bn)
 {
-    const int sb = bn > kBM ? bn : kBM;
+    const int sb = sym_block(cg, bn);
     const long long blocks = (m + sb - 1) / sb;
-    return static_cast<long long>(sb / kBM) * (sb / bn) * (blocks * (blocks + 1) / 2);
+    return static_cast<long long>(sb / (kBM * cg)) * (sb / bn) * (blocks * (blocks + 1) / 2);
+}
+long long all_tiles(int rows, int cols, int cg, int bn)
+{
+    return static_cast<long long>((rows + kBM * cg - 1) / (kBM * cg)) * ((cols + bn - 1) / bn);
 }
 
 // the time of one product with `tiles` tiles and `stages` stages each on
-// `ctas` CTAs, and how many of them share a tile
-double phase_us(long long tiles, int stages, int passes, double stage_us, int bn, int ctas, int& split)
+// `units` CTAs or pairs, and how many of them share a tile
+double phase_us(long long tiles, int stages, double stage, int bn, int units, int& split)
 {
     const double end = bn == 256 ? kResults256 : kResults128, join = bn == 256 ? kSplit256 : kSplit128;
-    const double mma = stages * passes * stage_us;
-    const long long rounds = (tiles + ctas - 1) / ctas;
+    const double mma = stages * stage;
+    const long long rounds = (tiles + units - 1) / units;
     double best = mma + (rounds - 1) * (mma > end ? mma : end) + end;
     split = 1;
-    for (int q = 2; q <= kMaxSplit && q <= stages && tiles * q <= ctas; q *= 2) {
-        const double us = static_cast<double>((stages + q - 1) / q) * passes * stage_us + join + end / q;
+    for (int q = 2; q <= kMaxSplit && q <= stages && tiles * q <= units; q *= 2) {
+        const double us = static_cast<double>((stages + q - 1) / q) * stage + join + end / q;
         if (us < best) best = us, split = q;
     }
     return best;
@@ -1085,38 +1097,37 @@ Plan plan_of(int rows, int cols, int batch, int products, int sms)
     const int m = rows < cols ? rows : cols, n = rows < cols ? cols : rows;
     Plan best;
     std::memset(&best, 0, sizeof(best));
-    for (int bn = 128; bn <= 256; bn += 128) {
-        const int joint = bn == 128 && products == 3, passes = joint ? 1 : products;
-        const double st = joint ? kStageJoint : bn == 128 ? kStage128 : kStage256;
-        const long long sym = sym_tiles(m, bn);
-        const long long up = static_cast<long long>((rows + kBM - 1) / kBM) * ((cols + bn - 1) / bn);
+    for (int kind = 0; kind < 3; ++kind) {
+        Plan p;
+        p.cg = kind == 0 ? 1 : 2;
+        p.bn = kind == 2 ? 256 : 128;
+        p.joint = p.bn == 128 && products == 3;
+        const double st = stage_us(p.cg, p.bn, p.joint) * (p.joint ? 1 : products);
+        const long long sym = sym_tiles(m, p.cg, p.bn), up = all_tiles(rows, cols, p.cg, p.bn);
+        const int all = sms / p.cg;
         int last = 0;
-        for (int groups = 1; groups <= batch && groups <= sms; ++groups) {
-            Plan p;
-            p.bn = bn;
-            p.joint = joint;
-            p.groups = groups;
-            p.ctas = sms / groups;
-            const int turns = (batch + groups - 1) / groups;
+        for (p.groups = 1; p.groups <= batch && p.groups <= all; ++p.groups) {
+            const int turns = (batch + p.groups - 1) / p.groups;
             if (turns == last) continue;   // the same with smaller groups
             last = turns;
-            for (int pass = 0; pass < 2; ++pass) {
-                // as they are, then alone: without the meetings
-                if (pass == 1) p.ctas = 1;
-                const double us = phase_us(sym, (n + kBK - 1) / kBK, passes, st, bn, p.ctas, p.split[0]) +
-                                  phase_us(sym, (m + kBK - 1) / kBK, passes, st, bn, p.ctas, p.split[1]) +
-                                  phase_us(up, (m + kBK - 1) / kBK, passes, st, bn, p.ctas, p.split[2]);
-                p.us = turns * (us + 3 * (p.ctas > 1 ? kMeet : kMeetAlone));
+            for (int alone = 0; alone < 2; ++alone) {
+                // as they are, then a unit alone: without the meetings
+                const int units = alone ? 1 : all / p.groups;
+                p.ctas = units * p.cg;
+                const double us = phase_us(sym, (n + kBK - 1) / kBK, st, p.bn, units, p.split[0]) +
+                                  phase_us(sym, (m + kBK - 1) / kBK, st, p.bn, units, p.split[1]) +
+                                  phase_us(up, (m + kBK - 1) / kBK, st, p.bn, units, p.split[2]);
+                p.us = turns * (us + 3 * (units > 1 ? kMeet : kMeetAlone));
                 if (best.bn == 0 || p.us < best.us) best = p;
             }
         }
     }
     long long most = 0;
     for (int q = 0; q < 3; ++q) {
-        const long long tiles = q < 2 ? sym_tiles(m, best.bn) : static_cast<long long>((rows + kBM - 1) / kBM) * ((cols + best.bn - 1) / best.bn);
+        const long long tiles = q < 2 ? sym_tiles(m, best.cg, best.bn) : all_tiles(rows, cols, best.cg, best.bn);
         if (most < tiles * best.split[q]) most = tiles * best.split[q];
     }
-    if (most < best.ctas) best.ctas = static_cast<int>(most);   // CTAs that would only wait
+    if (most * best.cg < best.ctas) best.ctas = static_cast<int>(most) * best.cg;   // CTAs that would only wait
     return best;
 }
 
@@ -1176,11 +1187,11 @@ int sm_count()
     return n < kMaxSms ? n : kMaxSms;
 }
 
-template <int BN, bool JOINT>
+template <int CG, int BN, bool JOINT>
 cudaError_t launch_ns_as(const NsKernelArgs& a, cudaStream_t st)
 {
-    constexpr int smem = MmShape<BN, JOINT>::kSmem;
-    const auto k = ns_kernel<BN, JOINT>;
+    constexpr int smem = MmShape<CG, BN, JOINT>::kSmem;
+    const auto k = ns_kernel<CG, BN, JOINT>;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t c;
@@ -1189,22 +1200,31 @@ cudaError_t launch_ns_as(const NsKernelArgs& a, cudaStream_t st)
     c.blockDim = dim3(kThreads);
     c.dynamicSmemBytes = smem;
     c.stream = st;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeCooperative;   // CTAs that wait for one another are resident together
-    at.val.cooperative = 1;
-    c.attrs = &at;
-    c.numAttrs = a.ctas > 1 ? 1 : 0;
+    cudaLaunchAttribute at[2];
+    c.attrs = at;
+    if (CG == 2) {
+        at[c.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        at[c.numAttrs].val.clusterDim.x = 2;
+        at[c.numAttrs].val.clusterDim.y = at[c.numAttrs].val.clusterDim.z = 1;
+        ++c.numAttrs;
+    }
+    if (a.ctas > CG) {   // CTAs that wait for one another are resident together
+        at[c.numAttrs].id = cudaLaunchAttributeCooperative;
+        at[c.numAttrs].val.cooperative = 1;
+        ++c.numAttrs;
+    }
     count_launch();
     return cudaLaunchKernelEx(&c, k, a);
 }
 
 cudaError_t launch_products(const Plan& p, const NsKernelArgs& a, cudaStream_t st)
 {
-    if (p.bn == 256) return launch_ns_as<256, false>(a, st);
-    return p.joint ? launch_ns_as<128, true>(a, st) : launch_ns_as<128, false>(a, st);
+    if (p.cg == 1) return p.joint ? launch_ns_as<1, 128, true>(a, st) : launch_ns_as<1, 128, false>(a, st);
+    if (p.bn == 256) return launch_ns_as<2, 256, false>(a, st);
+    return p.joint ? launch_ns_as<2, 128, true>(a, st) : launch_ns_as<2, 128, false>(a, st);
 }
 
-bool set_planes(DevPlanes& d, Maps* maps, const Planes& p, int batch)
+bool set_planes(DevPlanes& d, CUtensorMap* maps, const Planes& p, int batch)
 {
     d.hi = p.hi;
     d.lo = p.lo;
@@ -1242,6 +1262,7 @@ cudaError_t launch_mm_starved(void* scratch, zero_dev_scalars* sc, unsigned long
     if (!set_planes(k.x[0], k.xmap[0], p, 1) || !set_planes(k.g, k.gmap, p, 1)) return cudaErrorInvalidValue;
     Plan plan;
     std::memset(&plan, 0, sizeof(plan));
+    plan.cg = 1;
     plan.bn = 128;
     return launch_products(plan, k, st);
 }
