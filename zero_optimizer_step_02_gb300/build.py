@@ -19,8 +19,8 @@ LIB = os.path.join(PKG, "libzero.so")
 BUILD = os.path.join(PKG, "_build")
 
 SOURCES = ["zk_stream.cu", "zk_aux.cu", "zk_capi.cu", "zk_noalloc.cu", "zk_small.cu", "zk_norm.cu", "zk_ortho.cu",
-           "zk_capi_ops.cu"]
-HEADERS = ["zk_common.cuh", "zk_launch.h", "zk_capi.h", "zk_ops.h", "zk_tc.cuh"]
+           "zk_ortho_small.cu", "zk_capi_ops.cu"]
+HEADERS = ["zk_common.cuh", "zk_launch.h", "zk_capi.h", "zk_ops.h", "zk_tc.cuh", "zk_ns.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-fmad=false", "-prec-div=true", "-prec-sqrt=true",

@@ -1,0 +1,204 @@
+// zk_ns.cuh -- what the two forms of the Newton-Schulz iteration share: the
+// scaling, element types, the rank mean and momentum of a Muon step.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "zk_common.cuh"
+#include "zk_ops.h"
+#include "zk_tc.cuh"
+
+namespace zk {
+
+constexpr float kScale = 4096.0f;
+constexpr float kInvScale = 1.0f / 4096.0f;
+
+__device__ __forceinline__ float2 half2_up(uint32_t w)
+{
+    const __half2 h = *reinterpret_cast<const __half2*>(&w);
+    return __half22float2(h);
+}
+
+__device__ __forceinline__ uint16_t narrow16(int dt, float v)
+{
+    return dt == ZERO_BF16 ? Lp<ZERO_BF16>::narrow(v) : Lp<ZERO_FP16>::narrow(v);
+}
+__device__ __forceinline__ uint32_t narrow16x2(int dt, float v, float w)
+{
+    return dt == ZERO_BF16 ? Lp<ZERO_BF16>::narrow2(v, w) : Lp<ZERO_FP16>::narrow2(v, w);
+}
+
+// eight consecutive values of a row of `dt`; n: how many of them exist
+__device__ __forceinline__ void put_row8(void* base, int dt, long long i, const float* v, int n, bool vec)
+{
+    if (dt == ZERO_FP32) {
+        float* p = static_cast<float*>(base) + i;
+        if (vec && n >= 8) {
+            *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < n) p[e] = v[e];
+        }
+    } else {
+        uint16_t* p = static_cast<uint16_t*>(base) + i;
+        if (vec && n >= 8) {
+            *reinterpret_cast<uint4*>(p) = make_uint4(narrow16x2(dt, v[0], v[1]), narrow16x2(dt, v[2], v[3]),
+                                                      narrow16x2(dt, v[4], v[5]), narrow16x2(dt, v[6], v[7]));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < n) p[e] = narrow16(dt, v[e]);
+        }
+    }
+}
+
+// eight consecutive elements from column 8 * ch of a row, zeros past its end
+__device__ __forceinline__ void load_row8(const void* in, int dtype, bool vec, long long row_at, int cols, int ch, float (&v)[8])
+{
+    const long long i = row_at + 8 * ch;
+    const int n = cols - 8 * ch;
+    if (dtype == ZERO_FP32) {
+        const float* p = static_cast<const float*>(in) + i;
+        if (vec && n >= 8) {
+            const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + 4);
+            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = e < n ? p[e] : 0.0f;
+        }
+        return;
+    }
+    const uint16_t* p = static_cast<const uint16_t*>(in) + i;
+    uint32_t w[4];
+    if (vec && n >= 8) {
+        const uint4 x = *reinterpret_cast<const uint4*>(p);
+        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            w[e] = (2 * e < n ? p[2 * e] : 0u) | ((2 * e + 1 < n ? static_cast<uint32_t>(p[2 * e + 1]) : 0u) << 16);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        v[2 * e] = dtype == ZERO_BF16 ? Lp<ZERO_BF16>::lo(w[e]) : Lp<ZERO_FP16>::lo(w[e]);
+        v[2 * e + 1] = dtype == ZERO_BF16 ? Lp<ZERO_BF16>::hi(w[e]) : Lp<ZERO_FP16>::hi(w[e]);
+    }
+}
+
+// the squares of eight values; in fp32 unless that overflows
+__device__ __forceinline__ double squares8(const float (&v)[8])
+{
+    float s = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = fmaf(v[e], v[e], s);
+    if (is_finite_f32(s)) return static_cast<double>(s);
+    double d = 0.0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) d += static_cast<double>(v[e]) * static_cast<double>(v[e]);
+    return d;
+}
+
+// sum over a block, in every thread; red: a double for each warp
+__device__ __forceinline__ double block_sum_f64(double v, double* red)
+{
+    v = warp_sum_f64(v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    double s = 0.0;
+    for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) s += red[i];
+    return s;
+}
+
+struct MuonArgs {
+    const void* rank[ZERO_MAX_RANKS];
+    int n_d, dtype, nesterov;
+    float divisor, mu;
+    float* momentum;
+    float* u;
+    long long stride, u_stride;
+    uint32_t elems;              // of one matrix
+    double* parts;
+    unsigned* counters;
+    int n_counters;
+};
+
+// Rank mean (rank order, fp32), momentum, and the update direction u of
+// elements 8 i .. of matrix b: m <- mu m + g, u = g + mu m (Nesterov) or m;
+// zeros past the matrix.
+__device__ __forceinline__ void muon_direction8(const MuonArgs& a, int b, uint32_t i, float (&u)[8])
+{
+    const int n = a.elems - 8 * i < 8 ? static_cast<int>(a.elems - 8 * i) : 8;
+    const long long at = b * a.stride + 8ll * i;
+    float g[8], m[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[e] = m[e] = 0.0f;
+    float* mp = a.momentum + at;
+    if (n == 8) {
+        const float4 x = *reinterpret_cast<const float4*>(mp), y = *reinterpret_cast<const float4*>(mp + 4);
+        m[0] = x.x, m[1] = x.y, m[2] = x.z, m[3] = x.w, m[4] = y.x, m[5] = y.y, m[6] = y.z, m[7] = y.w;
+#pragma unroll 4
+        for (int q = 0; q < a.n_d; ++q) {
+            const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.rank[q]) + at);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                g[2 * e] += a.dtype == ZERO_BF16 ? Lp<ZERO_BF16>::lo(w[e]) : Lp<ZERO_FP16>::lo(w[e]);
+                g[2 * e + 1] += a.dtype == ZERO_BF16 ? Lp<ZERO_BF16>::hi(w[e]) : Lp<ZERO_FP16>::hi(w[e]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (e >= n) continue;
+            m[e] = mp[e];
+            for (int q = 0; q < a.n_d; ++q) {
+                const uint16_t h = static_cast<const uint16_t*>(a.rank[q])[at + e];
+                g[e] += a.dtype == ZERO_BF16 ? Lp<ZERO_BF16>::widen(h) : Lp<ZERO_FP16>::widen(h);
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float mean = __fdiv_rn(g[e], a.divisor);
+        m[e] = __fadd_rn(__fmul_rn(a.mu, m[e]), mean);
+        u[e] = e >= n ? 0.0f : a.nesterov ? __fadd_rn(mean, __fmul_rn(a.mu, m[e])) : m[e];
+    }
+    put_row8(a.momentum, ZERO_FP32, at, m, n, true);
+    put_row8(a.u, ZERO_FP32, b * a.u_stride + 8ll * i, u, 8, true);
+}
+
+// w <- w * (1 - lr wd) - step * o for n of eight consecutive weights, and
+// their 16-bit cast (lp may be null)
+__device__ __forceinline__ void put_weights8(float* master, void* lp, int lp_dtype, long long at, float (&o)[8], int n, bool vec,
+                                             float decay, float step)
+{
+    float w[8];
+    if (vec && n >= 8) {
+        const float4 p = *reinterpret_cast<const float4*>(master + at), q = *reinterpret_cast<const float4*>(master + at + 4);
+        w[0] = p.x, w[1] = p.y, w[2] = p.z, w[3] = p.w, w[4] = q.x, w[5] = q.y, w[6] = q.z, w[7] = q.w;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = e < n ? master[at + e] : 0.0f;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = fmaf(-step, o[e], w[e] * decay);
+    put_row8(master, ZERO_FP32, at, o, n, vec);
+    if (lp != nullptr) put_row8(lp, lp_dtype, at, o, n, vec);
+}
+
+// whether rows of dt from p on may be read and written 16 bytes at a time
+inline bool wide_rows(const void* p, int dt, long long ld, long long stride)
+{
+    const int v = 16 / dtype_bytes(dt);
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % v == 0 && stride % v == 0;
+}
+
+// the form for matrices that one SM holds (zk_ortho_small.cu); mu: the Muon
+// step's, or null
+bool small_ns_fits(int rows, int cols, int products);
+cudaError_t launch_small_ns(const NsArgs& a, const MuonArgs* mu, cudaStream_t st);
+
+}  // namespace zk

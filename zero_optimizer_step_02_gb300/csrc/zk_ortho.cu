@@ -19,21 +19,17 @@
 // (relative, 2-norm), about the rounding of a bf16 result (1.7e-3).
 // products = 3 also carries G and P as pairs and multiplies
 // lo*hi + hi*lo + hi*hi: 3e-7 to 4e-6 off, for results kept in more than bf16.
-#include <cuda_fp16.h>
-
 #include <climits>
 #include <cstring>
 
-#include "zk_common.cuh"
 #include "zk_launch.h"
+#include "zk_ns.cuh"
 #include "zk_ops.h"
 #include "zk_tc.cuh"
 
 namespace zk {
 namespace {
 
-constexpr float kScale = 4096.0f;
-constexpr float kInvScale = 1.0f / 4096.0f;
 constexpr int kBM = 128;       // output rows of a CTA (TMEM lanes); a pair of CTAs shares tiles of twice as many
 constexpr int kBK = 64;        // depth of a pipeline stage: 128 bytes, one swizzle line
 constexpr int kBox = 64;       // rows (columns) of an operand that one TMA copy brings, 8 KB
@@ -172,12 +168,6 @@ struct Slot {
 };
 
 // ------------------------------------------------------------- epilogues
-__device__ __forceinline__ float2 half2_up(uint32_t w)
-{
-    const __half2 h = *reinterpret_cast<const __half2*>(&w);
-    return __half22float2(h);
-}
-
 // eight consecutive values of a pair of planes (lo may be null: zeros), from
 // L2: another SM may have written them a moment ago
 struct Addend {
@@ -238,41 +228,6 @@ __device__ __forceinline__ void put_planes8(const Eight& x, __half* hi, __half* 
     if (lo != nullptr) *reinterpret_cast<uint4*>(lo) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
 }
 
-__device__ __forceinline__ uint16_t narrow16(int dt, float v)
-{
-    return dt == ZERO_BF16 ? Lp<ZERO_BF16>::narrow(v) : Lp<ZERO_FP16>::narrow(v);
-}
-__device__ __forceinline__ uint32_t narrow16x2(int dt, float v, float w)
-{
-    return dt == ZERO_BF16 ? Lp<ZERO_BF16>::narrow2(v, w) : Lp<ZERO_FP16>::narrow2(v, w);
-}
-
-// eight consecutive values of a row of `dt`; n: how many of them exist
-__device__ __forceinline__ void put_row8(void* base, int dt, long long i, const float* v, int n, bool vec)
-{
-    if (dt == ZERO_FP32) {
-        float* p = static_cast<float*>(base) + i;
-        if (vec && n >= 8) {
-            *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (e < n) p[e] = v[e];
-        }
-    } else {
-        uint16_t* p = static_cast<uint16_t*>(base) + i;
-        if (vec && n >= 8) {
-            *reinterpret_cast<uint4*>(p) = make_uint4(narrow16x2(dt, v[0], v[1]), narrow16x2(dt, v[2], v[3]),
-                                                      narrow16x2(dt, v[4], v[5]), narrow16x2(dt, v[6], v[7]));
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (e < n) p[e] = narrow16(dt, v[e]);
-        }
-    }
-}
-
 // what becomes of a phase's sums: a pair of fp16 planes, the result, or the weights
 enum { RES_PLANES = 0, RES_OUT = 1, RES_MUON = 2 };
 
@@ -314,21 +269,7 @@ __device__ __noinline__ void put_last(const Phase* ph, int row, int col, Eight u
         put_row8(ph->res_out, ph->res_dtype, o, v, n, vec);
         return;
     }
-    // w <- w * (1 - lr wd) - step * o, rounded to the master's fp32, then its 16-bit cast
-    float* master = ph->master;
-    const float decay = ph->decay, step = ph->step;
-    float w[8];
-    if (vec && n >= 8) {
-        const float4 p = *reinterpret_cast<const float4*>(master + o), q = *reinterpret_cast<const float4*>(master + o + 4);
-        w[0] = p.x, w[1] = p.y, w[2] = p.z, w[3] = p.w, w[4] = q.x, w[5] = q.y, w[6] = q.z, w[7] = q.w;
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = e < n ? master[o + e] : 0.0f;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = fmaf(-step, v[e], w[e] * decay);
-    put_row8(master, ZERO_FP32, o, v, n, vec);
-    if (ph->res_out != nullptr) put_row8(ph->res_out, ph->res_dtype, o, v, n, vec);
+    put_weights8(ph->master, ph->res_out, ph->res_dtype, o, v, n, vec, ph->decay, ph->step);
 }
 
 // eight sums of one row from column `col`, to where they belong
@@ -459,64 +400,6 @@ struct PrepArgs {
     int n_counters;
 };
 
-// eight consecutive elements from column 8 * ch of a row, zeros past its end
-__device__ __forceinline__ void load_row8(const void* in, int dtype, bool vec, long long row_at, int cols, int ch, float (&v)[8])
-{
-    const long long i = row_at + 8 * ch;
-    const int n = cols - 8 * ch;
-    if (dtype == ZERO_FP32) {
-        const float* p = static_cast<const float*>(in) + i;
-        if (vec && n >= 8) {
-            const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + 4);
-            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = e < n ? p[e] : 0.0f;
-        }
-        return;
-    }
-    const uint16_t* p = static_cast<const uint16_t*>(in) + i;
-    uint32_t w[4];
-    if (vec && n >= 8) {
-        const uint4 x = *reinterpret_cast<const uint4*>(p);
-        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            w[e] = (2 * e < n ? p[2 * e] : 0u) | ((2 * e + 1 < n ? static_cast<uint32_t>(p[2 * e + 1]) : 0u) << 16);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        v[2 * e] = dtype == ZERO_BF16 ? Lp<ZERO_BF16>::lo(w[e]) : Lp<ZERO_FP16>::lo(w[e]);
-        v[2 * e + 1] = dtype == ZERO_BF16 ? Lp<ZERO_BF16>::hi(w[e]) : Lp<ZERO_FP16>::hi(w[e]);
-    }
-}
-
-// the squares of eight values; in fp32 unless that overflows
-__device__ __forceinline__ double squares8(const float (&v)[8])
-{
-    float s = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s = fmaf(v[e], v[e], s);
-    if (is_finite_f32(s)) return static_cast<double>(s);
-    double d = 0.0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) d += static_cast<double>(v[e]) * static_cast<double>(v[e]);
-    return d;
-}
-
-// sum over a block, in every thread; red: a double for each warp
-__device__ __forceinline__ double block_sum_f64(double v, double* red)
-{
-    v = warp_sum_f64(v);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    double s = 0.0;
-    for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) s += red[i];
-    return s;
-}
-
 __device__ __forceinline__ void clear_counters(unsigned* c, int n)
 {
     if (blockIdx.x == 0 && blockIdx.y == 0)
@@ -541,21 +424,7 @@ __global__ void __launch_bounds__(256) ns_sqnorm(const __grid_constant__ PrepArg
     if (threadIdx.x == 0) a.parts[blockIdx.y * static_cast<long long>(gridDim.x) + blockIdx.x] = s;
 }
 
-struct MuonArgs {
-    const void* rank[ZERO_MAX_RANKS];
-    int n_d, dtype, nesterov;
-    float divisor, mu;
-    float* momentum;
-    float* u;
-    long long stride, u_stride;
-    uint32_t elems;              // of one matrix
-    double* parts;
-    unsigned* counters;
-    int n_counters;
-};
-
-// Rank mean (rank order, fp32), momentum, and the update direction u with its
-// squared norm: m <- mu m + g, u = g + mu m (Nesterov) or m.
+// the update direction of every matrix, with the sums of its squares
 __global__ void __launch_bounds__(256) muon_direction(const __grid_constant__ MuonArgs a)
 {
     __shared__ double red[8];
@@ -563,51 +432,8 @@ __global__ void __launch_bounds__(256) muon_direction(const __grid_constant__ Mu
     clear_counters(a.counters, a.n_counters);
     double s = 0.0;
     for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i * 8u < a.elems; i += gridDim.x * 256) {
-        const int n = a.elems - 8 * i < 8 ? static_cast<int>(a.elems - 8 * i) : 8;
-        const long long at = blockIdx.y * a.stride + 8ll * i;
-        float g[8], m[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = 0.0f;
-        if (n == 8) {
-#pragma unroll 4
-            for (int q = 0; q < a.n_d; ++q) {
-                const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.rank[q]) + at);
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    g[2 * e] += a.dtype == ZERO_BF16 ? Lp<ZERO_BF16>::lo(w[e]) : Lp<ZERO_FP16>::lo(w[e]);
-                    g[2 * e + 1] += a.dtype == ZERO_BF16 ? Lp<ZERO_BF16>::hi(w[e]) : Lp<ZERO_FP16>::hi(w[e]);
-                }
-            }
-        } else {
-            for (int q = 0; q < a.n_d; ++q)
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (e < n) {
-                        const uint16_t h = static_cast<const uint16_t*>(a.rank[q])[at + e];
-                        g[e] += a.dtype == ZERO_BF16 ? Lp<ZERO_BF16>::widen(h) : Lp<ZERO_FP16>::widen(h);
-                    }
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m[e] = 0.0f;
-        float* mp = a.momentum + at;
-        if (n == 8) {
-            const float4 x = *reinterpret_cast<const float4*>(mp), y = *reinterpret_cast<const float4*>(mp + 4);
-            m[0] = x.x, m[1] = x.y, m[2] = x.z, m[3] = x.w, m[4] = y.x, m[5] = y.y, m[6] = y.z, m[7] = y.w;
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (e < n) m[e] = mp[e];
-        }
         float u[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float mean = __fdiv_rn(g[e], a.divisor);
-            m[e] = __fadd_rn(__fmul_rn(a.mu, m[e]), mean);
-            u[e] = e >= n ? 0.0f : a.nesterov ? __fadd_rn(mean, __fmul_rn(a.mu, m[e])) : m[e];
-        }
-        put_row8(a.momentum, ZERO_FP32, at, m, n, true);
-        put_row8(a.u, ZERO_FP32, blockIdx.y * a.u_stride + 8ll * i, u, 8, true);
+        muon_direction8(a, blockIdx.y, i, u);
         s += squares8(u);
     }
     s = block_sum_f64(s, red);
@@ -1269,15 +1095,34 @@ cudaError_t launch_mm_starved(void* scratch, zero_dev_scalars* sc, unsigned long
 
 cudaError_t launch_ns(const NsArgs& a, cudaStream_t st)
 {
-    const int sms = sm_count();
-    if (sms == 0) return cudaErrorInvalidDevice;
     const bool muon = a.out == nullptr, wide = a.rows <= a.cols;
     const int m = wide ? a.rows : a.cols;
     const Layout l = layout_of(a.rows, a.cols, a.batch, a.products, muon);
-    const Plan plan = plan_of(a.rows, a.cols, a.batch, a.products, sms);
     char* ws = static_cast<char*>(a.ws);
     unsigned* counters = reinterpret_cast<unsigned*>(ws + l.counters);
-
+    double* parts = reinterpret_cast<double*>(ws + l.parts);
+    MuonArgs mu;
+    if (muon) {
+        std::memset(&mu, 0, sizeof(mu));
+        for (int q = 0; q < a.n_d; ++q) mu.rank[q] = a.ranks[q];
+        mu.n_d = a.n_d;
+        mu.dtype = a.in_dtype;
+        mu.nesterov = a.nesterov;
+        mu.divisor = a.divisor;
+        mu.mu = a.mu;
+        mu.momentum = a.momentum;
+        mu.u = reinterpret_cast<float*>(ws + l.u);
+        mu.stride = a.flat_stride;
+        mu.elems = static_cast<uint32_t>(a.rows) * static_cast<uint32_t>(a.cols);
+        mu.u_stride = (static_cast<long long>(mu.elems) + 7) / 8 * 8;
+        mu.parts = parts;
+        mu.counters = counters;
+        mu.n_counters = kMaxSms * (kBarStride + 1);
+    }
+    if (small_ns_fits(a.rows, a.cols, a.products)) return launch_small_ns(a, muon ? &mu : nullptr, st);
+    const int sms = sm_count();
+    if (sms == 0) return cudaErrorInvalidDevice;
+    const Plan plan = plan_of(a.rows, a.cols, a.batch, a.products, sms);
     NsKernelArgs k;
     std::memset(&k, 0, sizeof(k));
     bool ok = true;
@@ -1298,7 +1143,6 @@ cudaError_t launch_ns(const NsArgs& a, cudaStream_t st)
     std::memcpy(k.coef, a.coef, sizeof(k.coef));
     k.chunks = (a.cols + 7) / 8;
     k.eps = a.eps;
-    double* parts = reinterpret_cast<double*>(ws + l.parts);
     k.parts = parts;
     k.group_bar = counters;
     k.tile_bar = counters + kMaxSms * kBarStride;
@@ -1314,22 +1158,6 @@ cudaError_t launch_ns(const NsArgs& a, cudaStream_t st)
     k.parts_n = static_cast<int>(per);
     const dim3 grid(static_cast<unsigned>(per), a.batch);
     if (muon) {
-        MuonArgs mu;
-        std::memset(&mu, 0, sizeof(mu));
-        for (int q = 0; q < a.n_d; ++q) mu.rank[q] = a.ranks[q];
-        mu.n_d = a.n_d;
-        mu.dtype = a.in_dtype;
-        mu.nesterov = a.nesterov;
-        mu.divisor = a.divisor;
-        mu.mu = a.mu;
-        mu.momentum = a.momentum;
-        mu.u = reinterpret_cast<float*>(ws + l.u);
-        mu.stride = a.flat_stride;
-        mu.elems = static_cast<uint32_t>(a.rows) * static_cast<uint32_t>(a.cols);
-        mu.u_stride = (static_cast<long long>(mu.elems) + 7) / 8 * 8;
-        mu.parts = parts;
-        mu.counters = counters;
-        mu.n_counters = kMaxSms * (kBarStride + 1);
         k.in = mu.u;
         k.in_dtype = ZERO_FP32;
         k.in_ld = a.cols;
@@ -1346,18 +1174,17 @@ cudaError_t launch_ns(const NsArgs& a, cudaStream_t st)
         k.step = a.step;
         ZK_GO(launch_after(muon_direction, grid, dim3(256), 0, st, mu));
     } else {
-        const int v = 16 / dtype_bytes(a.in_dtype), w = 16 / dtype_bytes(a.out_dtype);
         k.in = a.in;
         k.in_dtype = a.in_dtype;
         k.in_ld = a.in_ld;
         k.in_stride = a.in_stride;
-        k.in_vec = reinterpret_cast<uintptr_t>(a.in) % 16 == 0 && a.in_ld % v == 0 && a.in_stride % v == 0;
+        k.in_vec = wide_rows(a.in, a.in_dtype, a.in_ld, a.in_stride);
         k.res = RES_OUT;
         k.out = a.out;
         k.out_dtype = a.out_dtype;
         k.out_ld = a.out_ld;
         k.out_stride = a.out_stride;
-        k.out_vec = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.out_ld % w == 0 && a.out_stride % w == 0;
+        k.out_vec = wide_rows(a.out, a.out_dtype, a.out_ld, a.out_stride);
         PrepArgs pr;
         std::memset(&pr, 0, sizeof(pr));
         pr.in = k.in;

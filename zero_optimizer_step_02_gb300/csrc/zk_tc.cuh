@@ -128,13 +128,31 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32])
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// v[0 .. 15] += sixteen of them
+__device__ __forceinline__ void tmem_add16(uint32_t addr, float (&v)[16])
+{
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32"
+        " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(r[i]);
+}
+
 // -------------------------------------------------------------------- MMA
 // Shared-memory operand descriptor, 128-byte swizzle.  A K-major tile is rows
 // of 64 16-bit values (128 bytes), eight-row groups 1024 bytes apart; an
 // MN-major tile is panels of 64 rows/columns, one K index per 128-byte line,
-// eight K indices per 1024 bytes (stride), panels 8192 bytes apart (leading).
+// eight K indices per 1024 bytes (stride), panels `leading` bytes apart.
 // Low word: address and leading offset; high word: stride, version, swizzle.
-__device__ __forceinline__ uint32_t smem_desc_lo(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | ((8192u >> 4) << 16); }
+__device__ __forceinline__ uint32_t smem_desc_lo(uint32_t addr, uint32_t leading = 8192u)
+{
+    return ((addr & 0x3FFFFu) >> 4) | ((leading >> 4) << 16);
+}
 constexpr uint32_t kSmemDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 
 // kind::f16 instruction descriptor: fp16 operands, fp32 accumulator
