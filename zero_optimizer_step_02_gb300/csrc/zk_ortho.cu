@@ -878,18 +878,21 @@ struct Plan {
     double us;
 };
 
-// Times of a CTA or a pair, in us, that the choice goes by (measured): a
-// 64-deep stage, the results of a tile (beside the next tile's products), the
-// exchange of partial sums, the meeting of a group and the first copies after
-// it.
-double stage_us(int cg, int bn, int joint)
+// Times of a CTA or a pair, in us, that the choice goes by, fitted to 22 shapes
+// timed in each form (from 256 x 256 to 4096 x 4096, one and three products;
+// the choice is within 5% of the best of the three for all but one, 10%): a
+// 64-deep stage, the results of a tile beside the next tile's products and
+// alone at the end, the same with an exchange of partial sums, the meeting of
+// a group and the first copies after it.
+struct Costs {
+    double stage, results, end, split_end, meet, alone;
+};
+Costs costs_of(int cg, int bn, int joint)
 {
-    if (cg == 1) return joint ? 0.53 : 0.27;
-    return bn == 256 ? 0.29 : joint ? 0.41 : 0.21;
+    if (cg == 1) return {joint ? 0.53 : 0.27, 4.6, 3.0, 7.0, 3.2, 2.2};
+    if (bn == 256) return {0.29, 6.5, 5.0, 14.0, 3.9, 2.9};
+    return {joint ? 0.41 : 0.21, 5.2, 3.4, 7.4, 3.9, 2.9};
 }
-constexpr double kResults256 = 4.8, kResults128 = 2.4;
-constexpr double kSplit256 = 8.4, kSplit128 = 4.7;
-constexpr double kMeet = 3.2, kMeetAlone = 2.2;
 
 long long sym_tiles(int m, int cg, int bn)
 {
@@ -904,15 +907,14 @@ long long all_tiles(int rows, int cols, int cg, int bn)
 
 // the time of one product with `tiles` tiles and `stages` stages each on
 // `units` CTAs or pairs, and how many of them share a tile
-double phase_us(long long tiles, int stages, double stage, int bn, int units, int& split)
+double phase_us(long long tiles, int stages, const Costs& c, int passes, int units, int& split)
 {
-    const double end = bn == 256 ? kResults256 : kResults128, join = bn == 256 ? kSplit256 : kSplit128;
-    const double mma = stages * stage;
+    const double mma = stages * passes * c.stage;
     const long long rounds = (tiles + units - 1) / units;
-    double best = mma + (rounds - 1) * (mma > end ? mma : end) + end;
+    double best = mma + (rounds - 1) * (mma > c.results ? mma : c.results) + c.end;
     split = 1;
     for (int q = 2; q <= kMaxSplit && q <= stages && tiles * q <= units; q *= 2) {
-        const double us = static_cast<double>((stages + q - 1) / q) * stage + join + end / q;
+        const double us = static_cast<double>((stages + q - 1) / q) * passes * c.stage + c.split_end;
         if (us < best) best = us, split = q;
     }
     return best;
@@ -928,7 +930,8 @@ Plan plan_of(int rows, int cols, int batch, int products, int sms)
         p.cg = kind == 0 ? 1 : 2;
         p.bn = kind == 2 ? 256 : 128;
         p.joint = p.bn == 128 && products == 3;
-        const double st = stage_us(p.cg, p.bn, p.joint) * (p.joint ? 1 : products);
+        const Costs c = costs_of(p.cg, p.bn, p.joint);
+        const int passes = p.joint ? 1 : products;
         const long long sym = sym_tiles(m, p.cg, p.bn), up = all_tiles(rows, cols, p.cg, p.bn);
         const int all = sms / p.cg;
         int last = 0;
@@ -940,10 +943,10 @@ Plan plan_of(int rows, int cols, int batch, int products, int sms)
                 // as they are, then a unit alone: without the meetings
                 const int units = alone ? 1 : all / p.groups;
                 p.ctas = units * p.cg;
-                const double us = phase_us(sym, (n + kBK - 1) / kBK, st, p.bn, units, p.split[0]) +
-                                  phase_us(sym, (m + kBK - 1) / kBK, st, p.bn, units, p.split[1]) +
-                                  phase_us(up, (m + kBK - 1) / kBK, st, p.bn, units, p.split[2]);
-                p.us = turns * (us + 3 * (units > 1 ? kMeet : kMeetAlone));
+                const double us = phase_us(sym, (n + kBK - 1) / kBK, c, passes, units, p.split[0]) +
+                                  phase_us(sym, (m + kBK - 1) / kBK, c, passes, units, p.split[1]) +
+                                  phase_us(up, (m + kBK - 1) / kBK, c, passes, units, p.split[2]);
+                p.us = turns * (us + 3 * (units > 1 ? c.meet : c.alone));
                 if (best.bn == 0 || p.us < best.us) best = p;
             }
         }
