@@ -55,7 +55,8 @@ size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 size_t ln_parts_bytes(const zero_layernorm* d)
 {
-    const long long parts = d->rows < zk::kLnMaxParts ? d->rows : zk::kLnMaxParts;
+    // at least eight: some kernels deal rows out eight apart
+    const long long parts = d->rows < 8 ? 8 : d->rows < zk::kLnMaxParts ? d->rows : zk::kLnMaxParts;
     return round256(static_cast<size_t>(parts) * 2 * d->cols * sizeof(float));
 }
 

@@ -169,11 +169,19 @@ __global__ void __launch_bounds__(256) ln_backward_cols(const __grid_constant__ 
 // column sums stay in registers, and the rows to come are already on their way
 // into a ring of DEPTH stages in shared memory (16-byte asynchronous copies).
 //
-// ALIGNED: bases, strides and the width are multiples of 16 bytes.  A thread
-// then fills and empties its own ring slots alone.  Otherwise the group copies
-// the 16-byte words that cover a row as they lie in memory, a chunk is two
-// words of shared memory shifted into place, and results go through shared
-// memory too, so that global memory still sees whole words.
+// How the rows lie (MODE):
+//   kAligned  bases, strides and the width are multiples of 16 bytes.  A thread
+//             fills and empties its own ring slots alone.
+//   kAlike    not that, but equal rows of all arrays start equally far into a
+//             16-byte word (an odd width without gaps).  A CTA takes rows eight
+//             apart, which all start alike, and cuts them where memory's words
+//             lie: chunk j holds the columns from V j - first on.  Slots stay
+//             private; only a row's first and last word need care.
+//   kMixed    the group copies the words that cover a row as they lie, a chunk
+//             is two words of shared memory shifted into place, and results go
+//             through shared memory too, so that global memory sees whole words.
+enum { kAligned = 0, kAlike = 1, kMixed = 2 };
+
 template <int DT>
 constexpr int kV = DT == ZERO_FP32 ? 4 : 8;
 
@@ -226,21 +234,19 @@ __device__ __forceinline__ float both(f32x2 v)
     return a + b;
 }
 
-// a chunk without the columns from `cols` on (zeros there); c: its first
+// a chunk without the columns before 0 and from `cols` on (zeros there); c: its first
 template <int DT>
 __device__ __forceinline__ uint4 masked(const uint4& w, int c, int cols)
 {
-    if (c + kV<DT> <= cols) return w;
+    if (c >= 0 && c + kV<DT> <= cols) return w;
     uint32_t a[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if constexpr (DT == ZERO_FP32) {
-            if (c + i >= cols) a[i] = 0;
+            if (c + i < 0 || c + i >= cols) a[i] = 0;
         } else {
-            if (c + 2 * i >= cols)
-                a[i] = 0;
-            else if (c + 2 * i + 1 >= cols)
-                a[i] &= 0xFFFFu;
+            if (c + 2 * i < 0 || c + 2 * i >= cols) a[i] &= 0xFFFF0000u;
+            if (c + 2 * i + 1 < 0 || c + 2 * i + 1 >= cols) a[i] &= 0xFFFFu;
         }
     }
     return make_uint4(a[0], a[1], a[2], a[3]);
@@ -290,6 +296,21 @@ struct RowSource {
     }
     __device__ __forceinline__ uintptr_t row(long long r) const { return reinterpret_cast<uintptr_t>(base + r * stride); }
 
+    // The aligned word at `at`, which holds elements of the row [from, to), into
+    // *dst: whole if it lies inside the array, else the row's elements alone.
+    __device__ __forceinline__ void copy_word(uint4* dst, uintptr_t at, uintptr_t from, uintptr_t to) const
+    {
+        if (at >= lo && at + 16 <= hi) {
+            cp_async16(dst, reinterpret_cast<const void*>(at));
+            return;
+        }
+        T* d = reinterpret_cast<T*>(dst);
+        for (int e = 0; e < static_cast<int>(16 / sizeof(T)); ++e) {
+            const uintptr_t q = at + e * sizeof(T);
+            if (q >= from && q < to) d[e] = *reinterpret_cast<const T*>(q);
+        }
+    }
+
     // The words that cover row r into dst, word j by thread j, j + width, ...
     // Every word lies inside the array but for the first of the first row and
     // the last of the last one, which are copied element by element.
@@ -297,16 +318,45 @@ struct RowSource {
     {
         const uintptr_t from = row(r), to = from + static_cast<uintptr_t>(cols) * sizeof(T);
         uintptr_t at = (from & ~static_cast<uintptr_t>(15)) + 16u * t;
-        for (int j = t; at < to; j += width, at += 16u * width) {
-            if (at >= lo && at + 16 <= hi) {
-                cp_async16(dst + j, reinterpret_cast<const void*>(at));
-            } else {
-                T* d = reinterpret_cast<T*>(dst + j);
-                for (int e = 0; e < static_cast<int>(16 / sizeof(T)); ++e) {
-                    const uintptr_t q = at + e * sizeof(T);
-                    if (q >= from && q < to) d[e] = *reinterpret_cast<const T*>(q);
-                }
-            }
+        for (int j = t; at < to; j += width, at += 16u * width) copy_word(dst + j, at, from, to);
+    }
+};
+
+// V results from column c on of the row that starts at `row` (kAlike: c + row's
+// offset is a whole word; a row's first and last words are written in part)
+template <int DT>
+__device__ __forceinline__ void put_word(uintptr_t row, int c, int cols, const uint4& w)
+{
+    using T = typename El<DT>::T;
+    T* p = reinterpret_cast<T*>(row) + c;
+    if (c >= 0 && c + kV<DT> <= cols) {
+        __stcs(reinterpret_cast<uint4*>(p), w);
+        return;
+    }
+    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < kV<DT>; ++e) {
+        if (c + e < 0 || c + e >= cols) continue;
+        if constexpr (sizeof(T) == 4)
+            reinterpret_cast<uint32_t*>(p)[e] = a[e];
+        else
+            reinterpret_cast<uint16_t*>(p)[e] = static_cast<uint16_t>(a[e / 2] >> (16 * (e & 1)));
+    }
+}
+
+// The rows of a group: row(k) of the set at r0 is r0 + k * apart.
+template <int MODE, int R>
+struct Walk {
+    static constexpr int apart = MODE == kAlike ? 8 : 1;
+    long long r0, step;
+    __device__ __forceinline__ Walk(int grp, int groups)
+    {
+        if (MODE == kAlike) {   // gridDim.x is a multiple of 8
+            r0 = (blockIdx.x & 7) + 8ll * ((blockIdx.x >> 3) * groups + grp) * R;
+            step = 8ll * (gridDim.x >> 3) * groups * R;
+        } else {
+            r0 = (static_cast<long long>(blockIdx.x) * groups + grp) * R;
+            step = static_cast<long long>(gridDim.x) * groups * R;
         }
     }
 };
@@ -340,13 +390,13 @@ __device__ __forceinline__ void write_words(const uint4* src, uintptr_t from, in
 }
 
 // V weights from column c on, in whichever type they have; `none` without a
-// vector, 0 past the last column
+// vector, 0 where there is no such column
 template <int V>
 __device__ __forceinline__ void weights_at(const void* w, int dt, int c, int cols, float none, f32x2 (&v)[V / 2])
 {
     float f[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) f[e] = c + e >= cols ? 0.0f : w == nullptr ? none : weight_at(w, dt, c + e);
+    for (int e = 0; e < V; ++e) f[e] = c + e < 0 || c + e >= cols ? 0.0f : w == nullptr ? none : weight_at(w, dt, c + e);
 #pragma unroll
     for (int e = 0; e < V / 2; ++e) v[e] = pack2(f[2 * e], f[2 * e + 1]);
 }
@@ -411,7 +461,7 @@ __device__ __forceinline__ void group_sync(int grp, int warps, int width)
         named_bar_sync(1 + grp, width);
 }
 
-template <int DT, int NCH, int R, int DEPTH, int MINB, bool ALIGNED>
+template <int DT, int NCH, int R, int DEPTH, int MINB, int MODE>
 __global__ void __launch_bounds__(512, MINB)
     ln_forward_rows(const __grid_constant__ LnArgs a, int warps, int groups)
 {
@@ -420,6 +470,12 @@ __global__ void __launch_bounds__(512, MINB)
     __shared__ float red[2][8][kMaxWarps * R];
     const int width = warps * 32, grp = threadIdx.x / width, t = threadIdx.x % width, wg = t >> 5;
     const int chunks = (a.cols + V - 1) / V, words = row_words(chunks);
+    Walk<MODE, R> walk(grp, groups);
+    long long& r0 = walk.r0;
+    const long long step = walk.step;
+    // columns of the array's first word that belong to the row before
+    const int first = MODE == kAlike ? static_cast<int>((reinterpret_cast<uintptr_t>(static_cast<const typename El<DT>::T*>(a.x) + r0 * a.x_stride) & 15u) / sizeof(typename El<DT>::T)) : 0;
+    const int here = MODE == kAlike ? (first + a.cols + V - 1) / V : chunks;   // words of a row
     const float inv_c = 1.0f / static_cast<float>(a.cols);
     for (int i = threadIdx.x; i < 2 * 8 * kMaxWarps * R; i += blockDim.x) (&red[0][0][0])[i] = 0.0f;
     __syncthreads();
@@ -428,43 +484,49 @@ __global__ void __launch_bounds__(512, MINB)
     f32x2 gain[NCH][V / 2], bias[NCH][V / 2];
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-        weights_at<V>(a.gain, a.w_dtype, (t + i * width) * V, a.cols, 1.0f, gain[i]);
-        weights_at<V>(a.bias, a.w_dtype, (t + i * width) * V, a.cols, 0.0f, bias[i]);
+        weights_at<V>(a.gain, a.w_dtype, (t + i * width) * V - first, a.cols, 1.0f, gain[i]);
+        weights_at<V>(a.bias, a.w_dtype, (t + i * width) * V - first, a.cols, 0.0f, bias[i]);
     }
     const RowSource<DT> x(a.x, a.x_stride, a.rows, a.cols);
-    // ALIGNED: [DEPTH][R][NCH][threads], else a group's [DEPTH][R][words] and [R][words] of results
-    uint4* ring = reinterpret_cast<uint4*>(smem) + (ALIGNED ? threadIdx.x : grp * (DEPTH + 1) * R * words);
+    // [DEPTH][R][NCH][threads]; kMixed: a group's [DEPTH][R][words] and [R][words] of results
+    uint4* ring = reinterpret_cast<uint4*>(smem) + (MODE != kMixed ? threadIdx.x : grp * (DEPTH + 1) * R * words);
     uint4* outs = ring + DEPTH * R * words;
     auto fetch = [&](long long r0, int s) {
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            if (r0 + k >= a.rows) break;
-            if (ALIGNED) {
+            const long long r = r0 + k * walk.apart;
+            if (r >= a.rows) break;
+            if (MODE != kMixed) {
 #pragma unroll
                 for (int i = 0; i < NCH; ++i)
-                    if (t + i * width < chunks)
-                        cp_async16(ring + ((s * R + k) * NCH + i) * blockDim.x, x.base + (r0 + k) * x.stride + (t + i * width) * V);
+                    if (t + i * width < here) {
+                        uint4* p = ring + ((s * R + k) * NCH + i) * blockDim.x;
+                        const typename El<DT>::T* q = x.base + r * x.stride;
+                        if (MODE == kAligned)
+                            cp_async16(p, q + (t + i * width) * V);
+                        else
+                            x.copy_word(p, reinterpret_cast<uintptr_t>(q - first + (t + i * width) * V), reinterpret_cast<uintptr_t>(q), reinterpret_cast<uintptr_t>(q + a.cols));
+                    }
             } else {
-                x.copy_words(ring + (s * R + k) * words, r0 + k, a.cols, t, width);
+                x.copy_words(ring + (s * R + k) * words, r, a.cols, t, width);
             }
         }
         cp_async_commit();
     };
-    const long long step = static_cast<long long>(gridDim.x) * groups * R;
-    long long r0 = (static_cast<long long>(blockIdx.x) * groups + grp) * R;
     for (int s = 0; s < DEPTH - 1; ++s) fetch(r0 + s * step, s);
     for (int s = 0; r0 < a.rows; r0 += step, s = s + 1 == DEPTH ? 0 : s + 1) {
         cp_async_wait<DEPTH - 2>();
-        if (!ALIGNED) group_sync(grp, warps, width);
+        if (MODE == kMixed) group_sync(grp, warps, width);
         uint4 w[R][NCH];
 #pragma unroll
         for (int k = 0; k < R; ++k)
 #pragma unroll
             for (int i = 0; i < NCH; ++i) {
                 w[k][i] = make_uint4(0, 0, 0, 0);
-                if (t + i * width >= chunks || r0 + k >= a.rows) continue;
-                if (ALIGNED) {
+                if (t + i * width >= here || r0 + k * walk.apart >= a.rows) continue;
+                if (MODE != kMixed) {
                     w[k][i] = ring[((s * R + k) * NCH + i) * blockDim.x];
+                    if (MODE == kAlike) w[k][i] = masked<DT>(w[k][i], (t + i * width) * V - first, a.cols);
                 } else {
                     const uint4* p = ring + (s * R + k) * words + t + i * width;
                     w[k][i] = masked<DT>(shifted(p[0], p[1], x.row(r0 + k) & 15u), (t + i * width) * V, a.cols);
@@ -492,9 +554,9 @@ __global__ void __launch_bounds__(512, MINB)
             f32x2 sum = 0;
 #pragma unroll
             for (int i = 0; i < NCH; ++i) {
-                const int c = (t + i * width) * V;
+                const int c = (t + i * width) * V - first;
                 forget(w[k][i]);
-                if (c + V <= a.cols) {
+                if (c >= 0 && c + V <= a.cols) {
                     f32x2 f[V / 2];
                     widen<DT>(w[k][i], f);
 #pragma unroll
@@ -502,12 +564,12 @@ __global__ void __launch_bounds__(512, MINB)
                         f[e] = sub2(f[e], m);
                         sum = fma2(f[e], f[e], sum);
                     }
-                } else if (!ALIGNED && c < a.cols) {
+                } else if (MODE != kAligned && c < a.cols) {
                     float f[V], part = 0.0f;
                     widen<DT>(w[k][i], f);
 #pragma unroll
                     for (int e = 0; e < V; ++e)
-                        if (c + e < a.cols) part = fmaf(f[e] - mean[k], f[e] - mean[k], part);
+                        if (c + e >= 0 && c + e < a.cols) part = fmaf(f[e] - mean[k], f[e] - mean[k], part);
                     sum = add2(sum, pack2(part, 0.0f));
                 }
             }
@@ -516,14 +578,15 @@ __global__ void __launch_bounds__(512, MINB)
         group_sums<R>(rstd, red[1][grp & 7], warps, 1 + grp, width, wg);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            if (r0 + k >= a.rows) break;
+            const long long r = r0 + k * walk.apart;
+            if (r >= a.rows) break;
             rstd[k] = 1.0f / sqrtf(rstd[k] * inv_c + a.eps);
             const RowSource<DT> y(a.out, a.out_stride, a.rows, a.cols);
             // xhat in one operation: x * rstd - mean * rstd
             const f32x2 rs = pack2(rstd[k], rstd[k]), nm = pack2(-mean[k] * rstd[k], -mean[k] * rstd[k]);
 #pragma unroll
             for (int i = 0; i < NCH; ++i) {
-                const int c = (t + i * width) * V;
+                const int c = (t + i * width) * V - first;
                 if (c >= a.cols) break;
                 f32x2 f[V / 2];
                 float o[V];
@@ -532,17 +595,19 @@ __global__ void __launch_bounds__(512, MINB)
 #pragma unroll
                 for (int e = 0; e < V / 2; ++e) f[e] = fma2(fma2(f[e], rs, nm), gain[i][e], bias[i][e]);
                 unpack(f, o);
-                if (ALIGNED)
-                    __stcs(reinterpret_cast<uint4*>(y.row(r0 + k)) + t + i * width, narrowed<DT>(o));
+                if (MODE == kAligned)
+                    __stcs(reinterpret_cast<uint4*>(y.row(r)) + t + i * width, narrowed<DT>(o));
+                else if (MODE == kAlike)
+                    put_word<DT>(y.row(r), c, a.cols, narrowed<DT>(o));
                 else
                     outs[k * words + 1 + t + i * width] = narrowed<DT>(o);
             }
             if (t == 0) {
-                if (a.mean_out != nullptr) a.mean_out[r0 + k] = mean[k];
-                if (a.rstd_out != nullptr) a.rstd_out[r0 + k] = rstd[k];
+                if (a.mean_out != nullptr) a.mean_out[r] = mean[k];
+                if (a.rstd_out != nullptr) a.rstd_out[r] = rstd[k];
             }
         }
-        if (!ALIGNED) {
+        if (MODE == kMixed) {
             group_sync(grp, warps, width);
             const RowSource<DT> y(a.out, a.out_stride, a.rows, a.cols);
 #pragma unroll
@@ -552,7 +617,7 @@ __global__ void __launch_bounds__(512, MINB)
     }
 }
 
-template <int DT, int NCH, int R, int DEPTH, int MINB, bool ALIGNED>
+template <int DT, int NCH, int R, int DEPTH, int MINB, int MODE>
 __global__ void __launch_bounds__(512, MINB)
     ln_backward_rows_fused(const __grid_constant__ LnArgs a, int warps, int groups)
 {
@@ -561,6 +626,12 @@ __global__ void __launch_bounds__(512, MINB)
     __shared__ float red[2][8][kMaxWarps * 2 * R];
     const int width = warps * 32, grp = threadIdx.x / width, t = threadIdx.x % width, wg = t >> 5;
     const int chunks = (a.cols + V - 1) / V, words = row_words(chunks);
+    Walk<MODE, R> walk(grp, groups);
+    long long& r0 = walk.r0;
+    const long long step = walk.step;
+    // columns of the array's first word that belong to the row before
+    const int first = MODE == kAlike ? static_cast<int>((reinterpret_cast<uintptr_t>(static_cast<const typename El<DT>::T*>(a.x) + r0 * a.x_stride) & 15u) / sizeof(typename El<DT>::T)) : 0;
+    const int here = MODE == kAlike ? (first + a.cols + V - 1) / V : chunks;   // words of a row
     const float inv_c = 1.0f / static_cast<float>(a.cols);
     for (int i = threadIdx.x; i < 2 * 8 * kMaxWarps * 2 * R; i += blockDim.x) (&red[0][0][0])[i] = 0.0f;
     __syncthreads();
@@ -569,55 +640,71 @@ __global__ void __launch_bounds__(512, MINB)
     f32x2 gain[NCH][V / 2], dg2[NCH][V / 2], db2[NCH][V / 2];
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-        weights_at<V>(a.gain, a.w_dtype, (t + i * width) * V, a.cols, 1.0f, gain[i]);
+        weights_at<V>(a.gain, a.w_dtype, (t + i * width) * V - first, a.cols, 1.0f, gain[i]);
 #pragma unroll
         for (int e = 0; e < V / 2; ++e) dg2[i][e] = db2[i][e] = 0;
     }
     const RowSource<DT> x(a.x, a.x_stride, a.rows, a.cols), dy(a.dy, a.dy_stride, a.rows, a.cols);
-    // ALIGNED: [DEPTH][R][2][NCH][threads], else a group's [DEPTH][R][2][words] and [R][words] of results
-    uint4* ring = reinterpret_cast<uint4*>(smem) + (ALIGNED ? threadIdx.x : grp * (2 * DEPTH + 1) * R * words);
+    // [DEPTH][R][2][NCH][threads]; kMixed: a group's [DEPTH][R][2][words] and [R][words] of results
+    uint4* ring = reinterpret_cast<uint4*>(smem) + (MODE != kMixed ? threadIdx.x : grp * (2 * DEPTH + 1) * R * words);
     uint4* outs = ring + 2 * DEPTH * R * words;
     auto fetch = [&](long long r0, int s) {
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            if (r0 + k >= a.rows) break;
-            if (ALIGNED) {
+            const long long r = r0 + k * walk.apart;
+            if (r >= a.rows) break;
+            if (MODE != kMixed) {
 #pragma unroll
                 for (int i = 0; i < NCH; ++i)
-                    if (t + i * width < chunks) {
+                    if (t + i * width < here) {
                         uint4* p = ring + ((s * R + k) * 2 * NCH + i) * blockDim.x;
-                        cp_async16(p, x.base + (r0 + k) * x.stride + (t + i * width) * V);
-                        cp_async16(p + NCH * blockDim.x, dy.base + (r0 + k) * dy.stride + (t + i * width) * V);
+                        const typename El<DT>::T* q = x.base + r * x.stride;
+                        const typename El<DT>::T* d = dy.base + r * dy.stride;
+                        const int at = (t + i * width) * V;
+                        if (MODE == kAligned) {
+                            cp_async16(p, q + at);
+                            cp_async16(p + NCH * blockDim.x, d + at);
+                        } else {
+                            x.copy_word(p, reinterpret_cast<uintptr_t>(q - first + at), reinterpret_cast<uintptr_t>(q), reinterpret_cast<uintptr_t>(q + a.cols));
+                            dy.copy_word(p + NCH * blockDim.x, reinterpret_cast<uintptr_t>(d - first + at), reinterpret_cast<uintptr_t>(d), reinterpret_cast<uintptr_t>(d + a.cols));
+                        }
                     }
             } else {
                 uint4* p = ring + (s * R + k) * 2 * words;
-                x.copy_words(p, r0 + k, a.cols, t, width);
-                dy.copy_words(p + words, r0 + k, a.cols, t, width);
+                x.copy_words(p, r, a.cols, t, width);
+                dy.copy_words(p + words, r, a.cols, t, width);
             }
         }
         cp_async_commit();
     };
-    const long long step = static_cast<long long>(gridDim.x) * groups * R;
-    long long r0 = (static_cast<long long>(blockIdx.x) * groups + grp) * R;
     for (int s = 0; s < DEPTH - 1; ++s) fetch(r0 + s * step, s);
     float mean[R], rstd[R];
 #pragma unroll
-    for (int k = 0; k < R; ++k) mean[k] = r0 + k < a.rows ? a.mean[r0 + k] : 0.0f, rstd[k] = r0 + k < a.rows ? a.rstd[r0 + k] : 0.0f;
+    for (int k = 0; k < R; ++k) {
+        const long long r = r0 + k * walk.apart;
+        mean[k] = r < a.rows ? a.mean[r] : 0.0f;
+        rstd[k] = r < a.rows ? a.rstd[r] : 0.0f;
+    }
     int buf = 0;
     for (int s = 0; r0 < a.rows; r0 += step, s = s + 1 == DEPTH ? 0 : s + 1, buf ^= 1) {
         cp_async_wait<DEPTH - 2>();
-        if (!ALIGNED) group_sync(grp, warps, width);
+        if (MODE == kMixed) group_sync(grp, warps, width);
         uint4 wx[R][NCH], wd[R][NCH];
 #pragma unroll
         for (int k = 0; k < R; ++k)
 #pragma unroll
             for (int i = 0; i < NCH; ++i) {
                 wx[k][i] = wd[k][i] = make_uint4(0, 0, 0, 0);
-                if (t + i * width >= chunks || r0 + k >= a.rows) continue;
-                if (ALIGNED) {
+                if (t + i * width >= here || r0 + k * walk.apart >= a.rows) continue;
+                if (MODE != kMixed) {
                     const uint4* p = ring + ((s * R + k) * 2 * NCH + i) * blockDim.x;
                     wx[k][i] = p[0];
                     wd[k][i] = p[NCH * blockDim.x];
+                    if (MODE == kAlike) {
+                        const int c = (t + i * width) * V - first;
+                        wx[k][i] = masked<DT>(wx[k][i], c, a.cols);
+                        wd[k][i] = masked<DT>(wd[k][i], c, a.cols);
+                    }
                 } else {
                     const uint4* p = ring + (s * R + k) * 2 * words + t + i * width;
                     const int c = (t + i * width) * V;
@@ -629,7 +716,7 @@ __global__ void __launch_bounds__(512, MINB)
         float next_mean[R], next_rstd[R];
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            const long long r = r0 + step + k;
+            const long long r = r0 + step + k * walk.apart;
             next_mean[k] = r < a.rows ? a.mean[r] : 0.0f;
             next_rstd[k] = r < a.rows ? a.rstd[r] : 0.0f;
         }
@@ -660,14 +747,15 @@ __global__ void __launch_bounds__(512, MINB)
         const RowSource<DT> out(a.out, a.out_stride, a.rows, a.cols);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            if (r0 + k >= a.rows) break;
+            const long long r = r0 + k * walk.apart;
+            if (r >= a.rows) break;
             // dx = rstd * (dy * gain - s1 - xhat * s2)
             const float s1 = sum[2 * k] * inv_c, s2 = sum[2 * k + 1] * inv_c;
             const f32x2 m = pack2(mean[k], mean[k]), rs = pack2(rstd[k], rstd[k]), n1 = pack2(-s1, -s1);
             const f32x2 n2 = pack2(-s2 * rstd[k], -s2 * rstd[k]);
 #pragma unroll
             for (int i = 0; i < NCH; ++i) {
-                const int c = (t + i * width) * V;
+                const int c = (t + i * width) * V - first;
                 if (c >= a.cols) break;
                 f32x2 xv[V / 2], dv[V / 2];
                 float o[V];
@@ -679,13 +767,15 @@ __global__ void __launch_bounds__(512, MINB)
                 for (int e = 0; e < V / 2; ++e)
                     xv[e] = mul2(rs, fma2(sub2(xv[e], m), n2, fma2(dv[e], gain[i][e], n1)));
                 unpack(xv, o);
-                if (ALIGNED)
-                    __stcs(reinterpret_cast<uint4*>(out.row(r0 + k)) + t + i * width, narrowed<DT>(o));
+                if (MODE == kAligned)
+                    __stcs(reinterpret_cast<uint4*>(out.row(r)) + t + i * width, narrowed<DT>(o));
+                else if (MODE == kAlike)
+                    put_word<DT>(out.row(r), c, a.cols, narrowed<DT>(o));
                 else
                     outs[k * words + 1 + t + i * width] = narrowed<DT>(o);
             }
         }
-        if (!ALIGNED) {
+        if (MODE == kMixed) {
             group_sync(grp, warps, width);
 #pragma unroll
             for (int k = 0; k < R; ++k)
@@ -737,8 +827,8 @@ __global__ void __launch_bounds__(512, MINB)
         for (int i = 0; i < NCH; ++i)
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                const int c = (t + i * width) * V + e;
-                if (c >= a.cols) break;
+                const int c = (t + i * width) * V + e - first;
+                if (c < 0 || c >= a.cols) continue;
                 p[c] = dg[i][e];
                 p[a.cols + c] = db[i][e];
             }
@@ -784,8 +874,6 @@ int sms_of_device()
     return n;
 }
 
-bool wide(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
-
 constexpr size_t kRowSmem = 220 * 1024;   // of the 227 KB a CTA may have
 
 // how a launch cuts its rows up
@@ -796,7 +884,7 @@ struct RowShape {
 
 // Groups share a CTA of up to 512 threads, fewer where the rows would not
 // cover the SMs otherwise.
-RowShape row_shape(const LnArgs& a, int chunks, int nch, int r, int per_sm, size_t group_smem, int sms)
+RowShape row_shape(const LnArgs& a, int chunks, int nch, int r, int per_sm, size_t group_smem, int sms, bool eights)
 {
     RowShape s;
     s.warps = (chunks + 32 * nch - 1) / (32 * nch);
@@ -808,7 +896,26 @@ RowShape row_shape(const LnArgs& a, int chunks, int nch, int r, int per_sm, size
     s.threads = 32 * s.warps * s.groups;
     s.grid = (sets + s.groups - 1) / s.groups;
     if (s.grid > static_cast<long long>(sms) * per_sm) s.grid = static_cast<long long>(sms) * per_sm;
+    if (eights) s.grid = s.grid < 8 ? 8 : s.grid / 8 * 8;   // eight kinds of rows
     return s;
+}
+
+// words a thread's chunks have to cover: kAlike rows may begin inside one
+template <int DT>
+int chunks_of(int cols, int mode)
+{
+    return (cols + kV<DT> - 1 + (mode == kAlike ? kV<DT> - 1 : 0)) / kV<DT>;
+}
+
+// How equal rows of the arrays (null: none) lie; strides in elements.
+template <int DT>
+int mode_of(int cols, const void* p, long long ps, const void* q, long long qs, const void* r, long long rs)
+{
+    constexpr int V = kV<DT>;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q), c = r != nullptr ? reinterpret_cast<uintptr_t>(r) : a;
+    if (r == nullptr) rs = ps;
+    if (cols % V == 0 && ps % V == 0 && qs % V == 0 && rs % V == 0 && a % 16 == 0 && b % 16 == 0 && c % 16 == 0) return kAligned;
+    return a % 16 == b % 16 && a % 16 == c % 16 && ps % V == qs % V && ps % V == rs % V ? kAlike : kMixed;
 }
 
 template <typename K>
@@ -821,29 +928,29 @@ cudaError_t launch_rows(K kernel, const LnArgs& a, const RowShape& s, size_t sme
     return launch_after(kernel, dim3(static_cast<unsigned>(s.grid)), dim3(s.threads), smem, st, a, s.warps, s.groups);
 }
 
-template <int DT, int NCH, int R, int DEPTH, int MINB, bool ALIGNED>
+template <int DT, int NCH, int R, int DEPTH, int MINB, int MODE>
 cudaError_t forward_as(const LnArgs& a, int sms, cudaStream_t st)
 {
-    const int chunks = (a.cols + kV<DT> - 1) / kV<DT>;
+    const int chunks = chunks_of<DT>(a.cols, MODE);
     const int warps = (chunks + 32 * NCH - 1) / (32 * NCH);
-    const size_t per = 16u * R * (ALIGNED ? static_cast<size_t>(DEPTH) * NCH * 32 * warps : static_cast<size_t>(DEPTH + 1) * row_words(chunks));
-    const RowShape s = row_shape(a, chunks, NCH, R, MINB, per, sms);
-    return launch_rows(ln_forward_rows<DT, NCH, R, DEPTH, MINB, ALIGNED>, a, s, per * s.groups, st);
+    const size_t per = 16u * R * (MODE != kMixed ? static_cast<size_t>(DEPTH) * NCH * 32 * warps : static_cast<size_t>(DEPTH + 1) * row_words(chunks));
+    const RowShape s = row_shape(a, chunks, NCH, R, MINB, per, sms, MODE == kAlike);
+    return launch_rows(ln_forward_rows<DT, NCH, R, DEPTH, MINB, MODE>, a, s, per * s.groups, st);
 }
 
-template <int DT, int NCH, int R, int DEPTH, int MINB, bool ALIGNED>
+template <int DT, int NCH, int R, int DEPTH, int MINB, int MODE>
 cudaError_t backward_as(const LnArgs& a, int sms, cudaStream_t st, int& parts)
 {
-    const int chunks = (a.cols + kV<DT> - 1) / kV<DT>;
+    const int chunks = chunks_of<DT>(a.cols, MODE);
     const int warps = (chunks + 32 * NCH - 1) / (32 * NCH);
-    const size_t per = 16u * R * (ALIGNED ? static_cast<size_t>(2 * DEPTH) * NCH * 32 * warps : static_cast<size_t>(2 * DEPTH + 1) * row_words(chunks));
-    RowShape s = row_shape(a, chunks, NCH, R, MINB, per, sms);
+    const size_t per = 16u * R * (MODE != kMixed ? static_cast<size_t>(2 * DEPTH) * NCH * 32 * warps : static_cast<size_t>(2 * DEPTH + 1) * row_words(chunks));
+    RowShape s = row_shape(a, chunks, NCH, R, MINB, per, sms, MODE == kAlike);
     if (s.grid > kLnMaxParts) s.grid = kLnMaxParts;
     parts = static_cast<int>(s.grid);
     size_t smem = per * s.groups;
     const size_t sums = static_cast<size_t>(s.groups / 2) * 2 * NCH * kV<DT> * 32 * s.warps * sizeof(float);
     if (smem < sums) smem = sums;
-    return launch_rows(ln_backward_rows_fused<DT, NCH, R, DEPTH, MINB, ALIGNED>, a, s, smem, st);
+    return launch_rows(ln_backward_rows_fused<DT, NCH, R, DEPTH, MINB, MODE>, a, s, smem, st);
 }
 
 // A thread holds 16 columns of a row (one chunk of it where the row has no more
@@ -863,13 +970,17 @@ cudaError_t forward_of(const LnArgs& a, cudaStream_t st)
     constexpr int V = kV<DT>;
     const int sms = sms_of_device();
     if (sms == 0) return cudaErrorInvalidDevice;
-    const bool al = a.cols % V == 0 && a.x_stride % V == 0 && a.out_stride % V == 0 && wide(a.x) && wide(a.out);
-    const int chunks = (a.cols + V - 1) / V;
+    const int mode = mode_of<DT>(a.cols, a.x, a.x_stride, a.out, a.out_stride, nullptr, 0);
     constexpr int N = kNch<DT>;
-    if (chunks <= 32) return al ? forward_as<DT, 1, 2, 4, 2, true>(a, sms, st) : forward_as<DT, 1, 2, 3, 2, false>(a, sms, st);
-    if (a.cols <= kMaxCols) {
-        if (al) return forward_as<DT, N, 2, 3, 1, true>(a, sms, st);
-        return a.cols <= kDeepCols<DT> ? forward_as<DT, N, 1, 5, 1, false>(a, sms, st) : forward_as<DT, N, 1, 3, 1, false>(a, sms, st);
+    if (chunks_of<DT>(a.cols, mode) <= 32) {
+        if (mode == kAligned) return forward_as<DT, 1, 2, 4, 2, kAligned>(a, sms, st);
+        if (mode == kAlike) return forward_as<DT, 1, 2, 4, 2, kAlike>(a, sms, st);
+        return forward_as<DT, 1, 2, 3, 2, kMixed>(a, sms, st);
+    }
+    if (chunks_of<DT>(a.cols, mode) <= kMaxCols / V) {
+        if (mode == kAligned) return forward_as<DT, N, 2, 3, 1, kAligned>(a, sms, st);
+        if (mode == kAlike) return forward_as<DT, N, 2, 3, 1, kAlike>(a, sms, st);
+        return a.cols <= kDeepCols<DT> ? forward_as<DT, N, 1, 5, 1, kMixed>(a, sms, st) : forward_as<DT, N, 1, 3, 1, kMixed>(a, sms, st);
     }
     const long long grid = a.rows < (1 << 30) ? a.rows : (1 << 30);
     return launch_after(ln_forward_any<DT>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, a);
@@ -883,20 +994,25 @@ cudaError_t backward_of(const LnArgs& a, cudaStream_t st)
     if (sms == 0) return cudaErrorInvalidDevice;
     int parts = static_cast<int>(a.rows < kLnMaxParts ? a.rows : kLnMaxParts);
     if (a.rows > 0) {
-        const bool al = a.cols % V == 0 && a.x_stride % V == 0 && a.dy_stride % V == 0 && a.out_stride % V == 0 &&
-                        wide(a.x) && wide(a.dy) && wide(a.out);
-        const int chunks = (a.cols + V - 1) / V;
+        const int mode = mode_of<DT>(a.cols, a.x, a.x_stride, a.out, a.out_stride, a.dy, a.dy_stride);
         constexpr int N = kNch<DT>;
         cudaError_t e;
-        if (chunks <= 32) {
-            e = al ? backward_as<DT, 1, 2, 3, 1, true>(a, sms, st, parts) : backward_as<DT, 1, 2, 3, 1, false>(a, sms, st, parts);
-        } else if (a.cols <= kMaxCols) {
-            if (al)
-                e = backward_as<DT, N, 1, 3, 1, true>(a, sms, st, parts);
-            else if (a.cols <= kDeepCols<DT>)
-                e = backward_as<DT, N, 1, 5, 1, false>(a, sms, st, parts);
+        if (chunks_of<DT>(a.cols, mode) <= 32) {
+            if (mode == kAligned)
+                e = backward_as<DT, 1, 2, 3, 1, kAligned>(a, sms, st, parts);
+            else if (mode == kAlike)
+                e = backward_as<DT, 1, 2, 3, 1, kAlike>(a, sms, st, parts);
             else
-                e = backward_as<DT, N, 1, 2, 1, false>(a, sms, st, parts);
+                e = backward_as<DT, 1, 2, 3, 1, kMixed>(a, sms, st, parts);
+        } else if (chunks_of<DT>(a.cols, mode) <= kMaxCols / V) {
+            if (mode == kAligned)
+                e = backward_as<DT, N, 1, 3, 1, kAligned>(a, sms, st, parts);
+            else if (mode == kAlike)
+                e = backward_as<DT, N, 1, 3, 1, kAlike>(a, sms, st, parts);
+            else if (a.cols <= kDeepCols<DT>)
+                e = backward_as<DT, N, 1, 5, 1, kMixed>(a, sms, st, parts);
+            else
+                e = backward_as<DT, N, 1, 2, 1, kMixed>(a, sms, st, parts);
         } else {
             const long long grid = a.rows < (1 << 30) ? a.rows : (1 << 30);
             e = launch_after(ln_backward_rows<DT>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, a);
