@@ -87,29 +87,65 @@ __device__ __forceinline__ void load_row8(const void* in, int dtype, bool vec, l
     }
 }
 
-// the squares of eight values; in fp32 unless that overflows
-__device__ __forceinline__ double squares8(const float (&v)[8])
-{
-    float s = 0.0f;
+// A sum of squares in fp32, compensated; `big` the same of the values times
+// 2^-70, for matrices whose squares pass fp32's range.  (fp64 would cost more
+// than all else here: it runs at a small fraction of fp32's rate.)
+struct SquareSum {
+    float sum = 0.0f, lost = 0.0f, big = 0.0f;
+    __device__ __forceinline__ void add8(const float (&v)[8])
+    {
+        float q = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s = fmaf(v[e], v[e], s);
-    if (is_finite_f32(s)) return static_cast<double>(s);
-    double d = 0.0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) d += static_cast<double>(v[e]) * static_cast<double>(v[e]);
-    return d;
-}
+        for (int e = 0; e < 8; ++e) {
+            const float w = v[e] * 8.470329472543003e-22f;   // 2^-70
+            q = fmaf(v[e], v[e], q);
+            big = fmaf(w, w, big);
+        }
+        const float a = fmaxf(sum, q), b = fminf(sum, q), t = a + b;   // NaN: kept by `big`
+        lost += b - (t - a);
+        sum = t;
+    }
+    __device__ __forceinline__ float2 value() const { return make_float2(sum + lost, big); }
+};
 
-// sum over a block, in every thread; red: a double for each warp
-__device__ __forceinline__ double block_sum_f64(double v, double* red)
+// sums over a block, in thread 0; red: a float2 for each warp
+__device__ __forceinline__ float2 block_sum2(float2 v, float2* red)
 {
-    v = warp_sum_f64(v);
-    __syncthreads();
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, o);
+        v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, o);
+    }
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
-    double s = 0.0;
-    for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) s += red[i];
-    return s;
+    if (threadIdx.x < 32) {
+        v = threadIdx.x < (blockDim.x >> 5) ? red[threadIdx.x] : make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, o);
+            v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, o);
+        }
+    }
+    return v;
+}
+
+// kScale / (|g| + eps) from the two sums of squares (thread 0's), in every
+// thread; a NaN in g makes it NaN
+__device__ __forceinline__ float block_scale(float2 sums, float eps, float* shared)
+{
+    if (threadIdx.x == 0) {
+        const float s = sums.x;
+        float f;
+        if (sums.y != sums.y)
+            f = sums.y;
+        else if (is_finite_f32(s))
+            f = kScale / (sqrtf(s) + eps);
+        else   // sqrt(big) * 2^70, and eps, which is nothing beside it
+            f = is_finite_f32(sums.y) ? kScale * 8.470329472543003e-22f / sqrtf(sums.y) : 0.0f;
+        *shared = f;
+    }
+    __syncthreads();
+    return *shared;
 }
 
 struct MuonArgs {
@@ -120,7 +156,7 @@ struct MuonArgs {
     float* u;
     long long stride, u_stride;
     uint32_t elems;              // of one matrix
-    double* parts;
+    float2* parts;
     unsigned* counters;
     int n_counters;
 };

@@ -65,7 +65,7 @@ struct NsKernelArgs {
     int in_dtype, in_vec, chunks;
     long long in_ld, in_stride;
     float eps;
-    const double* parts;         // [batch][parts_n] sums of squares
+    const float2* parts;         // [batch][parts_n] sums of squares
     int parts_n;
     // the result
     int res;                     // RES_OUT or RES_MUON
@@ -395,7 +395,7 @@ struct PrepArgs {
     int dtype, vec;
     long long ld, stride;
     int rows, cols, chunks;      // chunks: groups of eight columns in a row
-    double* parts;               // [batch][gridDim.x]
+    float2* parts;               // [batch][gridDim.x] sums of squares
     unsigned* counters;          // cleared for the products' kernel
     int n_counters;
 };
@@ -408,36 +408,36 @@ __device__ __forceinline__ void clear_counters(unsigned* c, int n)
 
 __global__ void __launch_bounds__(256) ns_sqnorm(const __grid_constant__ PrepArgs a)
 {
-    __shared__ double red[8];
+    __shared__ float2 red[8];
     pdl_wait();
     clear_counters(a.counters, a.n_counters);
     const uint32_t total = static_cast<uint32_t>(a.rows) * a.chunks;
     const long long base = blockIdx.y * a.stride;
-    double s = 0.0;
+    SquareSum s;
     for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < total; i += gridDim.x * 256) {
         const uint32_t row = i / static_cast<uint32_t>(a.chunks);
         float v[8];
         load_row8(a.in, a.dtype, a.vec, base + row * a.ld, a.cols, i - row * a.chunks, v);
-        s += squares8(v);
+        s.add8(v);
     }
-    s = block_sum_f64(s, red);
-    if (threadIdx.x == 0) a.parts[blockIdx.y * static_cast<long long>(gridDim.x) + blockIdx.x] = s;
+    const float2 sums = block_sum2(s.value(), red);
+    if (threadIdx.x == 0) a.parts[blockIdx.y * static_cast<long long>(gridDim.x) + blockIdx.x] = sums;
 }
 
 // the update direction of every matrix, with the sums of its squares
 __global__ void __launch_bounds__(256) muon_direction(const __grid_constant__ MuonArgs a)
 {
-    __shared__ double red[8];
+    __shared__ float2 red[8];
     pdl_wait();
     clear_counters(a.counters, a.n_counters);
-    double s = 0.0;
+    SquareSum s;
     for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i * 8u < a.elems; i += gridDim.x * 256) {
         float u[8];
         muon_direction8(a, blockIdx.y, i, u);
-        s += squares8(u);
+        s.add8(u);
     }
-    s = block_sum_f64(s, red);
-    if (threadIdx.x == 0) a.parts[blockIdx.y * static_cast<long long>(gridDim.x) + blockIdx.x] = s;
+    const float2 sums = block_sum2(s.value(), red);
+    if (threadIdx.x == 0) a.parts[blockIdx.y * static_cast<long long>(gridDim.x) + blockIdx.x] = sums;
 }
 
 // ------------------------------------------------------------ the products
@@ -542,6 +542,44 @@ __device__ __forceinline__ void set_phase(Phase& ph, const NsKernelArgs& a, int 
     if (first < ph.tiles) ph.first = tile_of<CG, BN>(ph, first);
 }
 
+// x_0 = g / (|g| + eps) of matrix b, scaled, as a pair: this CTA's part.  Once
+// a matrix, so kept out of the phases' registers.
+__device__ __noinline__ void first_operand(const NsKernelArgs& a, int b, int cta, float2* red, float* shared_scale)
+{
+    float2 q = make_float2(0.0f, 0.0f);
+    for (int i = threadIdx.x; i < a.parts_n; i += kThreads) {
+        const float2 p = a.parts[static_cast<long long>(b) * a.parts_n + i];
+        q.x += p.x;
+        q.y += p.y;
+    }
+    const float f = block_scale(block_sum2(q, red), a.eps, shared_scale);
+    const uint32_t chunks = a.chunks, total = static_cast<uint32_t>(a.rows) * chunks, stride = a.ctas * kThreads;
+    const void* in = a.in;
+    const int dtype = a.in_dtype, cols = a.cols;
+    const bool vec = a.in_vec;
+    const long long base = b * a.in_stride, ld = a.in_ld, out_ld = a.x[0].ld;
+    __half* hi = a.x[0].hi + b * a.x[0].stride;
+    __half* lo = a.x[0].lo + b * a.x[0].stride;
+    for (uint32_t i = cta * kThreads + threadIdx.x; i < total; i += 4 * stride) {   // four loads under way
+        float v[4][8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t j = i + k * stride, row = j / chunks;
+            if (j < total) load_row8(in, dtype, vec, base + row * ld, cols, j - row * chunks, v[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t j = i + k * stride, row = j / chunks;
+            if (j >= total) break;
+            Eight u;
+            u.set(make_float4(v[k][0], v[k][1], v[k][2], v[k][3]), make_float4(v[k][4], v[k][5], v[k][6], v[k][7]));
+            u.scale(pack2(f, f));
+            const long long o = row * out_ld + 8 * (j - row * chunks);
+            put_planes8(u, hi + o, lo + o);
+        }
+    }
+}
+
 // The whole iteration in one launch.  The grid is `groups` of `ctas` CTAs, all
 // resident (a cooperative launch); a group takes its matrices one after the
 // other and meets at a counter in memory between products.  Within a product
@@ -561,7 +599,8 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
     __shared__ volatile int abort_flag;
     __shared__ Phase plan[2];
     __shared__ int stop_flag;
-    __shared__ double red[kThreads / 32];
+    __shared__ float2 red[kThreads / 32];
+    __shared__ float shared_scale;
     unsigned char* ring = smem_raw + (1024 - (smem_u32(smem_raw) & 1023u)) % 1024;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = blockIdx.x / a.ctas, cta = blockIdx.x % a.ctas;
@@ -603,24 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
     }
 
     for (int b = group; b < a.batch && !stop; b += a.groups) {
-        {   // x_0 = g / (|g| + eps), scaled
-            double q = 0.0;
-            for (int i = threadIdx.x; i < a.parts_n; i += kThreads) q += a.parts[static_cast<long long>(b) * a.parts_n + i];
-            q = block_sum_f64(q, red);
-            const float f = static_cast<float>(static_cast<double>(kScale) / (sqrt(q) + static_cast<double>(a.eps)));
-            const uint32_t total = static_cast<uint32_t>(a.rows) * a.chunks;
-            for (uint32_t i = cta * kThreads + threadIdx.x; i < total; i += a.ctas * kThreads) {
-                const uint32_t row = i / static_cast<uint32_t>(a.chunks);
-                const int ch = i - row * a.chunks;
-                float v[8];
-                load_row8(a.in, a.in_dtype, a.in_vec, b * a.in_stride + row * a.in_ld, a.cols, ch, v);
-                Eight u;
-                u.set(make_float4(v[0], v[1], v[2], v[3]), make_float4(v[4], v[5], v[6], v[7]));
-                u.scale(pack2(f, f));
-                const long long o = b * a.x[0].stride + row * a.x[0].ld + 8 * ch;
-                put_planes8(u, a.x[0].hi + o, a.x[0].lo + o);
-            }
-        }
+        first_operand(a, b, cta, red, &shared_scale);
         for (int phase = 0; phase < 3 * a.steps; ++phase) {
             // the group's results of the phase before, for everyone's TMA loads
             fence_proxy_async_global();
@@ -979,7 +1001,7 @@ Layout layout_of(int rows, int cols, int batch, int products, bool muon)
     l.counters = at;
     at += up256(static_cast<size_t>(kMaxSms) * (kBarStride + 1) * sizeof(unsigned));
     l.parts = at;
-    at += up256(static_cast<size_t>(batch) * kMaxNsParts * sizeof(double));
+    at += up256(static_cast<size_t>(batch) * kMaxNsParts * sizeof(float2));
     l.partial = at;
     at += static_cast<size_t>(kMaxSms) * kBM * 256 * sizeof(float);
     l.u = at;
@@ -1103,7 +1125,7 @@ cudaError_t launch_ns(const NsArgs& a, cudaStream_t st)
     const Layout l = layout_of(a.rows, a.cols, a.batch, a.products, muon);
     char* ws = static_cast<char*>(a.ws);
     unsigned* counters = reinterpret_cast<unsigned*>(ws + l.counters);
-    double* parts = reinterpret_cast<double*>(ws + l.parts);
+    float2* parts = reinterpret_cast<float2*>(ws + l.parts);
     MuonArgs mu;
     if (muon) {
         std::memset(&mu, 0, sizeof(mu));

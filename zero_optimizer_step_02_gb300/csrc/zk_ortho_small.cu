@@ -113,7 +113,8 @@ __device__ __forceinline__ void ns_small_body(const SmallNsArgs& a, const MuonAr
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint64_t bar, drain;
     __shared__ uint32_t tmem_base;
-    __shared__ double red[kSmallThreads / 32];
+    __shared__ float2 red[kSmallThreads / 32];
+    __shared__ float shared_scale;
     unsigned char* x = smem_raw + (1024 - (smem_u32(smem_raw) & 1023u)) % 1024;
     const int x_lo = a.panels * kPanelBytes, g_lo = kSquarePanels * kPanelBytes;
     unsigned char* g = x + 2 * x_lo;
@@ -131,23 +132,22 @@ __device__ __forceinline__ void ns_small_body(const SmallNsArgs& a, const MuonAr
 
     // |g|, then x = g / (|g| + eps), scaled
     const int chunks = (a.cols + 7) / 8, total = a.rows * chunks;
-    double q = 0.0;
+    SquareSum q;
     if (MUON) {
         for (uint32_t i = t; 8 * i < mu->elems; i += kSmallThreads) {
             float u[8];
             muon_direction8(*mu, b, i, u);
-            q += squares8(u);
+            q.add8(u);
         }
     } else {
         for (int i = t; i < total; i += kSmallThreads) {
             const int row = i / chunks;
             float v[8];
             load_row8(a.in, a.in_dtype, a.in_vec, b * a.in_stride + row * a.in_ld, a.cols, i - row * chunks, v);
-            q += squares8(v);
+            q.add8(v);
         }
     }
-    q = block_sum_f64(q, red);
-    const float f = static_cast<float>(static_cast<double>(kScale) / (sqrt(q) + static_cast<double>(a.eps)));
+    const float f = block_scale(block_sum2(q.value(), red), a.eps, &shared_scale);
     for (int i = t; i < total; i += kSmallThreads) {
         const int row = i / chunks, col = (i - row * chunks) * 8;
         float v[8];
