@@ -91,6 +91,17 @@ def test_shapes(batch, rows, cols, products):
     check(o, plain(x), tolerance(rows, cols, products, FP32))
 
 
+# either side of the form that keeps a matrix in one SM (128 x 256), more
+# matrices than SMs, every width of its panels
+@pytest.mark.parametrize("batch,rows,cols", [(1, 128, 256), (1, 256, 128), (1, 129, 256), (1, 256, 129), (1, 128, 257),
+                                             (1, 257, 128), (200, 64, 64), (170, 20, 250), (3, 1, 256), (3, 256, 1),
+                                             (1, 16, 16), (1, 15, 17), (2, 113, 65), (2, 191, 127), (1, 100, 193)])
+def test_small_shapes(batch, rows, cols):
+    g = gradients(batch, rows, cols)
+    x, o = orthogonalize(g, FP32, FP32, 3)
+    check(o, plain(x), tolerance(rows, cols, 3, FP32))
+
+
 @pytest.mark.parametrize("dt,out_dt", [(BF16, BF16), (FP16, FP16), (FP32, BF16), (BF16, FP32), (FP32, FP16)])
 @pytest.mark.parametrize("batch,rows,cols,ld,old,gap", [(2, 96, 160, 0, 0, 0), (2, 96, 160, 168, 176, 8), (3, 130, 77, 0, 0, 0),
                                                         (3, 130, 77, 81, 79, 5), (1, 64, 513, 520, 513, 0)])
