@@ -57,7 +57,7 @@ size_t ln_parts_bytes(const zero_layernorm* d)
 {
     // at least eight: some kernels deal rows out eight apart
     const long long parts = d->rows < 8 ? 8 : d->rows < zk::kLnMaxParts ? d->rows : zk::kLnMaxParts;
-    return round256(static_cast<size_t>(parts) * 2 * d->cols * sizeof(float));
+    return round256(static_cast<size_t>(parts) * 2 * zk::ln_pitch(d->cols) * sizeof(float));
 }
 
 zk::LnArgs ln_args(const zero_layernorm* d)
@@ -272,7 +272,8 @@ ZERO_API zero_status zero_debug_matmul_timeout(void* scratch, zero_dev_scalars* 
 ZERO_API size_t zero_layernorm_workspace_bytes(const zero_layernorm* d)
 {
     if (check_ln(d) != ZERO_OK) return 0;
-    return 256 + ln_parts_bytes(d) + round256(static_cast<size_t>(d->rows) * 2 * sizeof(float));
+    const size_t means = d->cols >= zk::kLnWide ? round256(static_cast<size_t>(d->rows) * 2 * sizeof(float)) : 0;
+    return 256 + ln_parts_bytes(d) + means;
 }
 
 ZERO_API zero_status zero_layernorm_forward(const zero_layernorm* d, const void* x, const void* gain, const void* bias,
@@ -332,6 +333,7 @@ ZERO_API zero_status zero_layernorm_backward(const zero_layernorm* d, const void
     a.out = dx;
     a.dgain = dgain;
     a.dbias = dbias;
+    a.pitch = zk::ln_pitch(d->cols);
     a.parts = reinterpret_cast<float*>(static_cast<char*>(ws) + 256);
     a.rowsums = reinterpret_cast<float*>(static_cast<char*>(ws) + 256 + ln_parts_bytes(d));
     return from_cuda(zk::launch_ln_backward(a, as_stream(stream)));

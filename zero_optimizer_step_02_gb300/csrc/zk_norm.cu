@@ -156,9 +156,9 @@ __global__ void __launch_bounds__(256) ln_backward_cols(const __grid_constant__ 
         const float dx = rstd * (dy * gain - a.rowsums[2 * r] - xhat * a.rowsums[2 * r + 1]);
         static_cast<typename E::T*>(a.out)[r * a.out_stride + c] = E::down(dx);
     }
-    float* p = a.parts + static_cast<long long>(blockIdx.y) * 2 * a.cols;
+    float* p = a.parts + static_cast<long long>(blockIdx.y) * 2 * a.pitch;
     p[c] = dg;
-    p[a.cols + c] = db;
+    p[a.pitch + c] = db;
 }
 
 // ------------------------------------------------------------- row pipelines
@@ -395,8 +395,27 @@ template <int V>
 __device__ __forceinline__ void weights_at(const void* w, int dt, int c, int cols, float none, f32x2 (&v)[V / 2])
 {
     float f[V];
+    const uintptr_t at = reinterpret_cast<uintptr_t>(w) + static_cast<intptr_t>(c) * (dt == ZERO_FP32 ? 4 : 2);
+    if (w != nullptr && c >= 0 && c + V <= cols && at % 16 == 0) {
+        if (dt == ZERO_FP32) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) f[e] = c + e < 0 || c + e >= cols ? 0.0f : w == nullptr ? none : weight_at(w, dt, c + e);
+            for (int e = 0; e < V; e += 4) {
+                const float4 x = *(reinterpret_cast<const float4*>(at) + e / 4);
+                f[e] = x.x, f[e + 1] = x.y, f[e + 2] = x.z, f[e + 3] = x.w;
+            }
+        } else {
+            const uint32_t* p = reinterpret_cast<const uint32_t*>(at);
+#pragma unroll
+            for (int e = 0; e < V / 2; ++e) {
+                const uint32_t x = p[e];
+                f[2 * e] = dt == ZERO_BF16 ? Lp<ZERO_BF16>::lo(x) : Lp<ZERO_FP16>::lo(x);
+                f[2 * e + 1] = dt == ZERO_BF16 ? Lp<ZERO_BF16>::hi(x) : Lp<ZERO_FP16>::hi(x);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) f[e] = c + e < 0 || c + e >= cols ? 0.0f : w == nullptr ? none : weight_at(w, dt, c + e);
+    }
 #pragma unroll
     for (int e = 0; e < V / 2; ++e) v[e] = pack2(f[2 * e], f[2 * e + 1]);
 }
@@ -792,7 +811,7 @@ __global__ void __launch_bounds__(512, MINB)
     }
     // the CTA's column sums: its row groups add up pairwise through the ring's
     // memory (free by then), then one row of partial sums leaves
-    float* p = a.parts + static_cast<long long>(blockIdx.x) * 2 * a.cols;
+    float* p = a.parts + static_cast<long long>(blockIdx.x) * 2 * a.pitch;
     float* acc = reinterpret_cast<float*>(smem);
     if (groups > 1) {
         cp_async_wait<0>();
@@ -823,36 +842,40 @@ __global__ void __launch_bounds__(512, MINB)
         }
     }
     if (grp == 0) {
+        // chunk by chunk: column c lies at c + first (the sums past a row are zeros)
 #pragma unroll
-        for (int i = 0; i < NCH; ++i)
+        for (int i = 0; i < NCH; ++i) {
+            const int c = (t + i * width) * V;
+            if (t + i * width >= here) break;
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const int c = (t + i * width) * V + e - first;
-                if (c < 0 || c >= a.cols) continue;
-                p[c] = dg[i][e];
-                p[a.cols + c] = db[i][e];
+            for (int e = 0; e < V; e += 4) {
+                *reinterpret_cast<float4*>(p + c + e) = make_float4(dg[i][e], dg[i][e + 1], dg[i][e + 2], dg[i][e + 3]);
+                *reinterpret_cast<float4*>(p + a.pitch + c + e) = make_float4(db[i][e], db[i][e + 1], db[i][e + 2], db[i][e + 3]);
             }
+        }
     }
 }
 
 // The partial column sums, in a fixed order: 32 columns a CTA, sixteen slices
 // of the parts side by side.
-__global__ void __launch_bounds__(512) ln_backward_finish(const __grid_constant__ LnArgs a, int parts)
+__global__ void __launch_bounds__(512) ln_backward_finish(const __grid_constant__ LnArgs a, int parts, uint32_t firsts)
 {
     __shared__ float red[16][33];
     const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
     const int i = blockIdx.x * 32 + lane;
-    const float* p = a.parts + i;
+    const bool bias = i >= a.cols;
+    const float* p = a.parts + (bias ? i - a.cols + a.pitch : i);
     pdl_wait();
     float s = 0.0f;
     if (i < 2 * a.cols) {
+        // a CTA's sums begin where its rows do (all eight kinds in turn: bits
+        // 4 k .. of `firsts`)
 #pragma unroll 10
-        for (int k = slice; k < parts; k += 16) s += p[static_cast<long long>(k) * 2 * a.cols];
+        for (int k = slice; k < parts; k += 16) s += p[static_cast<long long>(k) * 2 * a.pitch + (firsts >> 4 * (k & 7) & 15u)];
     }
     red[slice][lane] = s;
     __syncthreads();
     if (slice != 0 || i >= 2 * a.cols) return;
-    const bool bias = i >= a.cols;
     void* out = bias ? a.dbias : a.dgain;
     if (out == nullptr) return;
     float v[16];
@@ -957,6 +980,7 @@ cudaError_t backward_as(const LnArgs& a, int sms, cudaStream_t st, int& parts)
 // than a warp's worth), so that what a row costs each thread besides its
 // columns is spread; sixteen warps then hold kMaxCols columns.
 constexpr int kMaxCols = 8192;
+static_assert(kMaxCols - 2 * 8 >= kLnWide, "narrower rows never take the general kernels");
 template <int DT>
 constexpr int kNch = 16 / kV<DT>;
 // columns up to which a group's five unaligned stages (eleven rows of words,
@@ -987,14 +1011,19 @@ cudaError_t forward_of(const LnArgs& a, cudaStream_t st)
 }
 
 template <int DT>
-cudaError_t backward_of(const LnArgs& a, cudaStream_t st)
+cudaError_t backward_of(const LnArgs& args, cudaStream_t st)
 {
+    LnArgs a = args;
+    uint32_t firsts = 0;
     constexpr int V = kV<DT>;
     const int sms = sms_of_device();
     if (sms == 0) return cudaErrorInvalidDevice;
     int parts = static_cast<int>(a.rows < kLnMaxParts ? a.rows : kLnMaxParts);
     if (a.rows > 0) {
         const int mode = mode_of<DT>(a.cols, a.x, a.x_stride, a.out, a.out_stride, a.dy, a.dy_stride);
+        if (mode == kAlike)
+            for (int k = 0; k < 8; ++k)
+                firsts |= static_cast<uint32_t>((reinterpret_cast<uintptr_t>(a.x) + k * a.x_stride * dtype_bytes(DT)) % 16 / dtype_bytes(DT)) << 4 * k;
         constexpr int N = kNch<DT>;
         cudaError_t e;
         if (chunks_of<DT>(a.cols, mode) <= 32) {
@@ -1015,13 +1044,14 @@ cudaError_t backward_of(const LnArgs& a, cudaStream_t st)
                 e = backward_as<DT, N, 1, 2, 1, kMixed>(a, sms, st, parts);
         } else {
             const long long grid = a.rows < (1 << 30) ? a.rows : (1 << 30);
+            firsts = 0;
             e = launch_after(ln_backward_rows<DT>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, a);
             if (e == cudaSuccess) e = launch_after(ln_backward_cols<DT>, dim3((a.cols + 255) / 256, parts), dim3(256), 0, st, a);
         }
         if (e != cudaSuccess) return e;
     }
     if (a.dgain == nullptr && a.dbias == nullptr) return cudaSuccess;
-    return launch_after(ln_backward_finish, dim3((2 * a.cols + 31) / 32), dim3(512), 0, st, a, parts);
+    return launch_after(ln_backward_finish, dim3((2 * a.cols + 31) / 32), dim3(512), 0, st, a, parts, firsts);
 }
 
 }  // namespace

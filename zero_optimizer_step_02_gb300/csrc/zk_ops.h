@@ -25,7 +25,8 @@ struct LnArgs {
     float* rstd_out;
     void* dgain;         // backward; may be null
     void* dbias;
-    float* parts;        // backward: [parts][2][cols] partial column sums
+    float* parts;        // backward: [parts][2][pitch] partial column sums
+    int pitch;           // ln_pitch(cols)
     float* rowsums;      // backward: [rows][2]
     long long rows;
     long long x_stride, dy_stride, out_stride;
@@ -34,6 +35,11 @@ struct LnArgs {
     float eps;
 };
 
+// columns and what a row may begin with, in whole words
+inline int ln_pitch(int cols) { return (cols + 7) / 8 * 8 + 8; }
+// widths from which a row may be too wide for one CTA's registers (the row
+// means then go through the workspace)
+constexpr int kLnWide = 8176;
 cudaError_t launch_ln_forward(const LnArgs& a, cudaStream_t st);
 cudaError_t launch_ln_backward(const LnArgs& a, cudaStream_t st);
 
