@@ -1037,7 +1037,9 @@ cudaError_t backward_of(const LnArgs& args, cudaStream_t st)
             if (mode == kAligned)
                 e = backward_as<DT, N, 1, 3, 1, kAligned>(a, sms, st, parts);
             else if (mode == kAlike)
-                e = backward_as<DT, N, 1, 3, 1, kAlike>(a, sms, st, parts);
+                // (with 16 fp32 columns a thread this form spills)
+                e = chunks_of<DT>(a.cols, mode) <= 1024 ? backward_as<DT, 2, 1, 3, 1, kAlike>(a, sms, st, parts)
+                                                        : backward_as<DT, N, 1, 3, 1, kAlike>(a, sms, st, parts);
             else if (a.cols <= kDeepCols<DT>)
                 e = backward_as<DT, N, 1, 5, 1, kMixed>(a, sms, st, parts);
             else
