@@ -177,10 +177,14 @@ __global__ void __launch_bounds__(256) ln_backward_cols(const __grid_constant__ 
 //             apart, which all start alike, and cuts them where memory's words
 //             lie: chunk j holds the columns from V j - first on.  Slots stay
 //             private; only a row's first and last word need care.
-//   kMixed    the group copies the words that cover a row as they lie, a chunk
-//             is two words of shared memory shifted into place, and results go
-//             through shared memory too, so that global memory sees whole words.
-enum { kAligned = 0, kAlike = 1, kMixed = 2 };
+//   kFours    fp32 rows that lie differently: cut as the results' words lie, the
+//             inputs copied four bytes at a time.
+//   kMixed    16-bit rows that lie differently: the group copies the words that
+//             cover a row as they lie, a chunk is two words of shared memory
+//             shifted into place, and results go through shared memory too, so
+//             that global memory sees whole words.
+enum { kAligned = 0, kAlike = 1, kMixed = 2, kFours = 3 };
+__host__ __device__ constexpr bool by_words(int mode) { return mode == kAlike || mode == kFours; }
 
 template <int DT>
 constexpr int kV = DT == ZERO_FP32 ? 4 : 8;
@@ -188,6 +192,10 @@ constexpr int kV = DT == ZERO_FP32 ? 4 : 8;
 __device__ __forceinline__ void cp_async16(void* dst, const void* src)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(void* dst, const void* src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -311,6 +319,14 @@ struct RowSource {
         }
     }
 
+    // columns c .. of the row at q, four bytes each (fp32)
+    __device__ __forceinline__ void copy_fours(uint4* dst, const T* q, int c, int cols) const
+    {
+#pragma unroll
+        for (int e = 0; e < kV<DT>; ++e)
+            if (c + e >= 0 && c + e < cols) cp_async4(reinterpret_cast<uint32_t*>(dst) + e, q + c + e);
+    }
+
     // The words that cover row r into dst, word j by thread j, j + width, ...
     // Every word lies inside the array but for the first of the first row and
     // the last of the last one, which are copied element by element.
@@ -347,11 +363,11 @@ __device__ __forceinline__ void put_word(uintptr_t row, int c, int cols, const u
 // The rows of a group: row(k) of the set at r0 is r0 + k * apart.
 template <int MODE, int R>
 struct Walk {
-    static constexpr int apart = MODE == kAlike ? 8 : 1;
+    static constexpr int apart = by_words(MODE) ? 8 : 1;
     long long r0, step;
     __device__ __forceinline__ Walk(int grp, int groups)
     {
-        if (MODE == kAlike) {   // gridDim.x is a multiple of 8
+        if (by_words(MODE)) {   // gridDim.x is a multiple of 8
             r0 = (blockIdx.x & 7) + 8ll * ((blockIdx.x >> 3) * groups + grp) * R;
             step = 8ll * (gridDim.x >> 3) * groups * R;
         } else {
@@ -492,9 +508,9 @@ __global__ void __launch_bounds__(512, MINB)
     Walk<MODE, R> walk(grp, groups);
     long long& r0 = walk.r0;
     const long long step = walk.step;
-    // columns of the array's first word that belong to the row before
-    const int first = MODE == kAlike ? static_cast<int>((reinterpret_cast<uintptr_t>(static_cast<const typename El<DT>::T*>(a.x) + r0 * a.x_stride) & 15u) / sizeof(typename El<DT>::T)) : 0;
-    const int here = MODE == kAlike ? (first + a.cols + V - 1) / V : chunks;   // words of a row
+    // columns of a result row's first word that belong to the row before
+    const int first = by_words(MODE) ? static_cast<int>((reinterpret_cast<uintptr_t>(static_cast<const typename El<DT>::T*>(a.out) + r0 * a.out_stride) & 15u) / sizeof(typename El<DT>::T)) : 0;
+    const int here = by_words(MODE) ? (first + a.cols + V - 1) / V : chunks;   // words of a row
     const float inv_c = 1.0f / static_cast<float>(a.cols);
     for (int i = threadIdx.x; i < 2 * 8 * kMaxWarps * R; i += blockDim.x) (&red[0][0][0])[i] = 0.0f;
     __syncthreads();
@@ -523,6 +539,8 @@ __global__ void __launch_bounds__(512, MINB)
                         const typename El<DT>::T* q = x.base + r * x.stride;
                         if (MODE == kAligned)
                             cp_async16(p, q + (t + i * width) * V);
+                        else if (MODE == kFours)
+                            x.copy_fours(p, q, (t + i * width) * V - first, a.cols);
                         else
                             x.copy_word(p, reinterpret_cast<uintptr_t>(q - first + (t + i * width) * V), reinterpret_cast<uintptr_t>(q), reinterpret_cast<uintptr_t>(q + a.cols));
                     }
@@ -545,7 +563,7 @@ __global__ void __launch_bounds__(512, MINB)
                 if (t + i * width >= here || r0 + k * walk.apart >= a.rows) continue;
                 if (MODE != kMixed) {
                     w[k][i] = ring[((s * R + k) * NCH + i) * blockDim.x];
-                    if (MODE == kAlike) w[k][i] = masked<DT>(w[k][i], (t + i * width) * V - first, a.cols);
+                    if (by_words(MODE)) w[k][i] = masked<DT>(w[k][i], (t + i * width) * V - first, a.cols);
                 } else {
                     const uint4* p = ring + (s * R + k) * words + t + i * width;
                     w[k][i] = masked<DT>(shifted(p[0], p[1], x.row(r0 + k) & 15u), (t + i * width) * V, a.cols);
@@ -616,7 +634,7 @@ __global__ void __launch_bounds__(512, MINB)
                 unpack(f, o);
                 if (MODE == kAligned)
                     __stcs(reinterpret_cast<uint4*>(y.row(r)) + t + i * width, narrowed<DT>(o));
-                else if (MODE == kAlike)
+                else if (by_words(MODE))
                     put_word<DT>(y.row(r), c, a.cols, narrowed<DT>(o));
                 else
                     outs[k * words + 1 + t + i * width] = narrowed<DT>(o);
@@ -648,9 +666,9 @@ __global__ void __launch_bounds__(512, MINB)
     Walk<MODE, R> walk(grp, groups);
     long long& r0 = walk.r0;
     const long long step = walk.step;
-    // columns of the array's first word that belong to the row before
-    const int first = MODE == kAlike ? static_cast<int>((reinterpret_cast<uintptr_t>(static_cast<const typename El<DT>::T*>(a.x) + r0 * a.x_stride) & 15u) / sizeof(typename El<DT>::T)) : 0;
-    const int here = MODE == kAlike ? (first + a.cols + V - 1) / V : chunks;   // words of a row
+    // columns of a result row's first word that belong to the row before
+    const int first = by_words(MODE) ? static_cast<int>((reinterpret_cast<uintptr_t>(static_cast<const typename El<DT>::T*>(a.out) + r0 * a.out_stride) & 15u) / sizeof(typename El<DT>::T)) : 0;
+    const int here = by_words(MODE) ? (first + a.cols + V - 1) / V : chunks;   // words of a row
     const float inv_c = 1.0f / static_cast<float>(a.cols);
     for (int i = threadIdx.x; i < 2 * 8 * kMaxWarps * 2 * R; i += blockDim.x) (&red[0][0][0])[i] = 0.0f;
     __syncthreads();
@@ -683,6 +701,9 @@ __global__ void __launch_bounds__(512, MINB)
                         if (MODE == kAligned) {
                             cp_async16(p, q + at);
                             cp_async16(p + NCH * blockDim.x, d + at);
+                        } else if (MODE == kFours) {
+                            x.copy_fours(p, q, at - first, a.cols);
+                            dy.copy_fours(p + NCH * blockDim.x, d, at - first, a.cols);
                         } else {
                             x.copy_word(p, reinterpret_cast<uintptr_t>(q - first + at), reinterpret_cast<uintptr_t>(q), reinterpret_cast<uintptr_t>(q + a.cols));
                             dy.copy_word(p + NCH * blockDim.x, reinterpret_cast<uintptr_t>(d - first + at), reinterpret_cast<uintptr_t>(d), reinterpret_cast<uintptr_t>(d + a.cols));
@@ -719,7 +740,7 @@ __global__ void __launch_bounds__(512, MINB)
                     const uint4* p = ring + ((s * R + k) * 2 * NCH + i) * blockDim.x;
                     wx[k][i] = p[0];
                     wd[k][i] = p[NCH * blockDim.x];
-                    if (MODE == kAlike) {
+                    if (by_words(MODE)) {
                         const int c = (t + i * width) * V - first;
                         wx[k][i] = masked<DT>(wx[k][i], c, a.cols);
                         wd[k][i] = masked<DT>(wd[k][i], c, a.cols);
@@ -788,7 +809,7 @@ __global__ void __launch_bounds__(512, MINB)
                 unpack(xv, o);
                 if (MODE == kAligned)
                     __stcs(reinterpret_cast<uint4*>(out.row(r)) + t + i * width, narrowed<DT>(o));
-                else if (MODE == kAlike)
+                else if (by_words(MODE))
                     put_word<DT>(out.row(r), c, a.cols, narrowed<DT>(o));
                 else
                     outs[k * words + 1 + t + i * width] = narrowed<DT>(o);
@@ -923,11 +944,11 @@ RowShape row_shape(const LnArgs& a, int chunks, int nch, int r, int per_sm, size
     return s;
 }
 
-// words a thread's chunks have to cover: kAlike rows may begin inside one
+// words a thread's chunks have to cover: rows cut by words may begin inside one
 template <int DT>
 int chunks_of(int cols, int mode)
 {
-    return (cols + kV<DT> - 1 + (mode == kAlike ? kV<DT> - 1 : 0)) / kV<DT>;
+    return (cols + kV<DT> - 1 + (by_words(mode) ? kV<DT> - 1 : 0)) / kV<DT>;
 }
 
 // How equal rows of the arrays (null: none) lie; strides in elements.
@@ -938,7 +959,7 @@ int mode_of(int cols, const void* p, long long ps, const void* q, long long qs, 
     const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q), c = r != nullptr ? reinterpret_cast<uintptr_t>(r) : a;
     if (r == nullptr) rs = ps;
     if (cols % V == 0 && ps % V == 0 && qs % V == 0 && rs % V == 0 && a % 16 == 0 && b % 16 == 0 && c % 16 == 0) return kAligned;
-    return a % 16 == b % 16 && a % 16 == c % 16 && ps % V == qs % V && ps % V == rs % V ? kAlike : kMixed;
+    return a % 16 == b % 16 && a % 16 == c % 16 && ps % V == qs % V && ps % V == rs % V ? kAlike : DT == ZERO_FP32 ? kFours : kMixed;
 }
 
 template <typename K>
@@ -957,7 +978,7 @@ cudaError_t forward_as(const LnArgs& a, int sms, cudaStream_t st)
     const int chunks = chunks_of<DT>(a.cols, MODE);
     const int warps = (chunks + 32 * NCH - 1) / (32 * NCH);
     const size_t per = 16u * R * (MODE != kMixed ? static_cast<size_t>(DEPTH) * NCH * 32 * warps : static_cast<size_t>(DEPTH + 1) * row_words(chunks));
-    const RowShape s = row_shape(a, chunks, NCH, R, MINB, per, sms, MODE == kAlike);
+    const RowShape s = row_shape(a, chunks, NCH, R, MINB, per, sms, by_words(MODE));
     return launch_rows(ln_forward_rows<DT, NCH, R, DEPTH, MINB, MODE>, a, s, per * s.groups, st);
 }
 
@@ -967,7 +988,7 @@ cudaError_t backward_as(const LnArgs& a, int sms, cudaStream_t st, int& parts)
     const int chunks = chunks_of<DT>(a.cols, MODE);
     const int warps = (chunks + 32 * NCH - 1) / (32 * NCH);
     const size_t per = 16u * R * (MODE != kMixed ? static_cast<size_t>(2 * DEPTH) * NCH * 32 * warps : static_cast<size_t>(2 * DEPTH + 1) * row_words(chunks));
-    RowShape s = row_shape(a, chunks, NCH, R, MINB, per, sms, MODE == kAlike);
+    RowShape s = row_shape(a, chunks, NCH, R, MINB, per, sms, by_words(MODE));
     if (s.grid > kLnMaxParts) s.grid = kLnMaxParts;
     parts = static_cast<int>(s.grid);
     size_t smem = per * s.groups;
@@ -983,11 +1004,6 @@ constexpr int kMaxCols = 8192;
 static_assert(kMaxCols - 2 * 8 >= kLnWide, "narrower rows never take the general kernels");
 template <int DT>
 constexpr int kNch = 16 / kV<DT>;
-// columns up to which a group's five unaligned stages (eleven rows of words,
-// 176 bytes for each 8 or 4 columns) fit shared memory
-template <int DT>
-constexpr int kDeepCols = DT == ZERO_FP32 ? 4096 : 8192;
-
 template <int DT>
 cudaError_t forward_of(const LnArgs& a, cudaStream_t st)
 {
@@ -995,16 +1011,21 @@ cudaError_t forward_of(const LnArgs& a, cudaStream_t st)
     const int sms = sms_of_device();
     if (sms == 0) return cudaErrorInvalidDevice;
     const int mode = mode_of<DT>(a.cols, a.x, a.x_stride, a.out, a.out_stride, nullptr, 0);
-    constexpr int N = kNch<DT>;
-    if (chunks_of<DT>(a.cols, mode) <= 32) {
+    constexpr int N = kNch<DT>, kOther = DT == ZERO_FP32 ? kFours : kMixed;
+    const int chunks = chunks_of<DT>(a.cols, mode);
+    if (chunks <= 32) {
         if (mode == kAligned) return forward_as<DT, 1, 2, 4, 2, kAligned>(a, sms, st);
         if (mode == kAlike) return forward_as<DT, 1, 2, 4, 2, kAlike>(a, sms, st);
-        return forward_as<DT, 1, 2, 3, 2, kMixed>(a, sms, st);
+        return forward_as<DT, 1, 2, 3, 2, kOther>(a, sms, st);
     }
-    if (chunks_of<DT>(a.cols, mode) <= kMaxCols / V) {
+    if (chunks <= kMaxCols / V) {
         if (mode == kAligned) return forward_as<DT, N, 2, 3, 1, kAligned>(a, sms, st);
-        if (mode == kAlike) return forward_as<DT, N, 2, 3, 1, kAlike>(a, sms, st);
-        return a.cols <= kDeepCols<DT> ? forward_as<DT, N, 1, 5, 1, kMixed>(a, sms, st) : forward_as<DT, N, 1, 3, 1, kMixed>(a, sms, st);
+        // (fp32 rows up to 4096 columns go eight a thread: 1601 wide 13.7 -> 12.0 us)
+        if (mode == kAlike) return chunks <= 1024 ? forward_as<DT, 2, 2, 3, 1, kAlike>(a, sms, st) : forward_as<DT, N, 2, 3, 1, kAlike>(a, sms, st);
+        if constexpr (DT == ZERO_FP32)
+            return chunks <= 1024 ? forward_as<DT, 2, 2, 3, 1, kFours>(a, sms, st) : forward_as<DT, N, 2, 3, 1, kFours>(a, sms, st);
+        else
+            return forward_as<DT, N, 1, 5, 1, kMixed>(a, sms, st);
     }
     const long long grid = a.rows < (1 << 30) ? a.rows : (1 << 30);
     return launch_after(ln_forward_any<DT>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, a);
@@ -1021,29 +1042,30 @@ cudaError_t backward_of(const LnArgs& args, cudaStream_t st)
     int parts = static_cast<int>(a.rows < kLnMaxParts ? a.rows : kLnMaxParts);
     if (a.rows > 0) {
         const int mode = mode_of<DT>(a.cols, a.x, a.x_stride, a.out, a.out_stride, a.dy, a.dy_stride);
-        if (mode == kAlike)
+        if (by_words(mode))
             for (int k = 0; k < 8; ++k)
-                firsts |= static_cast<uint32_t>((reinterpret_cast<uintptr_t>(a.x) + k * a.x_stride * dtype_bytes(DT)) % 16 / dtype_bytes(DT)) << 4 * k;
-        constexpr int N = kNch<DT>;
+                firsts |= static_cast<uint32_t>((reinterpret_cast<uintptr_t>(a.out) + k * a.out_stride * dtype_bytes(DT)) % 16 / dtype_bytes(DT)) << 4 * k;
+        constexpr int N = kNch<DT>, kOther = DT == ZERO_FP32 ? kFours : kMixed;
+        const int chunks = chunks_of<DT>(a.cols, mode);
         cudaError_t e;
-        if (chunks_of<DT>(a.cols, mode) <= 32) {
+        if (chunks <= 32) {
             if (mode == kAligned)
                 e = backward_as<DT, 1, 2, 3, 1, kAligned>(a, sms, st, parts);
             else if (mode == kAlike)
                 e = backward_as<DT, 1, 2, 3, 1, kAlike>(a, sms, st, parts);
             else
-                e = backward_as<DT, 1, 2, 3, 1, kMixed>(a, sms, st, parts);
-        } else if (chunks_of<DT>(a.cols, mode) <= kMaxCols / V) {
+                e = backward_as<DT, 1, 2, 3, 1, kOther>(a, sms, st, parts);
+        } else if (chunks <= kMaxCols / V) {
+            // (fp32 rows up to 4096 columns that are not aligned go eight a
+            // thread: with sixteen these forms spill, 1601 wide 24.8 -> 19.6 us)
             if (mode == kAligned)
                 e = backward_as<DT, N, 1, 3, 1, kAligned>(a, sms, st, parts);
             else if (mode == kAlike)
-                // (with 16 fp32 columns a thread this form spills)
-                e = chunks_of<DT>(a.cols, mode) <= 1024 ? backward_as<DT, 2, 1, 3, 1, kAlike>(a, sms, st, parts)
-                                                        : backward_as<DT, N, 1, 3, 1, kAlike>(a, sms, st, parts);
-            else if (a.cols <= kDeepCols<DT>)
-                e = backward_as<DT, N, 1, 5, 1, kMixed>(a, sms, st, parts);
+                e = chunks <= 1024 ? backward_as<DT, 2, 1, 3, 1, kAlike>(a, sms, st, parts) : backward_as<DT, N, 1, 3, 1, kAlike>(a, sms, st, parts);
+            else if constexpr (DT == ZERO_FP32)
+                e = chunks <= 1024 ? backward_as<DT, 2, 1, 3, 1, kFours>(a, sms, st, parts) : backward_as<DT, N, 1, 3, 1, kFours>(a, sms, st, parts);
             else
-                e = backward_as<DT, N, 1, 2, 1, kMixed>(a, sms, st, parts);
+                e = backward_as<DT, N, 1, 5, 1, kMixed>(a, sms, st, parts);
         } else {
             const long long grid = a.rows < (1 << 30) ? a.rows : (1 << 30);
             firsts = 0;
