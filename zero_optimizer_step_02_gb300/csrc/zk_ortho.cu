@@ -697,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
                         const CUtensorMap* mb = ph.b + (pass == 1);
                         for (int k0 = k_from; k0 < k_to; k0 += kBK) {
                             if (count >= S::kStages &&
-                                !__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&empty[slot.i], slot.parity ^ 1, &abort_flag, a.timeout_ns))) {
+                                !__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&empty[slot.i], slot.parity ^ 1, &abort_flag, a.timeout_ns))) {
                                 abort_flag = 1;
                                 ok = false;
                                 break;
@@ -727,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
                 for (int t = first; ok && t < ph.tiles; t += step) {
                     const Tile tl = t == first ? ph.first : tile_of<CG, BN>(ph, t);
                     const int am = mn_from(ph.a_mode, S::kSb, tl.m0), bm = mn_from(ph.b_mode, S::kSb, tl.n0);
-                    if (count >= 2 && !__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&acc_empty[acc.i], acc.parity ^ 1, &abort_flag, a.timeout_ns))) {
+                    if (count >= 2 && !__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&acc_empty[acc.i], acc.parity ^ 1, &abort_flag, a.timeout_ns))) {
                         abort_flag = 1;
                         break;
                     }
@@ -737,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
                     uint32_t more = 0;   // 0: the accumulator starts anew
                     for (int pass = pass0; ok && pass < 3; ++pass) {
                         for (int k0 = k_from; k0 < k_to; k0 += kBK) {
-                            if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&full[slot.i], slot.parity, &abort_flag, a.timeout_ns))) {
+                            if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[slot.i], slot.parity, &abort_flag, a.timeout_ns))) {
                                 abort_flag = 1;
                                 ok = false;
                                 break;
@@ -778,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
                 for (int t = first; t < ph.tiles; t += step) {
                     Tile tl = t == first ? ph.first : tile_of<CG, BN>(ph, t);
                     tl.m0 += rank * kBM;
-                    if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(&acc_full[acc.i], acc.parity, &abort_flag, a.timeout_ns))) {
+                    if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(&acc_full[acc.i], acc.parity, &abort_flag, a.timeout_ns))) {
                         abort_flag = 1;
                         if (ph.split == 1) break;
                         // the other warps of the CTA still meet below
@@ -840,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
         // TMEM and the barriers are given up only after the last MMA
         if (rank == 0 && elect_one()) mma_commit<CG>(&drain);
         __syncwarp();
-        mbar_wait_cluster(&drain, 0, nullptr, 1000000000ull);
+        mbar_wait_bounded(&drain, 0, nullptr, 1000000000ull);
     }
     tc_fence_before();
     __syncthreads();

@@ -226,35 +226,12 @@ __device__ __forceinline__ void pair_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// arrive on the leader CTA's copy of `bar`
+// Arrive on the leader CTA's copy of `bar`.  What it orders is TMEM reads (by
+// the tcgen05 fence before it): released at cluster scope, it would also wait
+// for every store of this thread (1.5k cycles after a tile's results).
 __device__ __forceinline__ void mbar_arrive_leader(uint64_t* bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(leader_addr(smem_u32(bar))) : "memory");
-}
-
-// mbar_wait_bounded for barriers that the other CTA of a pair arrives on
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(kWaitHintNs)
-        : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, const volatile int* abort, unsigned long long timeout_ns)
-{
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (uint32_t it = 1; it < (1u << 28); ++it) {
-        if (mbar_try_wait_cluster(bar, parity)) return true;
-        if (abort != nullptr && *abort) return false;
-        if (globaltimer_ns() - t0 > timeout_ns) return false;
-    }
-    return false;
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(leader_addr(smem_u32(bar))) : "memory");
 }
 
 }  // namespace zk
