@@ -511,14 +511,17 @@ typedef struct {
  * contents need not be kept or cleared); 0 for an invalid descriptor.       */
 ZERO_API size_t zero_layernorm_workspace_bytes(const zero_layernorm* desc);
 
-/* y may be x (same stride); any other overlap is refused.  gain NULL: ones,
- * bias NULL: zeros; mean and rstd NULL: not stored.  One kernel.            */
+/* y may be x (same stride); any other overlap of the two is refused, and no
+ * other array that is written may overlap any.  gain NULL: ones, bias NULL:
+ * zeros; mean and rstd NULL: not stored.  One kernel.                       */
 ZERO_API zero_status zero_layernorm_forward(const zero_layernorm* desc, const void* x, const void* gain,
                                             const void* bias, void* y, float* mean, float* rstd, void* stream);
 
 /* mean and rstd as the forward call stored them.  dx may be dy or x (same
- * stride).  dgain and dbias are overwritten, not accumulated; either may be
- * NULL (not computed).                                                      */
+ * stride; other overlaps of them are refused), no other array that is written
+ * may overlap any.  dgain and dbias are overwritten, not accumulated; either
+ * may be NULL (not computed).  Two kernels; three for rows of more than
+ * 8176 to 8192 columns (as they lie).                                       */
 ZERO_API zero_status zero_layernorm_backward(const zero_layernorm* desc, const void* dy, const void* x,
                                              const void* gain, const float* mean, const float* rstd, void* dx,
                                              void* dgain, void* dbias, void* ws, void* stream);
@@ -570,9 +573,12 @@ ZERO_API size_t zero_orthogonalize_workspace_bytes(const zero_matrices* desc);
 ZERO_API size_t zero_muon_workspace_bytes(const zero_matrices* desc);
 
 /* out = the orthogonalised g.  g and out need the alignment of their element
- * type (16-byte bases and strides take the wide loads and stores); out may
- * overlap g, neither may overlap ws.  scalars_dev (may be NULL, else 256-byte
- * aligned) only receives ZERO_DEV_TIMEOUT if a bounded wait runs out.       */
+ * type (16-byte bases and strides take the wide loads and stores).  out may be g
+ * (element size and strides alike); a single matrix may overlap its result in
+ * any way, a batch in no other (refused; results between the inputs' rows, at
+ * the same strides, are none).  Neither may overlap ws.  scalars_dev (may be
+ * NULL, else 256-byte aligned) only receives ZERO_DEV_TIMEOUT if a bounded wait
+ * runs out.                                                                 */
 ZERO_API zero_status zero_orthogonalize(const zero_matrices* desc, const void* g, void* out, void* ws,
                                         zero_dev_scalars* scalars_dev, void* stream);
 

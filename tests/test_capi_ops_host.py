@@ -62,6 +62,13 @@ def test_layernorm_overlap_is_checked(z):
     assert ln_forward(z, wide, x=A + 128, y=A + 2) == INVALID
 
 
+def test_layernorm_extents_stay_in_64_bits(z):
+    d = z.layernorm(1 << 40, 64, x_stride=1 << 40)
+    assert z.zero_layernorm_workspace_bytes(d) == 0
+    assert ln_forward(z, d) == INVALID and ln_backward(z, d) == INVALID
+    assert z.zero_layernorm_workspace_bytes(z.layernorm(1 << 40, 64)) > 0
+
+
 def test_layernorm_workspace_size(z):
     assert z.zero_layernorm_workspace_bytes(z.layernorm(0, 64)) >= 256
     one = z.zero_layernorm_workspace_bytes(z.layernorm(1, 64))
@@ -117,6 +124,22 @@ def test_matrices_pointers_are_checked(z):
     assert orthogonalize(z, d, ws=C + 16) == MISALIGNED and orthogonalize(z, d, sc=D + 16) == MISALIGNED
     n = z.zero_orthogonalize_workspace_bytes(d)
     assert orthogonalize(z, d, g=C + n - 2) == INVALID and orthogonalize(z, d, out=C - 4) == INVALID
+
+
+def test_a_batch_lies_on_its_own_inputs_only(z):
+    """The matrices of a batch are under way side by side: a result on another one's input is refused."""
+    d = z.matrices(32, 64, batch=3, dtype=z.ZERO_BF16)
+    assert orthogonalize(z, d, g=A, out=A + 32 * 64 * 2) == INVALID          # on the next one
+    assert orthogonalize(z, d, g=A, out=A + 2) == INVALID
+    for kw in (dict(out_dtype=z.ZERO_FP32), dict(out_ld=65), dict(out_stride=32 * 64 + 64)):
+        assert orthogonalize(z, z.matrices(32, 64, batch=3, dtype=z.ZERO_BF16, **kw), g=A, out=A) == INVALID
+    # columns cut from one wide buffer: 128 bytes apart is side by side, 126 is not
+    wide = z.matrices(32, 64, batch=3, dtype=z.ZERO_BF16, in_ld=128, out_ld=128)
+    assert orthogonalize(z, wide, g=A, out=A + 126) == INVALID
+    assert orthogonalize(z, wide, g=A + 128, out=A + 2) == INVALID
+    # rows that do not repeat with the matrices
+    odd = z.matrices(32, 64, batch=3, dtype=z.ZERO_BF16, in_ld=128, out_ld=128, stride=32 * 128 + 8, out_stride=32 * 128 + 8)
+    assert orthogonalize(z, odd, g=A, out=A + 128) == INVALID
 
 
 def test_muon_arguments_are_checked(z):

@@ -176,6 +176,20 @@ def test_in_place_same_bits_other_stream_and_graph():
     assert torch.equal(out, g)
 
 
+@pytest.mark.parametrize("rows,cols", [(40, 64), (260, 384)])
+def test_results_beside_their_inputs_in_one_buffer(rows, cols):
+    buf = torch.zeros(3, rows, 2 * cols, device="cuda", dtype=torch.bfloat16)
+    g = gradients(3, rows, cols).to(torch.bfloat16)
+    buf[:, :, :cols] = g
+    packed = z.matrices(rows, cols, batch=3, dtype=BF16)
+    d = z.matrices(rows, cols, batch=3, dtype=BF16, in_ld=2 * cols, out_ld=2 * cols)
+    ws = torch.empty(z.zero_orthogonalize_workspace_bytes(d), dtype=torch.uint8, device="cuda")
+    want = torch.empty_like(g)
+    z.zero_orthogonalize(packed, g, want, ws)
+    z.zero_orthogonalize(d, buf, buf[:, :, cols:], ws)
+    assert torch.equal(buf[:, :, cols:], want) and torch.equal(buf[:, :, :cols], g)
+
+
 # ------------------------------------------------------------------ Muon step
 class Job:
     def __init__(self, rows, cols, batch=1, n_d=2, dt=BF16, pdt=None, gap=0, seed=0, **hp):

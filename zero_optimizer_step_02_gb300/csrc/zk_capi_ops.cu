@@ -33,6 +33,9 @@ zero_status check_ln(const zero_layernorm* d)
     const long long s[] = {d->x_stride, d->y_stride, d->dy_stride, d->dx_stride};
     for (long long v : s)
         if (v != 0 && (v < d->cols || v > (1LL << 40))) return ZERO_ERR_INVALID_ARG;
+    // an array's extent in bytes is reckoned in 64 bits
+    for (long long v : s)
+        if (d->rows > (1LL << 58) / stride_of(v, d->cols)) return ZERO_ERR_INVALID_ARG;
     return ZERO_OK;
 }
 
@@ -193,6 +196,16 @@ ZERO_API zero_status zero_orthogonalize(const zero_matrices* d, const void* g, v
     const size_t no = static_cast<size_t>((d->batch - 1) * a.out_stride + extent(d, a.out_ld)) * zk::dtype_bytes(d->out_dtype);
     const size_t nw = zk::ns_workspace_bytes(d->rows, d->cols, d->batch, a.products, false);
     if (overlap(g, ws, ni, nw) || overlap(out, ws, no, nw)) return ZERO_ERR_INVALID_ARG;
+    // a matrix is read whole before its result is written, but the matrices of a
+    // batch are under way side by side: each result may lie on its own input
+    // only, or between the inputs' rows
+    if (d->batch > 1 && overlap(g, out, ni, no)) {
+        if (zk::dtype_bytes(d->dtype) != zk::dtype_bytes(d->out_dtype) || a.in_ld != a.out_ld || a.in_stride != a.out_stride)
+            return ZERO_ERR_INVALID_ARG;
+        const long long all = (d->batch - 1) * (a.in_stride / a.in_ld) + d->rows;
+        if (g != out && (a.in_stride % a.in_ld != 0 || shares(g, a.in_ld, out, a.out_ld, all, d->cols, zk::dtype_bytes(d->dtype))))
+            return ZERO_ERR_INVALID_ARG;
+    }
     a.ws = ws;
     a.sc = sc;
     return from_cuda(zk::launch_ns(a, as_stream(stream)));

@@ -13,18 +13,14 @@
 namespace zk {
 
 // ------------------------------------------------------------------- TMA
-__device__ __forceinline__ void prefetch_tmap(const CUtensorMap* m)
-{
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
-}
-
 // Of a pair of CTAs (cluster of two), the address of the even one's copy of a
 // shared variable.
 __device__ __forceinline__ uint32_t leader_addr(uint32_t addr) { return addr & 0xFEFFFFFFu; }
 
-// One box of a rank-3 (rank-4) tensor at {x, y, z} ({x, y, z, w}) into this
-// CTA's shared memory, counted on `bar` (CG 2: on the leader CTA's copy of it).  x * element size must be a multiple of 16 bytes; what lies
-// outside the tensor arrives as zeros (and is counted in full).
+// One box of a rank-3 tensor at {x, y, z} into this CTA's shared memory, counted
+// on `bar` (CG 2: on the leader CTA's copy of it).  x * element size must be a
+// multiple of 16 bytes; what lies outside the tensor arrives as zeros (and is
+// counted in full).
 template <int CG>
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, int x, int y, int z, uint64_t* bar)
 {
@@ -39,22 +35,6 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, int
             "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
             " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
             "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-            : "memory");
-}
-template <int CG>
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* m, int x, int y, int z, int w, uint64_t* bar)
-{
-    if (CG == 2)
-        asm volatile(
-            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-            " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
-            "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(leader_addr(smem_u32(bar)))
-            : "memory");
-    else
-        asm volatile(
-            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-            " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
-            "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
             : "memory");
 }
 
