@@ -18,7 +18,23 @@
 // products = 1 multiplies the hi parts only: the result is 2e-4 to 1.7e-3 off
 // (relative, 2-norm), about the rounding of a bf16 result (1.7e-3).
 // products = 3 also carries G and P as pairs and multiplies
-// lo*hi + hi*lo + hi*hi: 3e-7 to 4e-6 off, for results kept in more than bf16.
+// lo*hi + hi*lo + hi*hi, for results kept in more than bf16: 3e-7 to 4e-6 off,
+// up to 3e-5 with a side of 4096, where the accumulator's own dropped bits (it
+// truncates at each addition of a 16-deep slice) outweigh the operands'.
+//
+// Work and floor.  With m the short and n the long side, a step multiplies
+// m (m + 1) n + m^2 (m + 1) + 2 m^2 n times and adds as often (G and P are
+// symmetric: half their blocks), three times that with products = 3; at 1926
+// TFLOP/s (a large library product's rate) 4096 x 14336 cannot take less than
+// 2.05 ms, twelve 768 x 768 56 us.  Large matrices are bound by the tensor
+// cores and, in effect, by power (4096 x 14336: 2.75 to 2.83 ms, 1.4 PFLOP/s).
+// Mid sizes are bound by what fifteen dependent products cost beside their
+// MMAs: a meeting of the CTAs (1 to 2 us), the first tiles' way from L2 (1 us)
+// and the last tiles' results (2 to 6 us); a 256 x 256 matrix, whose products
+// take 1 us each, pays 6.4 us a product.  Hence one launch for the whole
+// iteration (a launch for each product: 12 x 768 x 768 390 us, now 227), the
+// depth of a tile split among CTAs where tiles are few, and 32 x 32 pieces of
+// results that go out in whole 64-byte lines.
 #include <climits>
 #include <cstring>
 
@@ -406,6 +422,10 @@ __device__ __forceinline__ void clear_counters(unsigned* c, int n)
         for (int i = threadIdx.x; i < n; i += blockDim.x) c[i] = 0;
 }
 
+// The sums of squares of every matrix, a partial sum for each CTA.  Reads the
+// input once: 4096 x 14336 bf16 in 25 us (4.6 TB/s, 1% of the call), 12 x 768 x
+// 768 in 6 us.  Four loads under way a thread cost registers and were slower
+// (43 and 9 us).
 __global__ void __launch_bounds__(256) ns_sqnorm(const __grid_constant__ PrepArgs a)
 {
     __shared__ float2 red[8];
@@ -424,7 +444,10 @@ __global__ void __launch_bounds__(256) ns_sqnorm(const __grid_constant__ PrepArg
     if (threadIdx.x == 0) a.parts[blockIdx.y * static_cast<long long>(gridDim.x) + blockIdx.x] = sums;
 }
 
-// the update direction of every matrix, with the sums of its squares
+// The update direction of every matrix, with the sums of its squares: reads the
+// ranks' gradients and the momentum once, writes the momentum and the direction
+// in fp32.  Bound by memory: 2 x 4096 x 4096 over four ranks in 97 us (6.9
+// TB/s, 1.8% of the step); 768 x 2304 over eight ranks, 50 MB, in 16 us.
 __global__ void __launch_bounds__(256) muon_direction(const __grid_constant__ MuonArgs a)
 {
     __shared__ float2 red[8];
@@ -448,8 +471,22 @@ __global__ void __launch_bounds__(256) muon_direction(const __grid_constant__ Mu
 // products are three passes over the depth, the small ones first.
 // CG = 2: a pair of CTAs shares a tile of 256 rows.  Each brings its 128 rows
 // of A and half of B's, and holds its rows' sums.  An SM takes 64 bytes a clock
-// from L2; alone, a 128 x 256 tile wants 96 to keep its tensor core busy, in a
-// pair 64.
+// from L2, and a 64-deep stage's MMAs keep its tensor core busy for 2 BN clocks
+// (three times that JOINT).  Alone, a 128 x 128 tile's stage (32 KB) takes 512
+// clocks to arrive for 256 of MMAs, JOINT 1007 for 768, a 128 x 256 tile's 690
+// to 750 for 512; a pair's 256 x 256 tile brings 32 KB a CTA for 512 clocks of
+// MMAs, and measures 518.
+//
+// The forms, us for the whole five steps (timed side by side):
+//                           one CTA 128    pair 128    pair 256
+//     24 x 384 x 384             131         159         177
+//     4 x 1024 x 1024            177         215         197
+//     12 x 768 x 768             225         222         227
+//     12 x 768 x 768, three      353         321         359
+//     2048 x 2048, three         444         386         512
+//     4096 x 4096               1336        1274         929
+// A third form that no call would take is none: a 128 x 256 tile of one CTA was
+// slower than one of these everywhere.
 template <int CG, int BN, bool JOINT>
 struct MmShape {
     static constexpr int kABytes = kBM * kBK * 2, kBBytes = BN / CG * kBK * 2;
@@ -585,10 +622,20 @@ __device__ __noinline__ void first_operand(const NsKernelArgs& a, int b, int cta
 // other and meets at a counter in memory between products.  Within a product
 // the CTAs (CG = 2: the pairs) share the tiles, or, where there are fewer
 // tiles than units, each tile's depth (its parts meet at a counter of the tile
-// and each adds up its share of the columns, in order).  Within a CTA a producer thread keeps a
-// ring of 64-deep operand tiles full by TMA, one thread issues the MMAs into
-// one of two TMEM accumulators, and eight warps turn the other one into
-// results.
+// and each adds up its share of the columns, in order).  Within a CTA one warp
+// keeps a ring of 64-deep operand tiles full by TMA, one issues the MMAs into
+// one of two TMEM accumulators, eight turn the other one into results, and one
+// works out the next phase meanwhile (0.4 us that would stand between two
+// products).
+//
+// What the clocks go to beside the MMAs, in a phase: 1.0 to 1.3k for the fence
+// and the block's barrier, 2 to 4k for the meeting, 2.2k until the first stage
+// is there, 3.4 to 6.1k for the results of a 128 x 128 tile of a CTA, 6.8 to
+// 13k for 128 x 256 (the upper figures beside the next tile's MMAs), 13k for an
+// exchange of partial sums.  The results are bound by latency: a 32 x 32 piece
+// takes 1.2 to 2k clocks whether it leaves by plain stores or by TMA.  Sixteen
+// warps for them left 96 registers a thread, which spilled: 20 to 40% slower
+// everywhere; so did loading a piece's addends ahead.
 template <int CG, int BN, bool JOINT>
 __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__ NsKernelArgs a)
 {
@@ -900,12 +947,12 @@ struct Plan {
     double us;
 };
 
-// Times of a CTA or a pair, in us, that the choice goes by, fitted to 22 shapes
-// timed in each form (from 256 x 256 to 4096 x 4096, one and three products;
-// the choice is within 5% of the best of the three for all but one, 10%): a
-// 64-deep stage, the results of a tile beside the next tile's products and
-// alone at the end, the same with an exchange of partial sums, the meeting of
-// a group and the first copies after it.
+// Times of a CTA or a pair, in us, that the choice goes by, fitted to shapes
+// timed in each form (from 256 x 256 to 4096 x 4096, one and three products; of
+// sixteen, the choice is within 2% of the best form for thirteen and 6% for
+// all): a 64-deep stage, the results of a tile beside the next tile's products
+// and alone at the end, the same with an exchange of partial sums, the meeting
+// of a group and the first copies after it.
 struct Costs {
     double stage, results, end, split_end, meet, alone;
 };
@@ -1175,9 +1222,10 @@ cudaError_t launch_ns(const NsArgs& a, cudaStream_t st)
     k.sc = a.sc;
     k.timeout_ns = kDefaultTimeoutNs;
 
-    // the norm: CTAs a matrix, four chunks a thread, eight CTAs an SM over the batch
+    // the norm: CTAs a matrix, four chunks a thread (Muon, with more to load for
+    // each: one; 768 x 768 over 16 ranks, the whole step, 218 -> 203 us), eight CTAs an SM over the batch
     const long long chunks = static_cast<long long>(a.rows) * k.chunks;
-    long long per = (chunks + 1023) / 1024, most = (8LL * sms + a.batch - 1) / a.batch;
+    long long per = (chunks + (muon ? 255 : 1023)) / (muon ? 256 : 1024), most = (8LL * sms + a.batch - 1) / a.batch;
     if (per > most) per = most;
     if (per > kMaxNsParts) per = kMaxNsParts;
     k.parts_n = static_cast<int>(per);
