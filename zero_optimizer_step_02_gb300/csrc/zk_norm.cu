@@ -6,8 +6,23 @@
 //   dx = rstd * (h - mean_C(h) - xhat * mean_C(h * xhat))
 //   dgain = sum over rows of dy * xhat,  dbias = sum over rows of dy
 //
-// Every sum is fp32; the results are rounded once, to the tensor's type.  The sum of squares is taken about the
-// mean in a second pass over the row, so an offset in x costs no digits.
+// Every sum is fp32; the results are rounded once, to the tensor's type.  The
+// sum of squares is taken about the mean in a second pass over the row (in
+// registers), so an offset in x costs the variance no digits; xhat is x * rstd -
+// mean * rstd in one fused operation, whose rounding of mean * rstd is as large
+// as that of the mean itself.
+//
+// Bound: memory.  Forward reads x and writes y, backward reads x and dy and
+// writes dx; at 6783 GB/s (a copy's rate) 8192 x 4096 bf16 cannot take less than
+// 19.8 us forward and 29.7 us backward.  Measured: forward 25.4 us (5280 GB/s,
+// 0.78 of a copy), 16384 x 4096 45.8 us (5860, 0.86); backward 16384 x 4096 74.3
+// us (5420, 0.80), its second kernel included.  What is left is issue: a CTA of
+// sixteen warps an SM, 60% of the issue slots busy, fixed-latency and shared-
+// memory waits in between.  Few rows are bound by latency: 8 x 768 2.4 us, 256 x
+// 768 backward 6.1 us (two kernels, the second's start hidden behind the first).
+// Rows that do not lie on 16-byte words pay for it: 2999 x 1601 fp32 forward
+// 12.0 us alike and 12.5 us with unlike gaps (floor 5.7), 5003 x 1601 fp16
+// backward 24.1 us (floor 7.1).
 #include "zk_common.cuh"
 #include "zk_launch.h"
 #include "zk_ops.h"
@@ -73,8 +88,10 @@ __device__ __forceinline__ float block_sum(float v, float* red)
 }
 
 // ------------------------------------------------------ any width, any stride
-// For rows too wide for the kernels below.  One CTA a row; the row is read
-// three times, the last two from cache.
+// For rows too wide for the kernels below.  One CTA a row, one element a thread
+// at a time; the row is read three times, the last two from cache.  About a
+// sixth of a copy's rate: rows of more than 8192 columns are rare, so these
+// forms are kept short (and right for any width and alignment).
 template <int DT>
 __global__ void __launch_bounds__(256) ln_forward_any(const __grid_constant__ LnArgs a)
 {
@@ -168,6 +185,13 @@ __global__ void __launch_bounds__(256) ln_backward_cols(const __grid_constant__ 
 // groups walks the rows.  A thread's columns never change, so weights and
 // column sums stay in registers, and the rows to come are already on their way
 // into a ring of DEPTH stages in shared memory (16-byte asynchronous copies).
+// Sixteen columns a thread spread what a row costs each thread besides its
+// columns (the two sums over the group); a row to a warp, 128 columns a thread,
+// left too few loads under way (41 us forward where this takes 25, 70 us
+// backward at 8192 x 4096), eight columns a thread and four rows at a time took
+// 106 us backward at 16384 x 4096, two rows at a time spilled (139 us).  Values
+// stay packed two to a register pair, and operations on pairs (f32x2) halve the
+// issue slots.
 //
 // How the rows lie (MODE):
 //   kAligned  bases, strides and the width are multiples of 16 bytes.  A thread
@@ -496,6 +520,8 @@ __device__ __forceinline__ void group_sync(int grp, int warps, int width)
         named_bar_sync(1 + grp, width);
 }
 
+// Forward: one read, one write.  Two rows at a time, so that their sums share
+// the group's barriers.
 template <int DT, int NCH, int R, int DEPTH, int MINB, int MODE>
 __global__ void __launch_bounds__(512, MINB)
     ln_forward_rows(const __grid_constant__ LnArgs a, int warps, int groups)
@@ -654,6 +680,9 @@ __global__ void __launch_bounds__(512, MINB)
     }
 }
 
+// Backward: dx, and the column sums of the rows the CTA took, in one pass.  Each
+// CTA leaves one row of partial sums (at most 304), not an atomic: the same
+// bits every time.
 template <int DT, int NCH, int R, int DEPTH, int MINB, int MODE>
 __global__ void __launch_bounds__(512, MINB)
     ln_backward_rows_fused(const __grid_constant__ LnArgs a, int warps, int groups)
@@ -878,7 +907,8 @@ __global__ void __launch_bounds__(512, MINB)
 }
 
 // The partial column sums, in a fixed order: 32 columns a CTA, sixteen slices
-// of the parts side by side.
+// of the parts side by side.  5 MB for 4096 columns, out of L2; 2 to 3 us after
+// the rows' kernel, whose end it waits for (fp64 sums: 3 us more).
 __global__ void __launch_bounds__(512) ln_backward_finish(const __grid_constant__ LnArgs a, int parts, uint32_t firsts)
 {
     __shared__ float red[16][33];

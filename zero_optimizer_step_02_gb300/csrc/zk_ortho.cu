@@ -485,8 +485,8 @@ __global__ void __launch_bounds__(256) muon_direction(const __grid_constant__ Mu
 //     12 x 768 x 768, three      353         321         359
 //     2048 x 2048, three         444         386         512
 //     4096 x 4096               1336        1274         929
-// A third form that no call would take is none: a 128 x 256 tile of one CTA was
-// slower than one of these everywhere.
+// A 128 x 256 tile of one CTA was slower than the best of these everywhere, so
+// there is none.
 template <int CG, int BN, bool JOINT>
 struct MmShape {
     static constexpr int kABytes = kBM * kBK * 2, kBBytes = BN / CG * kBK * 2;
