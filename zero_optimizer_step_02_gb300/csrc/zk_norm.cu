@@ -74,6 +74,15 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
+// 1 / sqrt(v) to an ulp or so: the approximate root and a Newton step (a root
+// and a division in every thread were a seventh of the forward kernel's
+// instructions).  0, infinity and NaN as they come.
+__device__ __forceinline__ float inverse_root(float v)
+{
+    const float y = rsqrtf(v), e = fmaf(-v * y, y, 1.0f);
+    return is_finite_f32(e) ? fmaf(0.5f * y, e, y) : y;
+}
+
 // sum over the block, the same value in every thread; red: 32 floats
 __device__ __forceinline__ float block_sum(float v, float* red)
 {
@@ -643,7 +652,7 @@ __global__ void __launch_bounds__(512, MINB)
         for (int k = 0; k < R; ++k) {
             const long long r = r0 + k * walk.apart;
             if (r >= a.rows) break;
-            rstd[k] = 1.0f / sqrtf(rstd[k] * inv_c + a.eps);
+            rstd[k] = inverse_root(rstd[k] * inv_c + a.eps);
             const RowSource<DT> y(a.out, a.out_stride, a.rows, a.cols);
             // xhat in one operation: x * rstd - mean * rstd
             const f32x2 rs = pack2(rstd[k], rstd[k]), nm = pack2(-mean[k] * rstd[k], -mean[k] * rstd[k]);
