@@ -520,6 +520,16 @@ __device__ __forceinline__ void group_sums(float (&v)[N], float* red, int warps,
 // the shift, one that a shifted read may touch; as many for a row of results
 __host__ __device__ constexpr int row_words(int chunks) { return chunks + 2; }
 
+// zeros in this thread's ring slots for chunks that its rows do not have
+template <int ROWS, int NCH>
+__device__ __forceinline__ void clear_slots(uint4* ring, int t, int width, int here)
+{
+#pragma unroll
+    for (int i = 0; i < NCH; ++i)
+        if (t + i * width >= here)
+            for (int k = 0; k < ROWS; ++k) ring[(k * NCH + i) * blockDim.x] = make_uint4(0, 0, 0, 0);
+}
+
 // the threads of a group meet (a group of one warp needs no barrier of its own)
 __device__ __forceinline__ void group_sync(int grp, int warps, int width)
 {
@@ -535,6 +545,7 @@ template <int DT, int NCH, int R, int DEPTH, int MINB, int MODE>
 __global__ void __launch_bounds__(512, MINB)
     ln_forward_rows(const __grid_constant__ LnArgs a, int warps, int groups)
 {
+    using T = typename El<DT>::T;
     constexpr int V = kV<DT>;
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ float red[2][8][kMaxWarps * R];
@@ -544,7 +555,7 @@ __global__ void __launch_bounds__(512, MINB)
     long long& r0 = walk.r0;
     const long long step = walk.step;
     // columns of a result row's first word that belong to the row before
-    const int first = by_words(MODE) ? static_cast<int>((reinterpret_cast<uintptr_t>(static_cast<const typename El<DT>::T*>(a.out) + r0 * a.out_stride) & 15u) / sizeof(typename El<DT>::T)) : 0;
+    const int first = by_words(MODE) ? static_cast<int>((reinterpret_cast<uintptr_t>(static_cast<const T*>(a.out) + r0 * a.out_stride) & 15u) / sizeof(T)) : 0;
     const int here = by_words(MODE) ? (first + a.cols + V - 1) / V : chunks;   // words of a row
     const float inv_c = 1.0f / static_cast<float>(a.cols);
     for (int i = threadIdx.x; i < 2 * 8 * kMaxWarps * R; i += blockDim.x) (&red[0][0][0])[i] = 0.0f;
@@ -561,17 +572,23 @@ __global__ void __launch_bounds__(512, MINB)
     // [DEPTH][R][NCH][threads]; kMixed: a group's [DEPTH][R][words] and [R][words] of results
     uint4* ring = reinterpret_cast<uint4*>(smem) + (MODE != kMixed ? threadIdx.x : grp * (DEPTH + 1) * R * words);
     uint4* outs = ring + DEPTH * R * words;
-    auto fetch = [&](long long r0, int s) {
+    // words of a stage; where the next rows go and come from
+    const int stage = MODE != kMixed ? R * NCH * blockDim.x : R * words;
+    uint4* into = ring;
+    long long rf = r0;
+    const T* xf = x.base + r0 * x.stride;
+    if (MODE != kMixed)   // slots of chunks past the row are never written again
+        clear_slots<DEPTH * R, NCH>(ring, t, width, here);
+    auto fetch = [&]() {
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            const long long r = r0 + k * walk.apart;
-            if (r >= a.rows) break;
+            if (rf + k * walk.apart >= a.rows) break;
             if (MODE != kMixed) {
+                const T* q = xf + k * walk.apart * x.stride;
 #pragma unroll
                 for (int i = 0; i < NCH; ++i)
                     if (t + i * width < here) {
-                        uint4* p = ring + ((s * R + k) * NCH + i) * blockDim.x;
-                        const typename El<DT>::T* q = x.base + r * x.stride;
+                        uint4* p = into + (k * NCH + i) * blockDim.x;
                         if (MODE == kAligned)
                             cp_async16(p, q + (t + i * width) * V);
                         else if (MODE == kFours)
@@ -580,13 +597,18 @@ __global__ void __launch_bounds__(512, MINB)
                             x.copy_word(p, reinterpret_cast<uintptr_t>(q - first + (t + i * width) * V), reinterpret_cast<uintptr_t>(q), reinterpret_cast<uintptr_t>(q + a.cols));
                     }
             } else {
-                x.copy_words(ring + (s * R + k) * words, r, a.cols, t, width);
+                x.copy_words(into + k * words, rf + k * walk.apart, a.cols, t, width);
             }
         }
         cp_async_commit();
+        rf += step;
+        xf += step * x.stride;
+        into = into == ring + (DEPTH - 1) * stage ? ring : into + stage;
     };
-    for (int s = 0; s < DEPTH - 1; ++s) fetch(r0 + s * step, s);
-    for (int s = 0; r0 < a.rows; r0 += step, s = s + 1 == DEPTH ? 0 : s + 1) {
+    for (int s = 0; s < DEPTH - 1; ++s) fetch();
+    const uint4* from = ring;
+    T* yr = static_cast<T*>(a.out) + r0 * a.out_stride;
+    for (; r0 < a.rows; r0 += step, yr += step * a.out_stride, from = from == ring + (DEPTH - 1) * stage ? ring : from + stage) {
         cp_async_wait<DEPTH - 2>();
         if (MODE == kMixed) group_sync(grp, warps, width);
         uint4 w[R][NCH];
@@ -594,17 +616,18 @@ __global__ void __launch_bounds__(512, MINB)
         for (int k = 0; k < R; ++k)
 #pragma unroll
             for (int i = 0; i < NCH; ++i) {
-                w[k][i] = make_uint4(0, 0, 0, 0);
-                if (t + i * width >= here || r0 + k * walk.apart >= a.rows) continue;
+                // (rows past the last: whatever lies there, and no result)
                 if (MODE != kMixed) {
-                    w[k][i] = ring[((s * R + k) * NCH + i) * blockDim.x];
+                    w[k][i] = from[(k * NCH + i) * blockDim.x];
                     if (by_words(MODE)) w[k][i] = masked<DT>(w[k][i], (t + i * width) * V - first, a.cols);
                 } else {
-                    const uint4* p = ring + (s * R + k) * words + t + i * width;
+                    w[k][i] = make_uint4(0, 0, 0, 0);
+                    if (t + i * width >= here || r0 + k * walk.apart >= a.rows) continue;
+                    const uint4* p = from + k * words + t + i * width;
                     w[k][i] = masked<DT>(shifted(p[0], p[1], x.row(r0 + k) & 15u), (t + i * width) * V, a.cols);
                 }
             }
-        fetch(r0 + (DEPTH - 1) * step, s == 0 ? DEPTH - 1 : s - 1);
+        fetch();
         float mean[R], rstd[R];
 #pragma unroll
         for (int k = 0; k < R; ++k) {
@@ -653,7 +676,7 @@ __global__ void __launch_bounds__(512, MINB)
             const long long r = r0 + k * walk.apart;
             if (r >= a.rows) break;
             rstd[k] = inverse_root(rstd[k] * inv_c + a.eps);
-            const RowSource<DT> y(a.out, a.out_stride, a.rows, a.cols);
+            const uintptr_t y = reinterpret_cast<uintptr_t>(yr + k * walk.apart * a.out_stride);
             // xhat in one operation: x * rstd - mean * rstd
             const f32x2 rs = pack2(rstd[k], rstd[k]), nm = pack2(-mean[k] * rstd[k], -mean[k] * rstd[k]);
 #pragma unroll
@@ -668,9 +691,9 @@ __global__ void __launch_bounds__(512, MINB)
                 for (int e = 0; e < V / 2; ++e) f[e] = fma2(fma2(f[e], rs, nm), gain[i][e], bias[i][e]);
                 unpack(f, o);
                 if (MODE == kAligned)
-                    __stcs(reinterpret_cast<uint4*>(y.row(r)) + t + i * width, narrowed<DT>(o));
+                    __stcs(reinterpret_cast<uint4*>(y) + t + i * width, narrowed<DT>(o));
                 else if (by_words(MODE))
-                    put_word<DT>(y.row(r), c, a.cols, narrowed<DT>(o));
+                    put_word<DT>(y, c, a.cols, narrowed<DT>(o));
                 else
                     outs[k * words + 1 + t + i * width] = narrowed<DT>(o);
             }
@@ -681,10 +704,9 @@ __global__ void __launch_bounds__(512, MINB)
         }
         if (MODE == kMixed) {
             group_sync(grp, warps, width);
-            const RowSource<DT> y(a.out, a.out_stride, a.rows, a.cols);
 #pragma unroll
             for (int k = 0; k < R; ++k)
-                if (r0 + k < a.rows) write_words<DT>(outs + k * words, y.row(r0 + k), a.cols, t, width);
+                if (r0 + k < a.rows) write_words<DT>(outs + k * words, reinterpret_cast<uintptr_t>(yr + k * a.out_stride), a.cols, t, width);
         }
     }
 }
@@ -696,6 +718,7 @@ template <int DT, int NCH, int R, int DEPTH, int MINB, int MODE>
 __global__ void __launch_bounds__(512, MINB)
     ln_backward_rows_fused(const __grid_constant__ LnArgs a, int warps, int groups)
 {
+    using T = typename El<DT>::T;
     constexpr int V = kV<DT>;
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ float red[2][8][kMaxWarps * 2 * R];
@@ -705,7 +728,7 @@ __global__ void __launch_bounds__(512, MINB)
     long long& r0 = walk.r0;
     const long long step = walk.step;
     // columns of a result row's first word that belong to the row before
-    const int first = by_words(MODE) ? static_cast<int>((reinterpret_cast<uintptr_t>(static_cast<const typename El<DT>::T*>(a.out) + r0 * a.out_stride) & 15u) / sizeof(typename El<DT>::T)) : 0;
+    const int first = by_words(MODE) ? static_cast<int>((reinterpret_cast<uintptr_t>(static_cast<const T*>(a.out) + r0 * a.out_stride) & 15u) / sizeof(T)) : 0;
     const int here = by_words(MODE) ? (first + a.cols + V - 1) / V : chunks;   // words of a row
     const float inv_c = 1.0f / static_cast<float>(a.cols);
     for (int i = threadIdx.x; i < 2 * 8 * kMaxWarps * 2 * R; i += blockDim.x) (&red[0][0][0])[i] = 0.0f;
@@ -723,18 +746,23 @@ __global__ void __launch_bounds__(512, MINB)
     // [DEPTH][R][2][NCH][threads]; kMixed: a group's [DEPTH][R][2][words] and [R][words] of results
     uint4* ring = reinterpret_cast<uint4*>(smem) + (MODE != kMixed ? threadIdx.x : grp * (2 * DEPTH + 1) * R * words);
     uint4* outs = ring + 2 * DEPTH * R * words;
-    auto fetch = [&](long long r0, int s) {
+    // words of a stage; where the next rows go and come from
+    const int stage = MODE != kMixed ? 2 * R * NCH * blockDim.x : 2 * R * words;
+    int into = 0;
+    if (MODE != kMixed)   // slots of chunks past the row are never written again
+        clear_slots<DEPTH * R * 2, NCH>(ring, t, width, here);
+    auto fetch = [&](long long rf) {
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            const long long r = r0 + k * walk.apart;
+            const long long r = rf + k * walk.apart;
             if (r >= a.rows) break;
             if (MODE != kMixed) {
+                const T* q = x.base + r * x.stride;
+                const T* d = dy.base + r * dy.stride;
 #pragma unroll
                 for (int i = 0; i < NCH; ++i)
                     if (t + i * width < here) {
-                        uint4* p = ring + ((s * R + k) * 2 * NCH + i) * blockDim.x;
-                        const typename El<DT>::T* q = x.base + r * x.stride;
-                        const typename El<DT>::T* d = dy.base + r * dy.stride;
+                        uint4* p = ring + into + (k * 2 * NCH + i) * blockDim.x;
                         const int at = (t + i * width) * V;
                         if (MODE == kAligned) {
                             cp_async16(p, q + at);
@@ -748,14 +776,15 @@ __global__ void __launch_bounds__(512, MINB)
                         }
                     }
             } else {
-                uint4* p = ring + (s * R + k) * 2 * words;
+                uint4* p = ring + into + k * 2 * words;
                 x.copy_words(p, r, a.cols, t, width);
                 dy.copy_words(p + words, r, a.cols, t, width);
             }
         }
         cp_async_commit();
+        into = into == (DEPTH - 1) * stage ? 0 : into + stage;
     };
-    for (int s = 0; s < DEPTH - 1; ++s) fetch(r0 + s * step, s);
+    for (int s = 0; s < DEPTH - 1; ++s) fetch(r0 + s * step);
     float mean[R], rstd[R];
 #pragma unroll
     for (int k = 0; k < R; ++k) {
@@ -764,7 +793,7 @@ __global__ void __launch_bounds__(512, MINB)
         rstd[k] = r < a.rows ? a.rstd[r] : 0.0f;
     }
     int buf = 0;
-    for (int s = 0; r0 < a.rows; r0 += step, s = s + 1 == DEPTH ? 0 : s + 1, buf ^= 1) {
+    for (int from = 0; r0 < a.rows; r0 += step, from = from == (DEPTH - 1) * stage ? 0 : from + stage, buf ^= 1) {
         cp_async_wait<DEPTH - 2>();
         if (MODE == kMixed) group_sync(grp, warps, width);
         uint4 wx[R][NCH], wd[R][NCH];
@@ -772,10 +801,12 @@ __global__ void __launch_bounds__(512, MINB)
         for (int k = 0; k < R; ++k)
 #pragma unroll
             for (int i = 0; i < NCH; ++i) {
-                wx[k][i] = wd[k][i] = make_uint4(0, 0, 0, 0);
-                if (t + i * width >= here || r0 + k * walk.apart >= a.rows) continue;
+                if (MODE == kMixed || R > 1) {   // (R = 1: a loop's row is there)
+                    wx[k][i] = wd[k][i] = make_uint4(0, 0, 0, 0);
+                    if (t + i * width >= here || r0 + k * walk.apart >= a.rows) continue;
+                }
                 if (MODE != kMixed) {
-                    const uint4* p = ring + ((s * R + k) * 2 * NCH + i) * blockDim.x;
+                    const uint4* p = ring + from + (k * 2 * NCH + i) * blockDim.x;
                     wx[k][i] = p[0];
                     wd[k][i] = p[NCH * blockDim.x];
                     if (by_words(MODE)) {
@@ -784,13 +815,13 @@ __global__ void __launch_bounds__(512, MINB)
                         wd[k][i] = masked<DT>(wd[k][i], c, a.cols);
                     }
                 } else {
-                    const uint4* p = ring + (s * R + k) * 2 * words + t + i * width;
+                    const uint4* p = ring + from + k * 2 * words + t + i * width;
                     const int c = (t + i * width) * V;
                     wx[k][i] = masked<DT>(shifted(p[0], p[1], x.row(r0 + k) & 15u), c, a.cols);
                     wd[k][i] = masked<DT>(shifted(p[words], p[words + 1], dy.row(r0 + k) & 15u), c, a.cols);
                 }
             }
-        fetch(r0 + (DEPTH - 1) * step, s == 0 ? DEPTH - 1 : s - 1);
+        fetch(r0 + (DEPTH - 1) * step);
         float next_mean[R], next_rstd[R];
 #pragma unroll
         for (int k = 0; k < R; ++k) {
@@ -822,15 +853,15 @@ __global__ void __launch_bounds__(512, MINB)
             sum[2 * k + 1] = both(s2);
         }
         group_sums<2 * R>(sum, red[buf][grp & 7], warps, 1 + grp, width, wg);
-        const RowSource<DT> out(a.out, a.out_stride, a.rows, a.cols);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            const long long r = r0 + k * walk.apart;
-            if (r >= a.rows) break;
+            if (r0 + k * walk.apart >= a.rows) break;
+            const uintptr_t out = reinterpret_cast<uintptr_t>(static_cast<T*>(a.out) + (r0 + k * walk.apart) * a.out_stride);
             // dx = rstd * (dy * gain - s1 - xhat * s2)
             const float s1 = sum[2 * k] * inv_c, s2 = sum[2 * k + 1] * inv_c;
-            const f32x2 m = pack2(mean[k], mean[k]), rs = pack2(rstd[k], rstd[k]), n1 = pack2(-s1, -s1);
-            const f32x2 n2 = pack2(-s2 * rstd[k], -s2 * rstd[k]);
+            // = rstd * (dy * gain + x * n2 + n1)
+            const float q2 = -s2 * rstd[k], q1 = fmaf(-mean[k], q2, -s1);
+            const f32x2 rs = pack2(rstd[k], rstd[k]), n1 = pack2(q1, q1), n2 = pack2(q2, q2);
 #pragma unroll
             for (int i = 0; i < NCH; ++i) {
                 const int c = (t + i * width) * V - first;
@@ -843,12 +874,12 @@ __global__ void __launch_bounds__(512, MINB)
                 widen<DT>(wd[k][i], dv);
 #pragma unroll
                 for (int e = 0; e < V / 2; ++e)
-                    xv[e] = mul2(rs, fma2(sub2(xv[e], m), n2, fma2(dv[e], gain[i][e], n1)));
+                    xv[e] = mul2(rs, fma2(xv[e], n2, fma2(dv[e], gain[i][e], n1)));
                 unpack(xv, o);
                 if (MODE == kAligned)
-                    __stcs(reinterpret_cast<uint4*>(out.row(r)) + t + i * width, narrowed<DT>(o));
+                    __stcs(reinterpret_cast<uint4*>(out) + t + i * width, narrowed<DT>(o));
                 else if (by_words(MODE))
-                    put_word<DT>(out.row(r), c, a.cols, narrowed<DT>(o));
+                    put_word<DT>(out, c, a.cols, narrowed<DT>(o));
                 else
                     outs[k * words + 1 + t + i * width] = narrowed<DT>(o);
             }
@@ -857,7 +888,7 @@ __global__ void __launch_bounds__(512, MINB)
             group_sync(grp, warps, width);
 #pragma unroll
             for (int k = 0; k < R; ++k)
-                if (r0 + k < a.rows) write_words<DT>(outs + k * words, out.row(r0 + k), a.cols, t, width);
+                if (r0 + k < a.rows) write_words<DT>(outs + k * words, reinterpret_cast<uintptr_t>(static_cast<T*>(a.out) + (r0 + k) * a.out_stride), a.cols, t, width);
         }
 #pragma unroll
         for (int k = 0; k < R; ++k) mean[k] = next_mean[k], rstd[k] = next_rstd[k];
