@@ -212,12 +212,11 @@ __global__ void __launch_bounds__(256) ln_backward_cols(const __grid_constant__ 
 //             private; only a row's first and last word need care.
 //   kFours    fp32 rows that lie differently: cut as the results' words lie, the
 //             inputs copied four bytes at a time.
-//   kMixed    16-bit rows that lie differently: the group copies the words that
-//             cover a row as they lie, a chunk is two words of shared memory
-//             shifted into place, and results go through shared memory too, so
-//             that global memory sees whole words.
+//   kMixed    16-bit rows that lie differently: cut as the results' words lie,
+//             the inputs' words copied as they lie; a chunk is two of them, its
+//             own thread's and the next one's, shifted into place.
 enum { kAligned = 0, kAlike = 1, kMixed = 2, kFours = 3 };
-__host__ __device__ constexpr bool by_words(int mode) { return mode == kAlike || mode == kFours; }
+__host__ __device__ constexpr bool by_words(int mode) { return mode != kAligned; }
 
 template <int DT>
 constexpr int kV = DT == ZERO_FP32 ? 4 : 8;
@@ -360,14 +359,11 @@ struct RowSource {
             if (c + e >= 0 && c + e < cols) cp_async4(reinterpret_cast<uint32_t*>(dst) + e, q + c + e);
     }
 
-    // The words that cover row r into dst, word j by thread j, j + width, ...
-    // Every word lies inside the array but for the first of the first row and
-    // the last of the last one, which are copied element by element.
-    __device__ __forceinline__ void copy_words(uint4* dst, long long r, int cols, int t, int width) const
+    // The same if the word holds any of the row's elements (one that does not
+    // may lie in memory that is not there).
+    __device__ __forceinline__ void copy_if_any(uint4* dst, uintptr_t at, uintptr_t from, uintptr_t to) const
     {
-        const uintptr_t from = row(r), to = from + static_cast<uintptr_t>(cols) * sizeof(T);
-        uintptr_t at = (from & ~static_cast<uintptr_t>(15)) + 16u * t;
-        for (int j = t; at < to; j += width, at += 16u * width) copy_word(dst + j, at, from, to);
+        if (at + 16 > from && at < to) copy_word(dst, at, from, to);
     }
 };
 
@@ -409,34 +405,6 @@ struct Walk {
         }
     }
 };
-
-// A row's results from shared memory, where they lie chunk by chunk from word 1
-// on (word 0 may hold anything), to memory in whole words but at its ends.
-template <int DT>
-__device__ __forceinline__ void write_words(const uint4* src, uintptr_t from, int cols, int t, int width)
-{
-    using T = typename El<DT>::T;
-    const uint32_t off = from & 15u;
-    const uintptr_t to = from + static_cast<uintptr_t>(cols) * sizeof(T);
-    uintptr_t at = from - off + 16u * t;
-    for (int j = t; at < to; j += width, at += 16u * width) {
-        const uint4 w = off == 0 ? src[j + 1] : shifted(src[j], src[j + 1], 16u - off);
-        if (at >= from && at + 16 <= to) {
-            __stcs(reinterpret_cast<uint4*>(at), w);
-        } else {
-            const uint32_t a[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int e = 0; e < static_cast<int>(16 / sizeof(T)); ++e) {
-                const uintptr_t q = at + e * sizeof(T);
-                if (q < from || q >= to) continue;
-                if constexpr (sizeof(T) == 4)
-                    *reinterpret_cast<uint32_t*>(q) = a[e];
-                else
-                    *reinterpret_cast<uint16_t*>(q) = static_cast<uint16_t>(a[e / 2] >> (16 * (e & 1)));
-            }
-        }
-    }
-}
 
 // V weights from column c on, in whichever type they have; `none` without a
 // vector, 0 where there is no such column
@@ -516,9 +484,9 @@ __device__ __forceinline__ void group_sums(float (&v)[N], float* red, int warps,
     for (int k = 0; k < N; ++k) v[k] = N > 1 ? __shfl_sync(0xFFFFFFFFu, y[k % P], k / P) : y[0];
 }
 
-// words of shared memory that one row's copy takes: its chunks, one more for
-// the shift, one that a shifted read may touch; as many for a row of results
-__host__ __device__ constexpr int row_words(int chunks) { return chunks + 2; }
+// words of shared memory that one row's copy takes (kMixed): its chunks, and
+// one more for the shift
+__host__ __device__ constexpr int row_words(int chunks) { return chunks + 1; }
 
 // zeros in this thread's ring slots for chunks that its rows do not have
 template <int ROWS, int NCH>
@@ -550,13 +518,13 @@ __global__ void __launch_bounds__(512, MINB)
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ float red[2][8][kMaxWarps * R];
     const int width = warps * 32, grp = threadIdx.x / width, t = threadIdx.x % width, wg = t >> 5;
-    const int chunks = (a.cols + V - 1) / V, words = row_words(chunks);
+    const int words = row_words((a.cols + 2 * V - 2) / V);
     Walk<MODE, R> walk(grp, groups);
     long long& r0 = walk.r0;
     const long long step = walk.step;
     // columns of a result row's first word that belong to the row before
     const int first = by_words(MODE) ? static_cast<int>((reinterpret_cast<uintptr_t>(static_cast<const T*>(a.out) + r0 * a.out_stride) & 15u) / sizeof(T)) : 0;
-    const int here = by_words(MODE) ? (first + a.cols + V - 1) / V : chunks;   // words of a row
+    const int here = by_words(MODE) ? (first + a.cols + V - 1) / V : a.cols / V;   // words of a row
     const float inv_c = 1.0f / static_cast<float>(a.cols);
     for (int i = threadIdx.x; i < 2 * 8 * kMaxWarps * R; i += blockDim.x) (&red[0][0][0])[i] = 0.0f;
     __syncthreads();
@@ -569,9 +537,9 @@ __global__ void __launch_bounds__(512, MINB)
         weights_at<V>(a.bias, a.w_dtype, (t + i * width) * V - first, a.cols, 0.0f, bias[i]);
     }
     const RowSource<DT> x(a.x, a.x_stride, a.rows, a.cols);
-    // [DEPTH][R][NCH][threads]; kMixed: a group's [DEPTH][R][words] and [R][words] of results
-    uint4* ring = reinterpret_cast<uint4*>(smem) + (MODE != kMixed ? threadIdx.x : grp * (DEPTH + 1) * R * words);
-    uint4* outs = ring + DEPTH * R * words;
+    // [DEPTH][R][NCH][threads]; kMixed: a group's [DEPTH][R][words]
+    uint4* ring = reinterpret_cast<uint4*>(smem) + (MODE != kMixed ? threadIdx.x : grp * DEPTH * R * words);
+    const uint32_t x_off = MODE == kMixed ? (x.row(r0) - first * sizeof(T)) & 15u : 0u;   // of any chunk in its first word
     // words of a stage; where the next rows go and come from
     const int stage = MODE != kMixed ? R * NCH * blockDim.x : R * words;
     uint4* into = ring;
@@ -597,7 +565,12 @@ __global__ void __launch_bounds__(512, MINB)
                             x.copy_word(p, reinterpret_cast<uintptr_t>(q - first + (t + i * width) * V), reinterpret_cast<uintptr_t>(q), reinterpret_cast<uintptr_t>(q + a.cols));
                     }
             } else {
-                x.copy_words(into + k * words, rf + k * walk.apart, a.cols, t, width);
+                const uintptr_t row = reinterpret_cast<uintptr_t>(xf + k * walk.apart * x.stride), to = row + static_cast<uintptr_t>(a.cols) * sizeof(T);
+                const uintptr_t at = row - first * sizeof(T) - x_off;
+#pragma unroll
+                for (int i = 0; i < NCH; ++i)
+                    if (t + i * width < here) x.copy_if_any(into + k * words + t + i * width, at + 16u * (t + i * width), row, to);
+                if (t == 0) x.copy_if_any(into + k * words + here, at + 16u * here, row, to);
             }
         }
         cp_async_commit();
@@ -624,7 +597,7 @@ __global__ void __launch_bounds__(512, MINB)
                     w[k][i] = make_uint4(0, 0, 0, 0);
                     if (t + i * width >= here || r0 + k * walk.apart >= a.rows) continue;
                     const uint4* p = from + k * words + t + i * width;
-                    w[k][i] = masked<DT>(shifted(p[0], p[1], x.row(r0 + k) & 15u), (t + i * width) * V, a.cols);
+                    w[k][i] = masked<DT>(shifted(p[0], p[1], x_off), (t + i * width) * V - first, a.cols);
                 }
             }
         fetch();
@@ -692,21 +665,13 @@ __global__ void __launch_bounds__(512, MINB)
                 unpack(f, o);
                 if (MODE == kAligned)
                     __stcs(reinterpret_cast<uint4*>(y) + t + i * width, narrowed<DT>(o));
-                else if (by_words(MODE))
-                    put_word<DT>(y, c, a.cols, narrowed<DT>(o));
                 else
-                    outs[k * words + 1 + t + i * width] = narrowed<DT>(o);
+                    put_word<DT>(y, c, a.cols, narrowed<DT>(o));
             }
             if (t == 0) {
                 if (a.mean_out != nullptr) a.mean_out[r] = mean[k];
                 if (a.rstd_out != nullptr) a.rstd_out[r] = rstd[k];
             }
-        }
-        if (MODE == kMixed) {
-            group_sync(grp, warps, width);
-#pragma unroll
-            for (int k = 0; k < R; ++k)
-                if (r0 + k < a.rows) write_words<DT>(outs + k * words, reinterpret_cast<uintptr_t>(yr + k * a.out_stride), a.cols, t, width);
         }
     }
 }
@@ -723,13 +688,13 @@ __global__ void __launch_bounds__(512, MINB)
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ float red[2][8][kMaxWarps * 2 * R];
     const int width = warps * 32, grp = threadIdx.x / width, t = threadIdx.x % width, wg = t >> 5;
-    const int chunks = (a.cols + V - 1) / V, words = row_words(chunks);
+    const int words = row_words((a.cols + 2 * V - 2) / V);
     Walk<MODE, R> walk(grp, groups);
     long long& r0 = walk.r0;
     const long long step = walk.step;
     // columns of a result row's first word that belong to the row before
     const int first = by_words(MODE) ? static_cast<int>((reinterpret_cast<uintptr_t>(static_cast<const T*>(a.out) + r0 * a.out_stride) & 15u) / sizeof(T)) : 0;
-    const int here = by_words(MODE) ? (first + a.cols + V - 1) / V : chunks;   // words of a row
+    const int here = by_words(MODE) ? (first + a.cols + V - 1) / V : a.cols / V;   // words of a row
     const float inv_c = 1.0f / static_cast<float>(a.cols);
     for (int i = threadIdx.x; i < 2 * 8 * kMaxWarps * 2 * R; i += blockDim.x) (&red[0][0][0])[i] = 0.0f;
     __syncthreads();
@@ -743,9 +708,11 @@ __global__ void __launch_bounds__(512, MINB)
         for (int e = 0; e < V / 2; ++e) dg2[i][e] = db2[i][e] = 0;
     }
     const RowSource<DT> x(a.x, a.x_stride, a.rows, a.cols), dy(a.dy, a.dy_stride, a.rows, a.cols);
-    // [DEPTH][R][2][NCH][threads]; kMixed: a group's [DEPTH][R][2][words] and [R][words] of results
-    uint4* ring = reinterpret_cast<uint4*>(smem) + (MODE != kMixed ? threadIdx.x : grp * (2 * DEPTH + 1) * R * words);
-    uint4* outs = ring + 2 * DEPTH * R * words;
+    // [DEPTH][R][2][NCH][threads]; kMixed: a group's [DEPTH][R][2][words]
+    uint4* ring = reinterpret_cast<uint4*>(smem) + (MODE != kMixed ? threadIdx.x : grp * 2 * DEPTH * R * words);
+    // of any chunk in its first word
+    const uint32_t x_off = MODE == kMixed ? (x.row(r0) - first * sizeof(T)) & 15u : 0u;
+    const uint32_t d_off = MODE == kMixed ? (dy.row(r0) - first * sizeof(T)) & 15u : 0u;
     // words of a stage; where the next rows go and come from
     const int stage = MODE != kMixed ? 2 * R * NCH * blockDim.x : 2 * R * words;
     int into = 0;
@@ -777,8 +744,18 @@ __global__ void __launch_bounds__(512, MINB)
                     }
             } else {
                 uint4* p = ring + into + k * 2 * words;
-                x.copy_words(p, r, a.cols, t, width);
-                dy.copy_words(p + words, r, a.cols, t, width);
+                const uintptr_t xr = x.row(r), dr = dy.row(r), n = static_cast<uintptr_t>(a.cols) * sizeof(T);
+                const uintptr_t xa = xr - first * sizeof(T) - x_off, da = dr - first * sizeof(T) - d_off;
+#pragma unroll
+                for (int i = 0; i < NCH; ++i)
+                    if (t + i * width < here) {
+                        x.copy_if_any(p + t + i * width, xa + 16u * (t + i * width), xr, xr + n);
+                        dy.copy_if_any(p + words + t + i * width, da + 16u * (t + i * width), dr, dr + n);
+                    }
+                if (t == 0) {
+                    x.copy_if_any(p + here, xa + 16u * here, xr, xr + n);
+                    dy.copy_if_any(p + words + here, da + 16u * here, dr, dr + n);
+                }
             }
         }
         cp_async_commit();
@@ -816,9 +793,9 @@ __global__ void __launch_bounds__(512, MINB)
                     }
                 } else {
                     const uint4* p = ring + from + k * 2 * words + t + i * width;
-                    const int c = (t + i * width) * V;
-                    wx[k][i] = masked<DT>(shifted(p[0], p[1], x.row(r0 + k) & 15u), c, a.cols);
-                    wd[k][i] = masked<DT>(shifted(p[words], p[words + 1], dy.row(r0 + k) & 15u), c, a.cols);
+                    const int c = (t + i * width) * V - first;
+                    wx[k][i] = masked<DT>(shifted(p[0], p[1], x_off), c, a.cols);
+                    wd[k][i] = masked<DT>(shifted(p[words], p[words + 1], d_off), c, a.cols);
                 }
             }
         fetch(r0 + (DEPTH - 1) * step);
@@ -878,17 +855,9 @@ __global__ void __launch_bounds__(512, MINB)
                 unpack(xv, o);
                 if (MODE == kAligned)
                     __stcs(reinterpret_cast<uint4*>(out) + t + i * width, narrowed<DT>(o));
-                else if (by_words(MODE))
-                    put_word<DT>(out, c, a.cols, narrowed<DT>(o));
                 else
-                    outs[k * words + 1 + t + i * width] = narrowed<DT>(o);
+                    put_word<DT>(out, c, a.cols, narrowed<DT>(o));
             }
-        }
-        if (MODE == kMixed) {
-            group_sync(grp, warps, width);
-#pragma unroll
-            for (int k = 0; k < R; ++k)
-                if (r0 + k < a.rows) write_words<DT>(outs + k * words, reinterpret_cast<uintptr_t>(static_cast<T*>(a.out) + (r0 + k) * a.out_stride), a.cols, t, width);
         }
 #pragma unroll
         for (int k = 0; k < R; ++k) mean[k] = next_mean[k], rstd[k] = next_rstd[k];
@@ -1047,7 +1016,7 @@ cudaError_t forward_as(const LnArgs& a, int sms, cudaStream_t st)
 {
     const int chunks = chunks_of<DT>(a.cols, MODE);
     const int warps = (chunks + 32 * NCH - 1) / (32 * NCH);
-    const size_t per = 16u * R * (MODE != kMixed ? static_cast<size_t>(DEPTH) * NCH * 32 * warps : static_cast<size_t>(DEPTH + 1) * row_words(chunks));
+    const size_t per = 16u * R * (MODE != kMixed ? static_cast<size_t>(DEPTH) * NCH * 32 * warps : static_cast<size_t>(DEPTH) * row_words(chunks));
     const RowShape s = row_shape(a, chunks, NCH, R, MINB, per, sms, by_words(MODE));
     return launch_rows(ln_forward_rows<DT, NCH, R, DEPTH, MINB, MODE>, a, s, per * s.groups, st);
 }
@@ -1057,7 +1026,7 @@ cudaError_t backward_as(const LnArgs& a, int sms, cudaStream_t st, int& parts)
 {
     const int chunks = chunks_of<DT>(a.cols, MODE);
     const int warps = (chunks + 32 * NCH - 1) / (32 * NCH);
-    const size_t per = 16u * R * (MODE != kMixed ? static_cast<size_t>(2 * DEPTH) * NCH * 32 * warps : static_cast<size_t>(2 * DEPTH + 1) * row_words(chunks));
+    const size_t per = 16u * R * (MODE != kMixed ? static_cast<size_t>(2 * DEPTH) * NCH * 32 * warps : static_cast<size_t>(2 * DEPTH) * row_words(chunks));
     RowShape s = row_shape(a, chunks, NCH, R, MINB, per, sms, by_words(MODE));
     if (s.grid > kLnMaxParts) s.grid = kLnMaxParts;
     parts = static_cast<int>(s.grid);
@@ -1095,7 +1064,7 @@ cudaError_t forward_of(const LnArgs& a, cudaStream_t st)
         if constexpr (DT == ZERO_FP32)
             return chunks <= 1024 ? forward_as<DT, 2, 2, 3, 1, kFours>(a, sms, st) : forward_as<DT, N, 2, 3, 1, kFours>(a, sms, st);
         else
-            return forward_as<DT, N, 1, 5, 1, kMixed>(a, sms, st);
+            return forward_as<DT, N, 2, 3, 1, kMixed>(a, sms, st);
     }
     const long long grid = a.rows < (1 << 30) ? a.rows : (1 << 30);
     return launch_after(ln_forward_any<DT>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, a);
@@ -1135,7 +1104,7 @@ cudaError_t backward_of(const LnArgs& args, cudaStream_t st)
             else if constexpr (DT == ZERO_FP32)
                 e = chunks <= 1024 ? backward_as<DT, 2, 1, 3, 1, kFours>(a, sms, st, parts) : backward_as<DT, N, 1, 3, 1, kFours>(a, sms, st, parts);
             else
-                e = backward_as<DT, N, 1, 5, 1, kMixed>(a, sms, st, parts);
+                e = backward_as<DT, N, 1, 3, 1, kMixed>(a, sms, st, parts);
         } else {
             const long long grid = a.rows < (1 << 30) ? a.rows : (1 << 30);
             firsts = 0;
