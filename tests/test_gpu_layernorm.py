@@ -308,3 +308,78 @@ def test_graph_capture():
     torch.cuda.synchronize()
     for a, b in zip(want, (c.y, c.dx, c.dgain, c.dbias)):
         assert torch.equal(a, b)
+
+
+class Unlike(Case):
+    """The same with arrays that lie differently: (pad, shift) of x, dy, y and dx."""
+
+    def __init__(self, rows, cols, dt, lies, **kw):
+        self.lies = iter(lies)
+        super().__init__(rows, cols, dt, FP32, **kw)
+        self.desc = z.layernorm(rows, cols, dtype=dt, w_dtype=FP32, eps=EPS, x_stride=self.x.stride(0),
+                                dy_stride=self.dy.stride(0), y_stride=self.y.stride(0), dx_stride=self.dx.stride(0))
+
+    def place(self, t):
+        pad, shift = next(self.lies)
+        buf = torch.full((shift + self.rows * (self.cols + pad) + 16,), float("nan"), dtype=TORCH[self.dt])
+        buf[shift: shift + self.rows * (self.cols + pad)].view(self.rows, -1)[:, : self.cols] = t.to(TORCH[self.dt])
+        buf = buf.cuda()
+        out = buf[shift: shift + self.rows * (self.cols + pad)].view(self.rows, -1)[:, : self.cols]
+        self.buffers = getattr(self, "buffers", []) + [(buf, out)]
+        return out
+
+    def guards_intact(self):
+        for buf, out in self.buffers:
+            c = buf.clone()
+            torch.as_strided(c, out.shape, out.stride(), out.storage_offset()).fill_(float("nan"))
+            assert bool(torch.isnan(c).all())
+
+
+@pytest.mark.parametrize("lies", [((0, 0), (3, 1), (1, 2), (5, 0)), ((1, 1), (0, 0), (2, 7), (3, 3)),
+                                  ((8, 0), (0, 8), (0, 1), (16, 0)), ((5, 0), (0, 0), (0, 0), (0, 0))])
+@pytest.mark.parametrize("rows,cols", [(13, 40), (1201, 97), (90, 130), (13, 768), (301, 1601), (6, 4096), (1300, 2047),
+                                       (200, 8189), (5, 8192)])
+@pytest.mark.parametrize("dt", [BF16, FP16, FP32])
+def test_arrays_that_lie_differently(rows, cols, dt, lies):
+    c = Unlike(rows, cols, dt, lies)
+    c.forward()
+    c.check_forward()
+    c.backward()
+    c.check_backward()
+    c.guards_intact()
+    # over x, whatever dy's alignment
+    x = c.x.clone()
+    d = z.layernorm(rows, cols, dtype=dt, w_dtype=FP32, eps=EPS, x_stride=c.x.stride(0), dy_stride=c.dy.stride(0),
+                    dx_stride=c.x.stride(0))
+    z.zero_layernorm_backward(d, c.dy, c.x, c.gain, c.mean, c.rstd, c.x, c.dgain, c.dbias, c.ws)
+    dx, c.x = c.x, x
+    c.check_backward(dx=dx)
+    c.guards_intact()
+
+
+# rows of which several share a warp: one lane group's rows may run out before another's
+@pytest.mark.parametrize("rows,cols", [(1, 64), (2, 8), (3, 57), (17, 64), (77, 31), (1234, 128), (1235, 121), (999, 113),
+                                       (4001, 9), (9000, 32), (2433, 58), (40003, 24)])
+@pytest.mark.parametrize("pad,shift", [(0, 0), (8, 8), (3, 1)])
+@pytest.mark.parametrize("dt", [BF16, FP16, FP32])
+def test_narrow_rows(rows, cols, dt, pad, shift):
+    c = Case(rows, cols, dt, FP32, pad=pad, shift=shift)
+    c.forward()
+    c.check_forward()
+    c.backward()
+    c.check_backward()
+    c.guards_intact()
+
+
+@pytest.mark.parametrize("cols", [24, 64, 120])
+def test_non_finite_narrow_rows_stay_in_their_rows(cols):
+    c, d = Case(37, cols), Case(37, cols)
+    bad = [0, 6, 18, 36]
+    c.x[bad, 3] = float("nan")
+    good = [r for r in range(37) if r not in bad]
+    for k in (c, d):
+        k.forward()
+        k.backward()
+    assert torch.equal(c.y[good], d.y[good]) and torch.equal(c.dx[good], d.dx[good])
+    assert bool(torch.isnan(c.y[bad]).all()) and bool(torch.isnan(c.dx[bad]).all())
+    assert torch.equal(c.dbias, d.dbias)

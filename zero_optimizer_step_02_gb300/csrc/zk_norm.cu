@@ -389,13 +389,15 @@ __device__ __forceinline__ void put_word(uintptr_t row, int c, int cols, const u
     }
 }
 
-// The rows of a group: row(k) of the set at r0 is r0 + k * apart.
-template <int MODE, int R>
+// The rows of a group: row(k) of the set at r0 is r0 + k * apart.  Groups that
+// share a warp (LANES < 32) walk on while the first of them has rows: r0 < end.
+template <int MODE, int R, int LANES>
 struct Walk {
     static constexpr int apart = by_words(MODE) ? 8 : 1;
-    long long r0, step;
-    __device__ __forceinline__ Walk(int grp, int groups)
+    long long r0, step, end;
+    __device__ __forceinline__ Walk(int grp, int groups, long long rows)
     {
+        end = rows + (LANES < 32 ? grp % (32 / LANES) * R * apart : 0);
         if (by_words(MODE)) {   // gridDim.x is a multiple of 8
             r0 = (blockIdx.x & 7) + 8ll * ((blockIdx.x >> 3) * groups + grp) * R;
             step = 8ll * (gridDim.x >> 3) * groups * R;
@@ -439,17 +441,18 @@ __device__ __forceinline__ void weights_at(const void* w, int dt, int c, int col
 
 constexpr int kMaxWarps = 16;   // of a group
 
-// Sums of N values over a group of `warps` warps, the same in all its threads.
-// Each shuffle step carries as many values as are still apart (N = 4: six
-// shuffles for twenty); red: this group's kMaxWarps * N floats.
-template <int N>
+// Sums of N values over a group of `warps` warps (LANES < 32: of so many lanes
+// of one), the same in all its threads.  Each shuffle step carries as many
+// values as are still apart (N = 4: six shuffles for twenty); red: this group's
+// kMaxWarps * N floats.
+template <int N, int LANES>
 __device__ __forceinline__ void group_sums(float (&v)[N], float* red, int warps, int bar, int width, int wg)
 {
     static_assert(N == 1 || N == 2 || N == 4 || N == 8, "");
     const int lane = threadIdx.x & 31;
-    // halve the values while lanes are left to carry them: lane bits 16, 8, 4
+    // halve the values while lanes are left to carry them: the upper lane bits
     // end up naming the value a lane holds
-    int o = 16;
+    int o = LANES / 2;
 #pragma unroll
     for (int n = N; n > 1; n /= 2, o /= 2) {
         const bool up = lane & o;
@@ -461,11 +464,11 @@ __device__ __forceinline__ void group_sums(float (&v)[N], float* red, int warps,
     }
     float x = v[0];
 #pragma unroll
-    for (int q = 16 / N; q > 0; q /= 2) x += __shfl_xor_sync(0xFFFFFFFFu, x, q);
-    constexpr int kStep = 32 / N;   // lane k * kStep holds value k
-    if (warps == 1) {
+    for (int q = LANES / 2 / N; q > 0; q /= 2) x += __shfl_xor_sync(0xFFFFFFFFu, x, q);
+    constexpr int kStep = LANES / N;   // lane k * kStep holds value k
+    if (LANES < 32 || warps == 1) {
 #pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = N == 1 ? x : __shfl_sync(0xFFFFFFFFu, x, k * kStep);
+        for (int k = 0; k < N; ++k) v[k] = N == 1 ? x : __shfl_sync(0xFFFFFFFFu, x, k * kStep, LANES);
         return;
     }
     if (lane % kStep == 0) red[wg * N + lane / kStep] = x;
@@ -498,10 +501,10 @@ __device__ __forceinline__ void clear_slots(uint4* ring, int t, int width, int h
             for (int k = 0; k < ROWS; ++k) ring[(k * NCH + i) * blockDim.x] = make_uint4(0, 0, 0, 0);
 }
 
-// the threads of a group meet (a group of one warp needs no barrier of its own)
+// the threads of a group meet (a group of one warp, or less, needs no barrier of its own)
 __device__ __forceinline__ void group_sync(int grp, int warps, int width)
 {
-    if (warps == 1)
+    if (warps <= 1)
         __syncwarp();
     else
         named_bar_sync(1 + grp, width);
@@ -509,17 +512,18 @@ __device__ __forceinline__ void group_sync(int grp, int warps, int width)
 
 // Forward: one read, one write.  Two rows at a time, so that their sums share
 // the group's barriers.
-template <int DT, int NCH, int R, int DEPTH, int MINB, int MODE>
+template <int DT, int NCH, int R, int DEPTH, int MINB, int MODE, int LANES = 32>
 __global__ void __launch_bounds__(512, MINB)
-    ln_forward_rows(const __grid_constant__ LnArgs a, int warps, int groups)
+    ln_forward_rows(const __grid_constant__ LnArgs a, int width, int groups)
 {
     using T = typename El<DT>::T;
     constexpr int V = kV<DT>;
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ float red[2][8][kMaxWarps * R];
-    const int width = warps * 32, grp = threadIdx.x / width, t = threadIdx.x % width, wg = t >> 5;
+    if (LANES < 32) width = LANES;
+    const int warps = width / 32, grp = threadIdx.x / width, t = threadIdx.x % width, wg = t >> 5;
     const int words = row_words((a.cols + 2 * V - 2) / V);
-    Walk<MODE, R> walk(grp, groups);
+    Walk<MODE, R, LANES> walk(grp, groups, a.rows);
     long long& r0 = walk.r0;
     const long long step = walk.step;
     // columns of a result row's first word that belong to the row before
@@ -581,7 +585,7 @@ __global__ void __launch_bounds__(512, MINB)
     for (int s = 0; s < DEPTH - 1; ++s) fetch();
     const uint4* from = ring;
     T* yr = static_cast<T*>(a.out) + r0 * a.out_stride;
-    for (; r0 < a.rows; r0 += step, yr += step * a.out_stride, from = from == ring + (DEPTH - 1) * stage ? ring : from + stage) {
+    for (; r0 < walk.end; r0 += step, yr += step * a.out_stride, from = from == ring + (DEPTH - 1) * stage ? ring : from + stage) {
         cp_async_wait<DEPTH - 2>();
         if (MODE == kMixed) group_sync(grp, warps, width);
         uint4 w[R][NCH];
@@ -614,7 +618,7 @@ __global__ void __launch_bounds__(512, MINB)
             }
             mean[k] = both(sum);
         }
-        group_sums<R>(mean, red[0][grp & 7], warps, 1 + grp, width, wg);
+        group_sums<R, LANES>(mean, red[0][grp & 7], warps, 1 + grp, width, wg);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             mean[k] *= inv_c;
@@ -643,7 +647,7 @@ __global__ void __launch_bounds__(512, MINB)
             }
             rstd[k] = both(sum);
         }
-        group_sums<R>(rstd, red[1][grp & 7], warps, 1 + grp, width, wg);
+        group_sums<R, LANES>(rstd, red[1][grp & 7], warps, 1 + grp, width, wg);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             const long long r = r0 + k * walk.apart;
@@ -679,17 +683,18 @@ __global__ void __launch_bounds__(512, MINB)
 // Backward: dx, and the column sums of the rows the CTA took, in one pass.  Each
 // CTA leaves one row of partial sums (at most 304), not an atomic: the same
 // bits every time.
-template <int DT, int NCH, int R, int DEPTH, int MINB, int MODE>
+template <int DT, int NCH, int R, int DEPTH, int MINB, int MODE, int LANES = 32>
 __global__ void __launch_bounds__(512, MINB)
-    ln_backward_rows_fused(const __grid_constant__ LnArgs a, int warps, int groups)
+    ln_backward_rows_fused(const __grid_constant__ LnArgs a, int width, int groups)
 {
     using T = typename El<DT>::T;
     constexpr int V = kV<DT>;
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ float red[2][8][kMaxWarps * 2 * R];
-    const int width = warps * 32, grp = threadIdx.x / width, t = threadIdx.x % width, wg = t >> 5;
+    if (LANES < 32) width = LANES;
+    const int warps = width / 32, grp = threadIdx.x / width, t = threadIdx.x % width, wg = t >> 5;
     const int words = row_words((a.cols + 2 * V - 2) / V);
-    Walk<MODE, R> walk(grp, groups);
+    Walk<MODE, R, LANES> walk(grp, groups, a.rows);
     long long& r0 = walk.r0;
     const long long step = walk.step;
     // columns of a result row's first word that belong to the row before
@@ -770,7 +775,7 @@ __global__ void __launch_bounds__(512, MINB)
         rstd[k] = r < a.rows ? a.rstd[r] : 0.0f;
     }
     int buf = 0;
-    for (int from = 0; r0 < a.rows; r0 += step, from = from == (DEPTH - 1) * stage ? 0 : from + stage, buf ^= 1) {
+    for (int from = 0; r0 < walk.end; r0 += step, from = from == (DEPTH - 1) * stage ? 0 : from + stage, buf ^= 1) {
         cp_async_wait<DEPTH - 2>();
         if (MODE == kMixed) group_sync(grp, warps, width);
         uint4 wx[R][NCH], wd[R][NCH];
@@ -778,7 +783,7 @@ __global__ void __launch_bounds__(512, MINB)
         for (int k = 0; k < R; ++k)
 #pragma unroll
             for (int i = 0; i < NCH; ++i) {
-                if (MODE == kMixed || R > 1) {   // (R = 1: a loop's row is there)
+                if (MODE == kMixed || R > 1 || LANES < 32) {   // (else a loop's row is there)
                     wx[k][i] = wd[k][i] = make_uint4(0, 0, 0, 0);
                     if (t + i * width >= here || r0 + k * walk.apart >= a.rows) continue;
                 }
@@ -829,7 +834,7 @@ __global__ void __launch_bounds__(512, MINB)
             sum[2 * k] = both(s1);
             sum[2 * k + 1] = both(s2);
         }
-        group_sums<2 * R>(sum, red[buf][grp & 7], warps, 1 + grp, width, wg);
+        group_sums<2 * R, LANES>(sum, red[buf][grp & 7], warps, 1 + grp, width, wg);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             if (r0 + k * walk.apart >= a.rows) break;
@@ -961,22 +966,23 @@ constexpr size_t kRowSmem = 220 * 1024;   // of the 227 KB a CTA may have
 
 // how a launch cuts its rows up
 struct RowShape {
-    int warps, groups, threads;
+    int width, groups, threads;
     long long grid;
 };
 
 // Groups share a CTA of up to 512 threads, fewer where the rows would not
 // cover the SMs otherwise.
-RowShape row_shape(const LnArgs& a, int chunks, int nch, int r, int per_sm, size_t group_smem, int sms, bool eights)
+RowShape row_shape(const LnArgs& a, int width, int r, int per_sm, size_t group_smem, int sms, bool eights)
 {
     RowShape s;
-    s.warps = (chunks + 32 * nch - 1) / (32 * nch);
+    s.width = width;
     const long long sets = (a.rows + r - 1) / r;
     const long long spread = (sets + sms - 1) / sms;
-    s.groups = kMaxWarps / s.warps;
+    s.groups = 32 * kMaxWarps / width;
     if (s.groups > static_cast<int>(kRowSmem / per_sm / group_smem)) s.groups = static_cast<int>(kRowSmem / per_sm / group_smem);
     if (s.groups > spread) s.groups = static_cast<int>(spread);
-    s.threads = 32 * s.warps * s.groups;
+    if (width < 32) s.groups = (s.groups + 32 / width - 1) / (32 / width) * (32 / width);   // whole warps
+    s.threads = width * s.groups;
     s.grid = (sets + s.groups - 1) / s.groups;
     if (s.grid > static_cast<long long>(sms) * per_sm) s.grid = static_cast<long long>(sms) * per_sm;
     if (eights) s.grid = s.grid < 8 ? 8 : s.grid / 8 * 8;   // eight kinds of rows
@@ -1008,32 +1014,32 @@ cudaError_t launch_rows(K kernel, const LnArgs& a, const RowShape& s, size_t sme
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return e;
     }
-    return launch_after(kernel, dim3(static_cast<unsigned>(s.grid)), dim3(s.threads), smem, st, a, s.warps, s.groups);
+    return launch_after(kernel, dim3(static_cast<unsigned>(s.grid)), dim3(s.threads), smem, st, a, s.width, s.groups);
 }
 
-template <int DT, int NCH, int R, int DEPTH, int MINB, int MODE>
+template <int DT, int NCH, int R, int DEPTH, int MINB, int MODE, int LANES = 32>
 cudaError_t forward_as(const LnArgs& a, int sms, cudaStream_t st)
 {
     const int chunks = chunks_of<DT>(a.cols, MODE);
-    const int warps = (chunks + 32 * NCH - 1) / (32 * NCH);
-    const size_t per = 16u * R * (MODE != kMixed ? static_cast<size_t>(DEPTH) * NCH * 32 * warps : static_cast<size_t>(DEPTH) * row_words(chunks));
-    const RowShape s = row_shape(a, chunks, NCH, R, MINB, per, sms, by_words(MODE));
-    return launch_rows(ln_forward_rows<DT, NCH, R, DEPTH, MINB, MODE>, a, s, per * s.groups, st);
+    const int width = LANES < 32 ? LANES : (chunks + 32 * NCH - 1) / (32 * NCH) * 32;
+    const size_t per = 16u * R * (MODE != kMixed ? static_cast<size_t>(DEPTH) * NCH * width : static_cast<size_t>(DEPTH) * row_words(chunks));
+    const RowShape s = row_shape(a, width, R, MINB, per, sms, by_words(MODE));
+    return launch_rows(ln_forward_rows<DT, NCH, R, DEPTH, MINB, MODE, LANES>, a, s, per * s.groups, st);
 }
 
-template <int DT, int NCH, int R, int DEPTH, int MINB, int MODE>
+template <int DT, int NCH, int R, int DEPTH, int MINB, int MODE, int LANES = 32>
 cudaError_t backward_as(const LnArgs& a, int sms, cudaStream_t st, int& parts)
 {
     const int chunks = chunks_of<DT>(a.cols, MODE);
-    const int warps = (chunks + 32 * NCH - 1) / (32 * NCH);
-    const size_t per = 16u * R * (MODE != kMixed ? static_cast<size_t>(2 * DEPTH) * NCH * 32 * warps : static_cast<size_t>(2 * DEPTH) * row_words(chunks));
-    RowShape s = row_shape(a, chunks, NCH, R, MINB, per, sms, by_words(MODE));
+    const int width = LANES < 32 ? LANES : (chunks + 32 * NCH - 1) / (32 * NCH) * 32;
+    const size_t per = 16u * R * (MODE != kMixed ? static_cast<size_t>(2 * DEPTH) * NCH * width : static_cast<size_t>(2 * DEPTH) * row_words(chunks));
+    RowShape s = row_shape(a, width, R, MINB, per, sms, by_words(MODE));
     if (s.grid > kLnMaxParts) s.grid = kLnMaxParts;
     parts = static_cast<int>(s.grid);
     size_t smem = per * s.groups;
-    const size_t sums = static_cast<size_t>(s.groups / 2) * 2 * NCH * kV<DT> * 32 * s.warps * sizeof(float);
+    const size_t sums = static_cast<size_t>(s.groups / 2) * 2 * NCH * kV<DT> * s.width * sizeof(float);
     if (smem < sums) smem = sums;
-    return launch_rows(ln_backward_rows_fused<DT, NCH, R, DEPTH, MINB, MODE>, a, s, smem, st);
+    return launch_rows(ln_backward_rows_fused<DT, NCH, R, DEPTH, MINB, MODE, LANES>, a, s, smem, st);
 }
 
 // A thread holds 16 columns of a row (one chunk of it where the row has no more
@@ -1043,6 +1049,27 @@ constexpr int kMaxCols = 8192;
 static_assert(kMaxCols - 2 * 8 >= kLnWide, "narrower rows never take the general kernels");
 template <int DT>
 constexpr int kNch = 16 / kV<DT>;
+// Rows of up to a warp's chunks, one to LANES lanes: the fewest of 8, 16 and 32
+// that hold them, so that few lanes idle and a warp's instructions serve several
+// rows (400000 x 64 bf16: 58 us forward and 80 backward with a warp a row, 21 and
+// 35 with eight lanes; x 128: 58 and 83, 39 and 57 with sixteen).  Two CTAs an
+// SM forward where 64 registers a thread are enough; the forms for 16-bit rows
+// that are not aligned would spill.
+template <int DT, int LANES>
+cudaError_t forward_narrow(const LnArgs& a, int mode, int sms, cudaStream_t st)
+{
+    if (mode == kAligned) return forward_as<DT, 1, 2, 4, 2, kAligned, LANES>(a, sms, st);
+    if (mode == kAlike) return forward_as<DT, 1, 2, 4, DT == ZERO_FP32 ? 2 : 1, kAlike, LANES>(a, sms, st);
+    return forward_as<DT, 1, 2, 3, DT == ZERO_FP32 ? 2 : 1, DT == ZERO_FP32 ? kFours : kMixed, LANES>(a, sms, st);
+}
+template <int DT, int LANES>
+cudaError_t backward_narrow(const LnArgs& a, int mode, int sms, cudaStream_t st, int& parts)
+{
+    if (mode == kAligned) return backward_as<DT, 1, 2, 3, 1, kAligned, LANES>(a, sms, st, parts);
+    if (mode == kAlike) return backward_as<DT, 1, 2, 3, 1, kAlike, LANES>(a, sms, st, parts);
+    return backward_as<DT, 1, 2, 3, 1, DT == ZERO_FP32 ? kFours : kMixed, LANES>(a, sms, st, parts);
+}
+
 template <int DT>
 cudaError_t forward_of(const LnArgs& a, cudaStream_t st)
 {
@@ -1050,13 +1077,11 @@ cudaError_t forward_of(const LnArgs& a, cudaStream_t st)
     const int sms = sms_of_device();
     if (sms == 0) return cudaErrorInvalidDevice;
     const int mode = mode_of<DT>(a.cols, a.x, a.x_stride, a.out, a.out_stride, nullptr, 0);
-    constexpr int N = kNch<DT>, kOther = DT == ZERO_FP32 ? kFours : kMixed;
+    constexpr int N = kNch<DT>;
     const int chunks = chunks_of<DT>(a.cols, mode);
-    if (chunks <= 32) {
-        if (mode == kAligned) return forward_as<DT, 1, 2, 4, 2, kAligned>(a, sms, st);
-        if (mode == kAlike) return forward_as<DT, 1, 2, 4, 2, kAlike>(a, sms, st);
-        return forward_as<DT, 1, 2, 3, 2, kOther>(a, sms, st);
-    }
+    if (chunks <= 8) return forward_narrow<DT, 8>(a, mode, sms, st);
+    if (chunks <= 16) return forward_narrow<DT, 16>(a, mode, sms, st);
+    if (chunks <= 32) return forward_narrow<DT, 32>(a, mode, sms, st);
     if (chunks <= kMaxCols / V) {
         if (mode == kAligned) return forward_as<DT, N, 2, 3, 1, kAligned>(a, sms, st);
         // (fp32 rows up to 4096 columns go eight a thread: 1601 wide 13.7 -> 12.0 us)
@@ -1084,16 +1109,15 @@ cudaError_t backward_of(const LnArgs& args, cudaStream_t st)
         if (by_words(mode))
             for (int k = 0; k < 8; ++k)
                 firsts |= static_cast<uint32_t>((reinterpret_cast<uintptr_t>(a.out) + k * a.out_stride * dtype_bytes(DT)) % 16 / dtype_bytes(DT)) << 4 * k;
-        constexpr int N = kNch<DT>, kOther = DT == ZERO_FP32 ? kFours : kMixed;
+        constexpr int N = kNch<DT>;
         const int chunks = chunks_of<DT>(a.cols, mode);
         cudaError_t e;
-        if (chunks <= 32) {
-            if (mode == kAligned)
-                e = backward_as<DT, 1, 2, 3, 1, kAligned>(a, sms, st, parts);
-            else if (mode == kAlike)
-                e = backward_as<DT, 1, 2, 3, 1, kAlike>(a, sms, st, parts);
-            else
-                e = backward_as<DT, 1, 2, 3, 1, kOther>(a, sms, st, parts);
+        if (chunks <= 8) {
+            e = backward_narrow<DT, 8>(a, mode, sms, st, parts);
+        } else if (chunks <= 16) {
+            e = backward_narrow<DT, 16>(a, mode, sms, st, parts);
+        } else if (chunks <= 32) {
+            e = backward_narrow<DT, 32>(a, mode, sms, st, parts);
         } else if (chunks <= kMaxCols / V) {
             // (fp32 rows up to 4096 columns that are not aligned go eight a
             // thread: with sixteen these forms spill, 1601 wide 24.8 -> 19.6 us)
