@@ -96,97 +96,6 @@ __device__ __forceinline__ float block_sum(float v, float* red)
     return s;
 }
 
-// ------------------------------------------------------ any width, any stride
-// For rows too wide for the kernels below.  One CTA a row, one element a thread
-// at a time; the row is read three times, the last two from cache.  About a
-// sixth of a copy's rate: rows of more than 8192 columns are rare, so these
-// forms are kept short (and right for any width and alignment).
-template <int DT>
-__global__ void __launch_bounds__(256) ln_forward_any(const __grid_constant__ LnArgs a)
-{
-    using E = El<DT>;
-    __shared__ float red[32];
-    const float inv_c = 1.0f / static_cast<float>(a.cols);
-    pdl_wait();
-    pdl_launch();
-    for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        const typename E::T* x = static_cast<const typename E::T*>(a.x) + r * a.x_stride;
-        typename E::T* y = static_cast<typename E::T*>(a.out) + r * a.out_stride;
-        float s = 0.0f;
-        for (int c = threadIdx.x; c < a.cols; c += blockDim.x) s += E::up(x[c]);
-        const float mean = block_sum(s, red) * inv_c;
-        float q = 0.0f;
-        for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
-            const float d = E::up(x[c]) - mean;
-            q = fmaf(d, d, q);
-        }
-        const float rstd = 1.0f / sqrtf(block_sum(q, red) * inv_c + a.eps);
-        for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
-            const float g = a.gain != nullptr ? weight_at(a.gain, a.w_dtype, c) : 1.0f;
-            const float b = a.bias != nullptr ? weight_at(a.bias, a.w_dtype, c) : 0.0f;
-            y[c] = E::down(fmaf((E::up(x[c]) - mean) * rstd, g, b));
-        }
-        if (threadIdx.x == 0) {
-            if (a.mean_out != nullptr) a.mean_out[r] = mean;
-            if (a.rstd_out != nullptr) a.rstd_out[r] = rstd;
-        }
-    }
-}
-
-// the two row means of the backward pass
-template <int DT>
-__global__ void __launch_bounds__(256) ln_backward_rows(const __grid_constant__ LnArgs a)
-{
-    using E = El<DT>;
-    __shared__ float red[32];
-    const float inv_c = 1.0f / static_cast<float>(a.cols);
-    pdl_wait();
-    pdl_launch();
-    for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        const typename E::T* x = static_cast<const typename E::T*>(a.x) + r * a.x_stride;
-        const typename E::T* dy = static_cast<const typename E::T*>(a.dy) + r * a.dy_stride;
-        const float mean = a.mean[r], rstd = a.rstd[r];
-        float s1 = 0.0f, s2 = 0.0f;
-        for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
-            const float h = E::up(dy[c]) * (a.gain != nullptr ? weight_at(a.gain, a.w_dtype, c) : 1.0f);
-            s1 += h;
-            s2 = fmaf(h, (E::up(x[c]) - mean) * rstd, s2);
-        }
-        s1 = block_sum(s1, red) * inv_c;
-        s2 = block_sum(s2, red) * inv_c;
-        if (threadIdx.x == 0) {
-            a.rowsums[2 * r] = s1;
-            a.rowsums[2 * r + 1] = s2;
-        }
-    }
-}
-
-// dx and the partial column sums: blockIdx.x takes 256 columns, blockIdx.y
-// every gridDim.y-th row
-template <int DT>
-__global__ void __launch_bounds__(256) ln_backward_cols(const __grid_constant__ LnArgs a)
-{
-    using E = El<DT>;
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    pdl_wait();
-    pdl_launch();
-    if (c >= a.cols) return;
-    const float gain = a.gain != nullptr ? weight_at(a.gain, a.w_dtype, c) : 1.0f;
-    float dg = 0.0f, db = 0.0f;
-    for (long long r = blockIdx.y; r < a.rows; r += gridDim.y) {
-        const float rstd = a.rstd[r];
-        const float xhat = (E::up(static_cast<const typename E::T*>(a.x)[r * a.x_stride + c]) - a.mean[r]) * rstd;
-        const float dy = E::up(static_cast<const typename E::T*>(a.dy)[r * a.dy_stride + c]);
-        dg = fmaf(dy, xhat, dg);
-        db += dy;
-        const float dx = rstd * (dy * gain - a.rowsums[2 * r] - xhat * a.rowsums[2 * r + 1]);
-        static_cast<typename E::T*>(a.out)[r * a.out_stride + c] = E::down(dx);
-    }
-    float* p = a.parts + static_cast<long long>(blockIdx.y) * 2 * a.pitch;
-    p[c] = dg;
-    p[a.pitch + c] = db;
-}
-
 // ------------------------------------------------------------- row pipelines
 // A row is cut into chunks of 16 bytes (V = 8 or 4 columns).  A group of
 // `warps` warps takes R consecutive rows at a time, thread t of the group the
@@ -920,6 +829,178 @@ __global__ void __launch_bounds__(512, MINB)
     }
 }
 
+// ------------------------------------------------------ any width, any stride
+// For rows too wide for the pipelines above.  One CTA a row; the row is read
+// three times forward and twice backward, all but the first from cache.
+// VEC: every row lies on 16-byte words and is a whole number of them; else one
+// element at a time.  A piece is what a thread takes at once (V columns or one).
+// 4096 x 16384 bf16: forward 73 us (3.7 TB/s; floor 39.6), backward 171 us (floor
+// 59; its second kernel reads x and dy again); one element at a time 234 and 324.
+template <int DT, bool VEC>
+constexpr int kPiece = VEC ? kV<DT> : 1;
+constexpr int kWideThreads = 512;
+
+template <int DT, bool VEC>
+__device__ __forceinline__ void get_piece(const void* row, int c, float (&v)[kPiece<DT, VEC>])
+{
+    const typename El<DT>::T* p = static_cast<const typename El<DT>::T*>(row) + c;
+    if constexpr (VEC)
+        widen<DT>(*reinterpret_cast<const uint4*>(p), v);
+    else
+        v[0] = El<DT>::up(*p);
+}
+template <int DT, bool VEC>
+__device__ __forceinline__ void put_piece(void* row, int c, const float (&v)[kPiece<DT, VEC>])
+{
+    typename El<DT>::T* p = static_cast<typename El<DT>::T*>(row) + c;
+    if constexpr (VEC)
+        __stcs(reinterpret_cast<uint4*>(p), narrowed<DT>(v));
+    else
+        *p = El<DT>::down(v[0]);
+}
+template <int DT, bool VEC>
+__device__ __forceinline__ void get_weights(const void* w, int dt, int c, int cols, float none, float (&v)[kPiece<DT, VEC>])
+{
+    if constexpr (VEC) {
+        f32x2 p[kV<DT> / 2];
+        weights_at<kV<DT>>(w, dt, c, cols, none, p);
+        unpack(p, v);
+    } else {
+        v[0] = w == nullptr ? none : weight_at(w, dt, c);
+    }
+}
+
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(kWideThreads, 2) ln_forward_any(const __grid_constant__ LnArgs a)
+{
+    using T = typename El<DT>::T;
+    constexpr int P = kPiece<DT, VEC>;
+    __shared__ float red[32];
+    const float inv_c = 1.0f / static_cast<float>(a.cols);
+    pdl_wait();
+    pdl_launch();
+    for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
+        const T* x = static_cast<const T*>(a.x) + r * a.x_stride;
+        T* y = static_cast<T*>(a.out) + r * a.out_stride;
+        float s = 0.0f;
+#pragma unroll 4
+        for (int c = threadIdx.x * P; c < a.cols; c += kWideThreads * P) {
+            float v[P];
+            get_piece<DT, VEC>(x, c, v);
+#pragma unroll
+            for (int e = 0; e < P; ++e) s += v[e];
+        }
+        const float mean = block_sum(s, red) * inv_c;
+        float q = 0.0f;
+#pragma unroll 4
+        for (int c = threadIdx.x * P; c < a.cols; c += kWideThreads * P) {
+            float v[P];
+            get_piece<DT, VEC>(x, c, v);
+#pragma unroll
+            for (int e = 0; e < P; ++e) q = fmaf(v[e] - mean, v[e] - mean, q);
+        }
+        const float rstd = inverse_root(block_sum(q, red) * inv_c + a.eps);
+#pragma unroll 2
+        for (int c = threadIdx.x * P; c < a.cols; c += kWideThreads * P) {
+            float v[P], g[P], b[P];
+            get_piece<DT, VEC>(x, c, v);
+            get_weights<DT, VEC>(a.gain, a.w_dtype, c, a.cols, 1.0f, g);
+            get_weights<DT, VEC>(a.bias, a.w_dtype, c, a.cols, 0.0f, b);
+#pragma unroll
+            for (int e = 0; e < P; ++e) v[e] = fmaf((v[e] - mean) * rstd, g[e], b[e]);
+            put_piece<DT, VEC>(y, c, v);
+        }
+        if (threadIdx.x == 0) {
+            if (a.mean_out != nullptr) a.mean_out[r] = mean;
+            if (a.rstd_out != nullptr) a.rstd_out[r] = rstd;
+        }
+    }
+}
+
+// the two row means of the backward pass
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(kWideThreads, 2) ln_backward_rows(const __grid_constant__ LnArgs a)
+{
+    using T = typename El<DT>::T;
+    constexpr int P = kPiece<DT, VEC>;
+    __shared__ float red[32];
+    const float inv_c = 1.0f / static_cast<float>(a.cols);
+    pdl_wait();
+    pdl_launch();
+    for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
+        const T* x = static_cast<const T*>(a.x) + r * a.x_stride;
+        const T* dy = static_cast<const T*>(a.dy) + r * a.dy_stride;
+        const float mean = a.mean[r], rstd = a.rstd[r];
+        float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll 2
+        for (int c = threadIdx.x * P; c < a.cols; c += kWideThreads * P) {
+            float v[P], d[P], g[P];
+            get_piece<DT, VEC>(x, c, v);
+            get_piece<DT, VEC>(dy, c, d);
+            get_weights<DT, VEC>(a.gain, a.w_dtype, c, a.cols, 1.0f, g);
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+                const float h = d[e] * g[e];
+                s1 += h;
+                s2 = fmaf(h, (v[e] - mean) * rstd, s2);
+            }
+        }
+        s1 = block_sum(s1, red) * inv_c;
+        s2 = block_sum(s2, red) * inv_c;
+        if (threadIdx.x == 0) {
+            a.rowsums[2 * r] = s1;
+            a.rowsums[2 * r + 1] = s2;
+        }
+    }
+}
+
+// dx and the partial column sums: blockIdx.x takes 256 pieces of columns,
+// blockIdx.y every gridDim.y-th row, a few under way at a time
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(256) ln_backward_cols(const __grid_constant__ LnArgs a)
+{
+    using T = typename El<DT>::T;
+    constexpr int P = kPiece<DT, VEC>, K = 2;
+    const int c = (blockIdx.x * 256 + threadIdx.x) * P;
+    pdl_wait();
+    pdl_launch();
+    if (c >= a.cols) return;
+    float g[P], dg[P], db[P];
+    get_weights<DT, VEC>(a.gain, a.w_dtype, c, a.cols, 1.0f, g);
+#pragma unroll
+    for (int e = 0; e < P; ++e) dg[e] = db[e] = 0.0f;
+    for (long long r0 = blockIdx.y; r0 < a.rows; r0 += K * static_cast<long long>(gridDim.y)) {
+        float v[K][P], d[K][P];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const long long r = r0 + k * static_cast<long long>(gridDim.y);
+            if (r >= a.rows) break;
+            get_piece<DT, VEC>(static_cast<const T*>(a.x) + r * a.x_stride, c, v[k]);
+            get_piece<DT, VEC>(static_cast<const T*>(a.dy) + r * a.dy_stride, c, d[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const long long r = r0 + k * static_cast<long long>(gridDim.y);
+            if (r >= a.rows) break;
+            const float mean = a.mean[r], rstd = a.rstd[r], s1 = a.rowsums[2 * r], s2 = a.rowsums[2 * r + 1];
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+                const float xhat = (v[k][e] - mean) * rstd;
+                dg[e] = fmaf(d[k][e], xhat, dg[e]);
+                db[e] += d[k][e];
+                v[k][e] = rstd * (d[k][e] * g[e] - s1 - xhat * s2);
+            }
+            put_piece<DT, VEC>(static_cast<T*>(a.out) + r * a.out_stride, c, v[k]);
+        }
+    }
+    float* p = a.parts + static_cast<long long>(blockIdx.y) * 2 * a.pitch + c;
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+        p[e] = dg[e];
+        p[a.pitch + e] = db[e];
+    }
+}
+
 // The partial column sums, in a fixed order: 32 columns a CTA, sixteen slices
 // of the parts side by side.  5 MB for 4096 columns, out of L2; 2 to 3 us after
 // the rows' kernel, whose end it waits for (fp64 sums: 3 us more).
@@ -1092,7 +1173,8 @@ cudaError_t forward_of(const LnArgs& a, cudaStream_t st)
             return forward_as<DT, N, 2, 3, 1, kMixed>(a, sms, st);
     }
     const long long grid = a.rows < (1 << 30) ? a.rows : (1 << 30);
-    return launch_after(ln_forward_any<DT>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, a);
+    if (mode == kAligned) return launch_after(ln_forward_any<DT, true>, dim3(static_cast<unsigned>(grid)), dim3(kWideThreads), 0, st, a);
+    return launch_after(ln_forward_any<DT, false>, dim3(static_cast<unsigned>(grid)), dim3(kWideThreads), 0, st, a);
 }
 
 template <int DT>
@@ -1132,8 +1214,19 @@ cudaError_t backward_of(const LnArgs& args, cudaStream_t st)
         } else {
             const long long grid = a.rows < (1 << 30) ? a.rows : (1 << 30);
             firsts = 0;
-            e = launch_after(ln_backward_rows<DT>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, a);
-            if (e == cudaSuccess) e = launch_after(ln_backward_cols<DT>, dim3((a.cols + 255) / 256, parts), dim3(256), 0, st, a);
+            const bool vec = mode == kAligned;
+            const int across = (a.cols + 256 * (vec ? V : 1) - 1) / (256 * (vec ? V : 1));
+            // as many CTAs as the SMs hold at a time: a part more is two rows of
+            // sums more (304 parts: 209 and 249 us for 4096 x 16384 and 500 x 65536,
+            // so 171 and 120); sixteen at least keep the chains of sums short
+            int most = ((vec ? 3 : 8) * sms + across - 1) / across;
+            if (most < 16) most = 16;
+            if (parts > most) parts = most;
+            const dim3 cols(across, parts);
+            const auto rows_of = vec ? ln_backward_rows<DT, true> : ln_backward_rows<DT, false>;
+            const auto cols_of = vec ? ln_backward_cols<DT, true> : ln_backward_cols<DT, false>;
+            e = launch_after(rows_of, dim3(static_cast<unsigned>(grid)), dim3(kWideThreads), 0, st, a);
+            if (e == cudaSuccess) e = launch_after(cols_of, cols, dim3(256), 0, st, a);
         }
         if (e != cudaSuccess) return e;
     }
