@@ -116,9 +116,8 @@ struct Phase {
     unsigned tile_target;        // tile_bar's count once all parts of a tile of this phase are there
     int res;
     float alpha, beta;
-    const __half* add_hi;        // this matrix's
+    const __half* add_hi;        // this matrix's; rows out.ld apart
     const __half* add_lo;
-    long long add_ld;
     DevPlanes out;               // RES_PLANES*: this matrix's
     void* res_out;               // RES_OUT, RES_MUON: this matrix's result, or master and 16-bit weights
     float* master;
@@ -247,28 +246,26 @@ __device__ __forceinline__ void put_planes8(const Eight& x, __half* hi, __half* 
 // what becomes of a phase's sums: a pair of fp16 planes, the result, or the weights
 enum { RES_PLANES = 0, RES_OUT = 1, RES_MUON = 2 };
 
-// What the results of a phase need, in registers.
+// What the results of a phase need, in registers.  Addends and results that are
+// planes lie alike: one offset (in elements, below 2^32 in any matrix) for all.
 struct Results {
     int m, n, res;
     float alpha, beta;
     const __half* add_hi;
     const __half* add_lo;
-    int add_ld;
     __half* hi;
     __half* lo;
-    int ld;
+    uint32_t ld;
 
     __device__ __forceinline__ explicit Results(const Phase& ph)
-        : m(ph.m), n(ph.n), res(ph.res), alpha(ph.alpha), beta(ph.beta), add_hi(ph.add_hi), add_lo(ph.add_lo),
-          add_ld(static_cast<int>(ph.add_ld)), hi(ph.out.hi), lo(ph.out.lo), ld(static_cast<int>(ph.out.ld))
+        : m(ph.m), n(ph.n), res(ph.res), alpha(ph.alpha), beta(ph.beta), add_hi(ph.add_hi), add_lo(ph.add_lo), hi(ph.out.hi),
+          lo(ph.out.lo), ld(static_cast<uint32_t>(ph.out.ld))
     {
     }
-    __device__ __forceinline__ void load(int row, int col, Addend& x) const
+    __device__ __forceinline__ void load(bool there, uint32_t at, Addend& x) const
     {
         x.zero();
-        if (add_hi == nullptr || row >= m || col >= n) return;
-        const long long at = static_cast<long long>(row) * add_ld + col;
-        x.load(add_hi + at, add_lo != nullptr ? add_lo + at : nullptr);
+        if (there && add_hi != nullptr) x.load(add_hi + at, add_lo != nullptr ? add_lo + at : nullptr);
     }
 };
 
@@ -289,13 +286,11 @@ __device__ __noinline__ void put_last(const Phase* ph, int row, int col, Eight u
 }
 
 // eight sums of one row from column `col`, to where they belong
-__device__ __forceinline__ void put_results(const Results& r, const Phase& ph, int row, int col, const Addend& x, Eight& u)
+__device__ __forceinline__ void put_results(const Results& r, const Phase& ph, int row, int col, uint32_t at, const Addend& x, Eight& u)
 {
-    if (row >= r.m || col >= r.n) return;
     u.combine(pack2(r.alpha, r.alpha), pack2(r.beta, r.beta), x);
     if (r.res == RES_PLANES) {
-        const long long o = static_cast<long long>(row) * r.ld + col;
-        put_planes8(u, r.hi + o, r.lo != nullptr ? r.lo + o : nullptr);
+        put_planes8(u, r.hi + at, r.lo != nullptr ? r.lo + at : nullptr);
     } else {
         put_last(&ph, row, col, u);
     }
@@ -314,39 +309,63 @@ __device__ __forceinline__ void load_sums(uint32_t tmem, float (&v)[32])
     }
 }
 
+__device__ __forceinline__ void smem_put(uint32_t addr, float a, float b, float c, float d)
+{
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
+}
+__device__ __forceinline__ float4 smem_get(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
 // The results of a whole tile, by eight warps: `quarter` the 32 TMEM lanes
 // (rows) this one may read, `half` its half of the columns.  A lane of TMEM is
 // a row; memory wants whole rows side by side.  32 x 32 sums at a time turn in
-// shared memory (16-byte chunks, swizzled by the row): lane l then has the
-// columns 8 (l % 4) + .. of the rows l / 4 + 8 i.  What the results need from
-// memory is loaded before the sums.
+// shared memory (16-byte chunks, swizzled by the row: chunk i of row l at
+// l * 128 + (i ^ l % 8) * 16): lane l then has the columns 8 (l % 4) + .. of the
+// rows l / 4 + 8 i.  What the results need from memory is loaded before the
+// sums.  turn: the buffer, on 128 bytes.
 template <int BN, bool JOINT>
 __device__ __forceinline__ void tile_results(const Results& r, const Phase& ph, const Tile& tl, uint32_t tmem, int quarter,
-                                             int half, int lane, unsigned char* turn)
+                                             int half, int lane, uint32_t turn)
 {
     const int row0 = tl.m0 + quarter * 32 + lane / 4;
+    const uint32_t down = 8 * r.ld;
+    const uint32_t in = turn + lane * 128 + (lane & 7) * 16;
+    const uint32_t out = turn + lane / 4 * 128 + ((lane % 4 * 2) ^ (lane / 4)) * 16;
+    int col = tl.n0 + half * (BN / 2) + lane % 4 * 8;
+    uint32_t at = static_cast<uint32_t>(row0) * r.ld + col;
 #pragma unroll 1
-    for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 32) {
+    for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 32, col += 32, at += 32) {
         if (tl.n0 + c >= r.n) break;
-        const int col = tl.n0 + c + lane % 4 * 8;
         Addend x[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) r.load(row0 + 8 * i, col, x[i]);
-        float v[32];
-        load_sums<BN, JOINT>(tmem + c, v);
+        for (int i = 0; i < 4; ++i) r.load(row0 + 8 * i < r.m && col < r.n, at + i * down, x[i]);
         __syncwarp();
+        constexpr int kAt = JOINT ? 16 : 32;   // sums at a time: two accumulators' 32 would spill
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<float4*>(turn + lane * 128 + ((i ^ (lane & 7)) * 16)) =
-                make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        for (int h = 0; h < 32 / kAt; ++h) {
+            float v[kAt];
+            if constexpr (JOINT) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+                tmem_add16(tmem + c + 16 * h, v);
+                tmem_add16(tmem + BN + c + 16 * h, v);
+            } else {
+                tmem_load32(tmem + c, v);
+            }
+#pragma unroll
+            for (int i = 0; i < kAt / 4; ++i)
+                smem_put(in ^ (64 * h + 16 * i), v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        }
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int k = lane / 4 + 8 * i, ch = lane % 4 * 2;
             Eight u;
-            u.set(*reinterpret_cast<const float4*>(turn + k * 128 + ((ch ^ (k & 7)) * 16)),
-                  *reinterpret_cast<const float4*>(turn + k * 128 + (((ch + 1) ^ (k & 7)) * 16)));
-            put_results(r, ph, row0 + 8 * i, col, x[i], u);
+            u.set(smem_get(out + 1024 * i), smem_get((out ^ 16) + 1024 * i));
+            if (row0 + 8 * i < r.m && col < r.n) put_results(r, ph, row0 + 8 * i, col, at + i * down, x[i], u);
         }
     }
 }
@@ -366,8 +385,9 @@ __device__ __forceinline__ void split_results(const Results& r, const Phase& ph,
         const int unit = part * units + i % units, k = i / units;
         const int row = tl.m0 + k, col = tl.n0 + 8 * unit;
         if (row >= r.m || col >= r.n) continue;
+        const uint32_t at = static_cast<uint32_t>(row) * r.ld + col;
         Addend x;
-        r.load(row, col, x);
+        r.load(true, at, x);
         const float4* p = reinterpret_cast<const float4*>(parts + unit * (kBM * 8) + k * 8);
         Eight u;
         u.set(make_float4(0.0f, 0.0f, 0.0f, 0.0f), make_float4(0.0f, 0.0f, 0.0f, 0.0f));
@@ -380,7 +400,7 @@ __device__ __forceinline__ void split_results(const Results& r, const Phase& ph,
 #pragma unroll
             for (int e = 0; e < 4; ++e) u.v[e] = add2(add2(u.v[e], y.v[e]), z.v[e]);
         }
-        put_results(r, ph, row, col, x, u);
+        put_results(r, ph, row, col, at, x, u);
     }
 }
 
@@ -513,7 +533,6 @@ __device__ __forceinline__ void set_phase(Phase& ph, const NsKernelArgs& a, int 
     ph.alpha = kInvScale;
     ph.beta = 0.0f;
     ph.add_hi = ph.add_lo = nullptr;
-    ph.add_ld = 0;
     if (kind == 0) {
         ph.a = ph.b = xm;
         ph.a_mode = ph.b_mode = a.wide ? kMajorK : kMajorMN;
@@ -528,7 +547,6 @@ __device__ __forceinline__ void set_phase(Phase& ph, const NsKernelArgs& a, int 
         ph.beta = a.coef[s][1];
         ph.add_hi = a.g.hi + b * a.g.stride;
         ph.add_lo = a.g.lo != nullptr ? a.g.lo + b * a.g.stride : nullptr;
-        ph.add_ld = a.g.ld;
         ph.out = a.p;
     } else {
         ph.a = a.wide ? a.pmap : xm;
@@ -541,7 +559,6 @@ __device__ __forceinline__ void set_phase(Phase& ph, const NsKernelArgs& a, int 
         ph.beta = a.coef[s][0];
         ph.add_hi = xi.hi + b * xi.stride;
         ph.add_lo = xi.lo + b * xi.stride;
-        ph.add_ld = xi.ld;
         ph.out = xo;
         if (last) {   // x itself leaves: scaled back
             ph.res = a.res;
@@ -673,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
     tc_fence_after();
     const uint32_t tmem = tmem_base;
 
-    unsigned char* turn = ring + S::kStages * S::kStageBytes + (warp - 2) * kTurnBytes;   // of the epilogue warps
+    const uint32_t turn = smem_u32(ring) + S::kStages * S::kStageBytes + (warp - 2) * kTurnBytes;   // of the epilogue warps
 
     // where the roles are in the ring and the accumulators, over all phases
     Slot<S::kStages> slot;
