@@ -709,8 +709,8 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
         first_operand(a, b, cta, red, &shared_scale);
         for (int phase = 0; phase < 3 * a.steps; ++phase) {
             // the group's results of the phase before, for everyone's TMA loads
+            // (the barrier orders this CTA's before thread 0's release)
             fence_proxy_async_global();
-            __threadfence();
             __syncthreads();
             if (threadIdx.x == 0) {
                 met += a.ctas;
@@ -874,8 +874,8 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
                     }
                     acc.next();
                     if (ph.split == 1) continue;
-                    // the tile's parts meet, then each adds up its columns
-                    __threadfence();
+                    // the tile's parts meet, then each adds up its columns (the
+                    // barrier orders this CTA's sums before the release)
                     named_bar_sync(1, kEpiWarps * 32);
                     if (threadIdx.x == 64 && !abort_flag) {
                         unsigned* bar = a.tile_bar + group * a.ctas + t * CG + rank;
