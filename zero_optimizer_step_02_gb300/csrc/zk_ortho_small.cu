@@ -180,7 +180,7 @@ __device__ __forceinline__ void ns_small_body(const SmallNsArgs& a, const MuonAr
     const int row = (warp & 3) * 32 + lane;   // this thread's line: its warp's quarter of TMEM
     const int fourth = warp >> 2;             // its warp's part of the columns
     const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const int width = (a.m + 15) / 16 * 16;
+    const int width = (a.m + 15) / 16 * 16, length = (a.n + 15) / 16 * 16;   // what the products cover
     uint32_t parity = 0;
     int failed = 0;
     for (int phase = 0; phase < 3 * a.steps; ++phase) {
@@ -192,11 +192,11 @@ __device__ __forceinline__ void ns_small_body(const SmallNsArgs& a, const MuonAr
             tc_fence_after();
             if (elect_one()) {
                 if (kind == 0)
-                    issue(tmem, xs, x_lo, xs, x_lo, width, (a.n + 15) / 16, false);
+                    issue(tmem, xs, x_lo, xs, x_lo, width, length / 16, false);
                 else if (kind == 1)
                     issue(tmem, gs, g_lo, gs, g_lo, width, width / 16, false);
                 else
-                    issue(tmem, gs, g_lo, xs, x_lo, a.panels * 64, width / 16, true);
+                    issue(tmem, gs, g_lo, xs, x_lo, length, width / 16, true);
                 mma_commit<1>(&bar);
             }
             __syncwarp();
@@ -212,7 +212,7 @@ __device__ __forceinline__ void ns_small_body(const SmallNsArgs& a, const MuonAr
         const int lo = kind == 2 ? x_lo : g_lo;
         const float alpha = (kind == 1 ? a.coef[s][2] : 1.0f) * (last ? kInvScale * kInvScale : kInvScale);
         const float beta = kind == 0 ? 0.0f : (kind == 1 ? a.coef[s][1] : a.coef[s][0]) * (last ? kInvScale : 1.0f);
-        const int cols = kind == 2 ? a.panels * 64 : width;
+        const int cols = kind == 2 ? length : width;
         for (int c = fourth * 16; c < cols; c += 64) {
             float v[16];
 #pragma unroll
