@@ -349,10 +349,7 @@ __device__ __forceinline__ void tile_results(const Results& r, const Phase& ph, 
         for (int h = 0; h < 32 / kAt; ++h) {
             float v[kAt];
             if constexpr (JOINT) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-                tmem_add16(tmem + c + 16 * h, v);
-                tmem_add16(tmem + BN + c + 16 * h, v);
+                tmem_sum16(tmem + c + 16 * h, tmem + BN + c + 16 * h, v);
             } else {
                 tmem_load32(tmem + c, v);
             }

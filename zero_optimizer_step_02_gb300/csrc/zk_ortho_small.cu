@@ -215,10 +215,7 @@ __device__ __forceinline__ void ns_small_body(const SmallNsArgs& a, const MuonAr
         const int cols = kind == 2 ? length : width;
         for (int c = fourth * 16; c < cols; c += 64) {
             float v[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = 0.0f;
-            tmem_add16(mine + c, v);
-            tmem_add16(mine + kTmemSmall + c, v);
+            tmem_sum16(mine + c, mine + kTmemSmall + c, v);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 float u[8];
