@@ -14,15 +14,16 @@
 //
 // Bound: memory.  Forward reads x and writes y, backward reads x and dy and
 // writes dx; at 6783 GB/s (a copy's rate) 8192 x 4096 bf16 cannot take less than
-// 19.8 us forward and 29.7 us backward.  Measured: forward 25.4 us (5280 GB/s,
-// 0.78 of a copy), 16384 x 4096 45.8 us (5860, 0.86); backward 16384 x 4096 74.3
-// us (5420, 0.80), its second kernel included.  What is left is issue: a CTA of
-// sixteen warps an SM, 60% of the issue slots busy, fixed-latency and shared-
-// memory waits in between.  Few rows are bound by latency: 8 x 768 2.4 us, 256 x
-// 768 backward 6.1 us (two kernels, the second's start hidden behind the first).
-// Rows that do not lie on 16-byte words pay for it: 2999 x 1601 fp32 forward
-// 12.0 us alike and 12.5 us with unlike gaps (floor 5.7), 5003 x 1601 fp16
-// backward 24.1 us (floor 7.1).
+// 19.8 us forward and 29.7 us backward.  Measured: forward 22.7 us (0.87 of a
+// copy), 16384 x 4096 42.5 us (0.93); backward 16384 x 4096 72 us (0.82; fp32 128
+// us, 0.93), its second kernel included.  Next to memory it is issue: a CTA of
+// sixteen warps an SM, 53% of the issue slots busy, fixed-latency and shared-
+// memory waits in between; every instruction a row fewer showed (the root and the
+// division 4 to 9%, addresses kept from row to row 4 to 20%).  Few rows are bound
+// by latency: 8 x 768 2.4 us, 256 x 768 backward 6 us (two kernels, the second's
+// start hidden behind the first).  Rows that do not lie on 16-byte words pay for
+// it: 2999 x 1601 fp32 forward 10.7 us alike and 11.2 us with unlike gaps (floor
+// 5.7), 5003 x 1601 fp16 backward 22.3 us (floor 7.1).
 #include "zk_common.cuh"
 #include "zk_launch.h"
 #include "zk_ops.h"
@@ -126,6 +127,10 @@ __device__ __forceinline__ float block_sum(float v, float* red)
 //             own thread's and the next one's, shifted into place.
 enum { kAligned = 0, kAlike = 1, kMixed = 2, kFours = 3 };
 __host__ __device__ constexpr bool by_words(int mode) { return mode != kAligned; }
+// Where rows begin and end inside a word but slots are private, thread 0 takes
+// the last chunk and all others one less: the two chunks that need care are then
+// in one warp (16384 x 1601 bf16 backward 52.4 -> 48.8 us).
+__host__ __device__ constexpr bool by_turns(int mode) { return mode == kAlike || mode == kFours; }
 
 template <int DT>
 constexpr int kV = DT == ZERO_FP32 ? 4 : 8;
@@ -246,10 +251,11 @@ struct RowSource {
     __device__ __forceinline__ uintptr_t row(long long r) const { return reinterpret_cast<uintptr_t>(base + r * stride); }
 
     // The aligned word at `at`, which holds elements of the row [from, to), into
-    // *dst: whole if it lies inside the array, else the row's elements alone.
-    __device__ __forceinline__ void copy_word(uint4* dst, uintptr_t at, uintptr_t from, uintptr_t to) const
+    // *dst: whole if it lies inside the array (as it does unless `ends`), else the
+    // row's elements alone.
+    __device__ __forceinline__ void copy_word(uint4* dst, uintptr_t at, uintptr_t from, uintptr_t to, bool ends) const
     {
-        if (at >= lo && at + 16 <= hi) {
+        if (!ends || (at >= lo && at + 16 <= hi)) {
             cp_async16(dst, reinterpret_cast<const void*>(at));
             return;
         }
@@ -270,9 +276,9 @@ struct RowSource {
 
     // The same if the word holds any of the row's elements (one that does not
     // may lie in memory that is not there).
-    __device__ __forceinline__ void copy_if_any(uint4* dst, uintptr_t at, uintptr_t from, uintptr_t to) const
+    __device__ __forceinline__ void copy_if_any(uint4* dst, uintptr_t at, uintptr_t from, uintptr_t to, bool ends) const
     {
-        if (at + 16 > from && at < to) copy_word(dst, at, from, to);
+        if (at + 16 > from && at < to) copy_word(dst, at, from, to, ends);
     }
 };
 
@@ -438,6 +444,9 @@ __global__ void __launch_bounds__(512, MINB)
     // columns of a result row's first word that belong to the row before
     const int first = by_words(MODE) ? static_cast<int>((reinterpret_cast<uintptr_t>(static_cast<const T*>(a.out) + r0 * a.out_stride) & 15u) / sizeof(T)) : 0;
     const int here = by_words(MODE) ? (first + a.cols + V - 1) / V : a.cols / V;   // words of a row
+    // the i-th chunk of this thread, and its first column
+    auto chunk = [&](int i) { return !by_turns(MODE) ? t + i * width : i == 0 && t == 0 ? here - 1 : t + i * width - 1; };
+    auto column = [&](int i) { return chunk(i) * V - first; };
     const float inv_c = 1.0f / static_cast<float>(a.cols);
     for (int i = threadIdx.x; i < 2 * 8 * kMaxWarps * R; i += blockDim.x) (&red[0][0][0])[i] = 0.0f;
     __syncthreads();
@@ -446,8 +455,8 @@ __global__ void __launch_bounds__(512, MINB)
     f32x2 gain[NCH][V / 2], bias[NCH][V / 2];
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-        weights_at<V>(a.gain, a.w_dtype, (t + i * width) * V - first, a.cols, 1.0f, gain[i]);
-        weights_at<V>(a.bias, a.w_dtype, (t + i * width) * V - first, a.cols, 0.0f, bias[i]);
+        weights_at<V>(a.gain, a.w_dtype, t + i * width < here ? column(i) : a.cols, a.cols, 1.0f, gain[i]);
+        weights_at<V>(a.bias, a.w_dtype, t + i * width < here ? column(i) : a.cols, a.cols, 0.0f, bias[i]);
     }
     const RowSource<DT> x(a.x, a.x_stride, a.rows, a.cols);
     // [DEPTH][R][NCH][threads]; kMixed: a group's [DEPTH][R][words]
@@ -463,7 +472,10 @@ __global__ void __launch_bounds__(512, MINB)
     auto fetch = [&]() {
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            if (rf + k * walk.apart >= a.rows) break;
+            const long long r = rf + k * walk.apart;
+            if (r >= a.rows) break;
+            // only these rows' words may reach past the array
+            const bool ends = MODE == kMixed || a.cols < V || r == 0 || r == a.rows - 1;
             if (MODE != kMixed) {
                 const T* q = xf + k * walk.apart * x.stride;
 #pragma unroll
@@ -471,19 +483,19 @@ __global__ void __launch_bounds__(512, MINB)
                     if (t + i * width < here) {
                         uint4* p = into + (k * NCH + i) * blockDim.x;
                         if (MODE == kAligned)
-                            cp_async16(p, q + (t + i * width) * V);
+                            cp_async16(p, q + chunk(i) * V);
                         else if (MODE == kFours)
-                            x.copy_fours(p, q, (t + i * width) * V - first, a.cols);
+                            x.copy_fours(p, q, column(i), a.cols);
                         else
-                            x.copy_word(p, reinterpret_cast<uintptr_t>(q - first + (t + i * width) * V), reinterpret_cast<uintptr_t>(q), reinterpret_cast<uintptr_t>(q + a.cols));
+                            x.copy_word(p, reinterpret_cast<uintptr_t>(q + column(i)), reinterpret_cast<uintptr_t>(q), reinterpret_cast<uintptr_t>(q + a.cols), ends);
                     }
             } else {
                 const uintptr_t row = reinterpret_cast<uintptr_t>(xf + k * walk.apart * x.stride), to = row + static_cast<uintptr_t>(a.cols) * sizeof(T);
                 const uintptr_t at = row - first * sizeof(T) - x_off;
 #pragma unroll
                 for (int i = 0; i < NCH; ++i)
-                    if (t + i * width < here) x.copy_if_any(into + k * words + t + i * width, at + 16u * (t + i * width), row, to);
-                if (t == 0) x.copy_if_any(into + k * words + here, at + 16u * here, row, to);
+                    if (t + i * width < here) x.copy_if_any(into + k * words + chunk(i), at + 16u * chunk(i), row, to, ends);
+                if (t == 0) x.copy_if_any(into + k * words + here, at + 16u * here, row, to, ends);
             }
         }
         cp_async_commit();
@@ -505,12 +517,12 @@ __global__ void __launch_bounds__(512, MINB)
                 // (rows past the last: whatever lies there, and no result)
                 if (MODE != kMixed) {
                     w[k][i] = from[(k * NCH + i) * blockDim.x];
-                    if (by_words(MODE)) w[k][i] = masked<DT>(w[k][i], (t + i * width) * V - first, a.cols);
+                    if (by_words(MODE)) w[k][i] = masked<DT>(w[k][i], column(i), a.cols);
                 } else {
                     w[k][i] = make_uint4(0, 0, 0, 0);
                     if (t + i * width >= here || r0 + k * walk.apart >= a.rows) continue;
-                    const uint4* p = from + k * words + t + i * width;
-                    w[k][i] = masked<DT>(shifted(p[0], p[1], x_off), (t + i * width) * V - first, a.cols);
+                    const uint4* p = from + k * words + chunk(i);
+                    w[k][i] = masked<DT>(shifted(p[0], p[1], x_off), column(i), a.cols);
                 }
             }
         fetch();
@@ -535,9 +547,10 @@ __global__ void __launch_bounds__(512, MINB)
             f32x2 sum = 0;
 #pragma unroll
             for (int i = 0; i < NCH; ++i) {
-                const int c = (t + i * width) * V - first;
+                const int c = column(i);
+                if (t + i * width >= here) break;
                 forget(w[k][i]);
-                if (c >= 0 && c + V <= a.cols) {
+                if (MODE == kAligned || (c >= 0 && c + V <= a.cols)) {
                     f32x2 f[V / 2];
                     widen<DT>(w[k][i], f);
 #pragma unroll
@@ -545,7 +558,7 @@ __global__ void __launch_bounds__(512, MINB)
                         f[e] = sub2(f[e], m);
                         sum = fma2(f[e], f[e], sum);
                     }
-                } else if (MODE != kAligned && c < a.cols) {
+                } else {
                     float f[V], part = 0.0f;
                     widen<DT>(w[k][i], f);
 #pragma unroll
@@ -567,8 +580,8 @@ __global__ void __launch_bounds__(512, MINB)
             const f32x2 rs = pack2(rstd[k], rstd[k]), nm = pack2(-mean[k] * rstd[k], -mean[k] * rstd[k]);
 #pragma unroll
             for (int i = 0; i < NCH; ++i) {
-                const int c = (t + i * width) * V - first;
-                if (c >= a.cols) break;
+                const int c = column(i);
+                if (t + i * width >= here) break;
                 f32x2 f[V / 2];
                 float o[V];
                 forget(w[k][i]);
@@ -609,6 +622,9 @@ __global__ void __launch_bounds__(512, MINB)
     // columns of a result row's first word that belong to the row before
     const int first = by_words(MODE) ? static_cast<int>((reinterpret_cast<uintptr_t>(static_cast<const T*>(a.out) + r0 * a.out_stride) & 15u) / sizeof(T)) : 0;
     const int here = by_words(MODE) ? (first + a.cols + V - 1) / V : a.cols / V;   // words of a row
+    // the i-th chunk of this thread, and its first column
+    auto chunk = [&](int i) { return !by_turns(MODE) ? t + i * width : i == 0 && t == 0 ? here - 1 : t + i * width - 1; };
+    auto column = [&](int i) { return chunk(i) * V - first; };
     const float inv_c = 1.0f / static_cast<float>(a.cols);
     for (int i = threadIdx.x; i < 2 * 8 * kMaxWarps * 2 * R; i += blockDim.x) (&red[0][0][0])[i] = 0.0f;
     __syncthreads();
@@ -617,7 +633,7 @@ __global__ void __launch_bounds__(512, MINB)
     f32x2 gain[NCH][V / 2], dg2[NCH][V / 2], db2[NCH][V / 2];
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-        weights_at<V>(a.gain, a.w_dtype, (t + i * width) * V - first, a.cols, 1.0f, gain[i]);
+        weights_at<V>(a.gain, a.w_dtype, t + i * width < here ? column(i) : a.cols, a.cols, 1.0f, gain[i]);
 #pragma unroll
         for (int e = 0; e < V / 2; ++e) dg2[i][e] = db2[i][e] = 0;
     }
@@ -637,6 +653,7 @@ __global__ void __launch_bounds__(512, MINB)
         for (int k = 0; k < R; ++k) {
             const long long r = rf + k * walk.apart;
             if (r >= a.rows) break;
+            const bool ends = MODE == kMixed || a.cols < V || r == 0 || r == a.rows - 1;
             if (MODE != kMixed) {
                 const T* q = x.base + r * x.stride;
                 const T* d = dy.base + r * dy.stride;
@@ -644,16 +661,16 @@ __global__ void __launch_bounds__(512, MINB)
                 for (int i = 0; i < NCH; ++i)
                     if (t + i * width < here) {
                         uint4* p = ring + into + (k * 2 * NCH + i) * blockDim.x;
-                        const int at = (t + i * width) * V;
+                        const int c = column(i);
                         if (MODE == kAligned) {
-                            cp_async16(p, q + at);
-                            cp_async16(p + NCH * blockDim.x, d + at);
+                            cp_async16(p, q + c);
+                            cp_async16(p + NCH * blockDim.x, d + c);
                         } else if (MODE == kFours) {
-                            x.copy_fours(p, q, at - first, a.cols);
-                            dy.copy_fours(p + NCH * blockDim.x, d, at - first, a.cols);
+                            x.copy_fours(p, q, c, a.cols);
+                            dy.copy_fours(p + NCH * blockDim.x, d, c, a.cols);
                         } else {
-                            x.copy_word(p, reinterpret_cast<uintptr_t>(q - first + at), reinterpret_cast<uintptr_t>(q), reinterpret_cast<uintptr_t>(q + a.cols));
-                            dy.copy_word(p + NCH * blockDim.x, reinterpret_cast<uintptr_t>(d - first + at), reinterpret_cast<uintptr_t>(d), reinterpret_cast<uintptr_t>(d + a.cols));
+                            x.copy_word(p, reinterpret_cast<uintptr_t>(q + c), reinterpret_cast<uintptr_t>(q), reinterpret_cast<uintptr_t>(q + a.cols), ends);
+                            dy.copy_word(p + NCH * blockDim.x, reinterpret_cast<uintptr_t>(d + c), reinterpret_cast<uintptr_t>(d), reinterpret_cast<uintptr_t>(d + a.cols), ends);
                         }
                     }
             } else {
@@ -663,12 +680,12 @@ __global__ void __launch_bounds__(512, MINB)
 #pragma unroll
                 for (int i = 0; i < NCH; ++i)
                     if (t + i * width < here) {
-                        x.copy_if_any(p + t + i * width, xa + 16u * (t + i * width), xr, xr + n);
-                        dy.copy_if_any(p + words + t + i * width, da + 16u * (t + i * width), dr, dr + n);
+                        x.copy_if_any(p + chunk(i), xa + 16u * chunk(i), xr, xr + n, ends);
+                        dy.copy_if_any(p + words + chunk(i), da + 16u * chunk(i), dr, dr + n, ends);
                     }
                 if (t == 0) {
-                    x.copy_if_any(p + here, xa + 16u * here, xr, xr + n);
-                    dy.copy_if_any(p + words + here, da + 16u * here, dr, dr + n);
+                    x.copy_if_any(p + here, xa + 16u * here, xr, xr + n, ends);
+                    dy.copy_if_any(p + words + here, da + 16u * here, dr, dr + n, ends);
                 }
             }
         }
@@ -701,13 +718,13 @@ __global__ void __launch_bounds__(512, MINB)
                     wx[k][i] = p[0];
                     wd[k][i] = p[NCH * blockDim.x];
                     if (by_words(MODE)) {
-                        const int c = (t + i * width) * V - first;
+                        const int c = column(i);
                         wx[k][i] = masked<DT>(wx[k][i], c, a.cols);
                         wd[k][i] = masked<DT>(wd[k][i], c, a.cols);
                     }
                 } else {
-                    const uint4* p = ring + from + k * 2 * words + t + i * width;
-                    const int c = (t + i * width) * V - first;
+                    const uint4* p = ring + from + k * 2 * words + chunk(i);
+                    const int c = column(i);
                     wx[k][i] = masked<DT>(shifted(p[0], p[1], x_off), c, a.cols);
                     wd[k][i] = masked<DT>(shifted(p[words], p[words + 1], d_off), c, a.cols);
                 }
@@ -755,8 +772,8 @@ __global__ void __launch_bounds__(512, MINB)
             const f32x2 rs = pack2(rstd[k], rstd[k]), n1 = pack2(q1, q1), n2 = pack2(q2, q2);
 #pragma unroll
             for (int i = 0; i < NCH; ++i) {
-                const int c = (t + i * width) * V - first;
-                if (c >= a.cols) break;
+                const int c = column(i);
+                if (t + i * width >= here) break;
                 f32x2 xv[V / 2], dv[V / 2];
                 float o[V];
                 forget(wx[k][i]);
@@ -818,8 +835,8 @@ __global__ void __launch_bounds__(512, MINB)
         // chunk by chunk: column c lies at c + first (the sums past a row are zeros)
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
-            const int c = (t + i * width) * V;
             if (t + i * width >= here) break;
+            const int c = chunk(i) * V;
 #pragma unroll
             for (int e = 0; e < V; e += 4) {
                 *reinterpret_cast<float4*>(p + c + e) = make_float4(dg[i][e], dg[i][e + 1], dg[i][e + 2], dg[i][e + 3]);
