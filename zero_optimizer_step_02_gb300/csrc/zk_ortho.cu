@@ -32,7 +32,7 @@
 // MMAs: a meeting of the CTAs (1 to 2 us), the first tiles' way from L2 (1 us)
 // and the last tiles' results (2 to 6 us); a 256 x 256 matrix, whose products
 // take 1 us each, pays 6.4 us a product.  Hence one launch for the whole
-// iteration (a launch for each product: 12 x 768 x 768 390 us, now 227), the
+// iteration (a launch for each product: 12 x 768 x 768 390 us, now 221), the
 // depth of a tile split among CTAs where tiles are few, and 32 x 32 pieces of
 // results that go out in whole 64-byte lines.
 #include <climits>
@@ -642,8 +642,8 @@ __device__ __noinline__ void first_operand(const NsKernelArgs& a, int b, int cta
 // works out the next phase meanwhile (0.4 us that would stand between two
 // products).
 //
-// What the clocks go to beside the MMAs, in a phase: 1.0 to 1.3k for the fence
-// and the block's barrier, 2 to 4k for the meeting, 2.2k until the first stage
+// What the clocks go to beside the MMAs, in a phase: about 1k for the block's
+// barrier and the release, 2 to 4k for the meeting, 2.2k until the first stage
 // is there, 3.4 to 6.1k for the results of a 128 x 128 tile of a CTA, 6.8 to
 // 13k for 128 x 256 (the upper figures beside the next tile's MMAs), 13k for an
 // exchange of partial sums.  The results are bound by latency: a 32 x 32 piece

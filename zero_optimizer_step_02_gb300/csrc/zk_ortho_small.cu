@@ -4,12 +4,12 @@
 // Every operand stays in shared memory for the whole iteration and every sum
 // in tensor memory, so a step costs its MMAs, two tensor-memory reads and
 // three block barriers, not three trips through L2.  One CTA a matrix, one
-// launch a call.  96 x 160 takes 40 us (the general form 100), 140 matrices of
-// 128 x 256 64 us side by side.  Its floor is nothing (under 0.1 us of work at
+// launch a call.  96 x 160 takes 37 us (the general form 100), 140 matrices of
+// 128 x 256 58 us side by side.  Its floor is nothing (under 0.1 us of work at
 // the whole chip's rate); what it takes is the latency of fifteen dependent
-// products: about 2.3 us each for the barrier, a short chain of MMAs, the sums
+// products: about 2.4 us each for the barrier, a short chain of MMAs, the sums
 // out of tensor memory and the pairs back into shared memory (by counters: issue
-// slots 41% busy, tensor cores 34%, waits for tensor memory on top of the
+// slots 39% busy, tensor cores 34%, waits for tensor memory on top of the
 // stalls).  Larger matrices do not fit: both planes of x, twice 128 x 256, and
 // of one square matrix are 192 KB.
 //
