@@ -1060,7 +1060,8 @@ int sms_of_device()
     return n;
 }
 
-constexpr size_t kRowSmem = 220 * 1024;   // of the 227 KB a CTA may have
+constexpr size_t kSmemOptin = 227 * 1024;   // that a CTA may have
+constexpr size_t kRowSmem = 220 * 1024;     // of it, for rows and partial sums
 
 // how a launch cuts its rows up
 struct RowShape {
@@ -1109,7 +1110,10 @@ template <typename K>
 cudaError_t launch_rows(K kernel, const LnArgs& a, const RowShape& s, size_t smem, cudaStream_t st)
 {
     if (smem > 40 * 1024) {   // 48 KB without asking, the static arrays included
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        // The limit belongs to the kernel, not to the call: the same for every
+        // call, so that one on another host thread cannot lower it in between.
+        static_assert(kRowSmem <= kSmemOptin - 4 * 1024, "and the static arrays");
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kRowSmem));
         if (e != cudaSuccess) return e;
     }
     return launch_after(kernel, dim3(static_cast<unsigned>(s.grid)), dim3(s.threads), smem, st, a, s.width, s.groups);
