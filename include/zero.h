@@ -541,6 +541,9 @@ ZERO_API zero_status zero_layernorm_backward(const zero_layernorm* desc, const v
  * picks 1 where the result is rounded to bf16 and 3 elsewhere (a Muon step,
  * whose result is added to fp32 weights, takes 3).  Matrices whose short side
  * is under 256 always take 3.
+ * |g|_F is taken over the whole range of the input's type.  The entries of x
+ * are kept to 2^-36, so a matrix whose norm is a millionth of eps and less
+ * (it comes out as good as zero) loses digits.
  * A matrix of zeros gives zeros; one with a NaN or an infinity gives NaN.
  * The same inputs give the same bits on the same device.
  *

@@ -87,61 +87,78 @@ __device__ __forceinline__ void load_row8(const void* in, int dtype, bool vec, l
     }
 }
 
-// A sum of squares in fp32, compensated; `big` the same of the values times
-// 2^-70, for matrices whose squares pass fp32's range.  (fp64 would cost more
-// than all else here: it runs at a small fraction of fp32's rate.)
+// A sum of squares in fp32, whatever the values' size: eight squares at a time
+// go to one of three sums, as they are (compensated), times 2^-180 if they pass
+// 2^90, times 2^180 if they are under 2^-90.  No sum over a matrix (2^28 eights
+// at most) passes 2^118 then, and no square that counts falls under fp32's
+// normal range: 2^-149 squared is 2^-118 in `tiny`, and what a square loses to
+// subnormals in `sum` is under 2^-50 of it.  NaN and infinity go to `big`.
+// (fp64 would cost more than all else here: it runs at a small fraction of
+// fp32's rate.)
+constexpr float kTo90 = 1.2379400392853803e27f;   // 2^90
 struct SquareSum {
-    float sum = 0.0f, lost = 0.0f, big = 0.0f;
+    float sum = 0.0f, lost = 0.0f, big = 0.0f, tiny = 0.0f;
     __device__ __forceinline__ void add8(const float (&v)[8])
     {
         float q = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float w = v[e] * 8.470329472543003e-22f;   // 2^-70
-            q = fmaf(v[e], v[e], q);
-            big = fmaf(w, w, big);
+        for (int e = 0; e < 8; ++e) q = fmaf(v[e], v[e], q);
+        if (q >= 1.0f / kTo90 && q <= kTo90) {
+            const float a = fmaxf(sum, q), b = fminf(sum, q), t = a + b;
+            lost += b - (t - a);
+            sum = t;
+            return;
         }
-        const float a = fmaxf(sum, q), b = fminf(sum, q), t = a + b;   // NaN: kept by `big`
-        lost += b - (t - a);
-        sum = t;
-    }
-    __device__ __forceinline__ float2 value() const { return make_float2(sum + lost, big); }
-};
-
-// sums over a block, in thread 0; red: a float2 for each warp
-__device__ __forceinline__ float2 block_sum2(float2 v, float2* red)
-{
+        const bool small = q < kTo90;
+        const float f = small ? kTo90 : 1.0f / kTo90;
+        q = 0.0f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, o);
-        v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, o);
+        for (int e = 0; e < 8; ++e) q = fmaf(v[e] * f, v[e] * f, q);
+        if (small)
+            tiny += q;
+        else
+            big += q;
     }
+    // {sum, big, tiny, 0}
+    __device__ __forceinline__ float4 value() const { return make_float4(sum + lost, big, tiny, 0.0f); }
+};
+__device__ __forceinline__ void add_sums(float4& a, const float4& b) { a.x += b.x, a.y += b.y, a.z += b.z; }
+
+// sums over a block, in thread 0; red: a float4 for each warp
+__device__ __forceinline__ float4 block_sums(float4 v, float4* red)
+{
+    const auto warp_sums = [](float4& x) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            add_sums(x, make_float4(__shfl_xor_sync(0xFFFFFFFFu, x.x, o), __shfl_xor_sync(0xFFFFFFFFu, x.y, o),
+                                    __shfl_xor_sync(0xFFFFFFFFu, x.z, o), 0.0f));
+    };
+    warp_sums(v);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
     if (threadIdx.x < 32) {
-        v = threadIdx.x < (blockDim.x >> 5) ? red[threadIdx.x] : make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, o);
-            v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, o);
-        }
+        v = threadIdx.x < (blockDim.x >> 5) ? red[threadIdx.x] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        warp_sums(v);
     }
     return v;
 }
 
-// kScale / (|g| + eps) from the two sums of squares (thread 0's), in every
-// thread; a NaN in g makes it NaN
-__device__ __forceinline__ float block_scale(float2 sums, float eps, float* shared)
+// kScale / (|g| + eps) from the sums of squares (thread 0's), in every thread; a
+// NaN or an infinity in g makes it NaN.  eps >= 1e-30 keeps it finite.
+__device__ __forceinline__ float block_scale(float4 sums, float eps, float* shared)
 {
     if (threadIdx.x == 0) {
-        const float s = sums.x;
+        constexpr float kDown = 1.0f / kTo90;
         float f;
-        if (sums.y != sums.y)
-            f = sums.y;
-        else if (is_finite_f32(s))
-            f = kScale / (sqrtf(s) + eps);
-        else   // sqrt(big) * 2^70, and eps, which is nothing beside it
-            f = is_finite_f32(sums.y) ? kScale * 8.470329472543003e-22f / sqrtf(sums.y) : 0.0f;
+        if (sums.y != 0.0f) {
+            // all of it times 2^-90; what is in `tiny` is nothing beside it
+            const float s = sums.y + sums.x * kDown * kDown;
+            f = is_finite_f32(s) ? kScale * kDown / (sqrtf(s) + eps * kDown) : s - s;
+        } else if (sums.x != 0.0f) {
+            f = kScale / (sqrtf(sums.x + sums.z * kDown * kDown) + eps);
+        } else {
+            f = kScale / (sqrtf(sums.z) * kDown + eps);
+        }
         *shared = f;
     }
     __syncthreads();
@@ -156,7 +173,7 @@ struct MuonArgs {
     float* u;
     long long stride, u_stride;
     uint32_t elems;              // of one matrix
-    float2* parts;
+    float4* parts;
     unsigned* counters;
     int n_counters;
 };

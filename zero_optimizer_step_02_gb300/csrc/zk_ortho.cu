@@ -81,7 +81,7 @@ struct NsKernelArgs {
     int in_dtype, in_vec, chunks;
     long long in_ld, in_stride;
     float eps;
-    const float2* parts;         // [batch][parts_n] sums of squares
+    const float4* parts;         // [batch][parts_n] sums of squares
     int parts_n;
     // the result
     int res;                     // RES_OUT or RES_MUON
@@ -428,7 +428,7 @@ struct PrepArgs {
     int dtype, vec;
     long long ld, stride;
     int rows, cols, chunks;      // chunks: groups of eight columns in a row
-    float2* parts;               // [batch][gridDim.x] sums of squares
+    float4* parts;               // [batch][gridDim.x] sums of squares
     unsigned* counters;          // cleared for the products' kernel
     int n_counters;
 };
@@ -445,7 +445,7 @@ __device__ __forceinline__ void clear_counters(unsigned* c, int n)
 // (43 and 9 us).
 __global__ void __launch_bounds__(256) ns_sqnorm(const __grid_constant__ PrepArgs a)
 {
-    __shared__ float2 red[8];
+    __shared__ float4 red[8];
     pdl_wait();
     clear_counters(a.counters, a.n_counters);
     const uint32_t total = static_cast<uint32_t>(a.rows) * a.chunks;
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(256) ns_sqnorm(const __grid_constant__ PrepArg
         load_row8(a.in, a.dtype, a.vec, base + row * a.ld, a.cols, i - row * a.chunks, v);
         s.add8(v);
     }
-    const float2 sums = block_sum2(s.value(), red);
+    const float4 sums = block_sums(s.value(), red);
     if (threadIdx.x == 0) a.parts[blockIdx.y * static_cast<long long>(gridDim.x) + blockIdx.x] = sums;
 }
 
@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(256) ns_sqnorm(const __grid_constant__ PrepArg
 // TB/s, 1.8% of the step); 768 x 2304 over eight ranks, 50 MB, in 16 us.
 __global__ void __launch_bounds__(256) muon_direction(const __grid_constant__ MuonArgs a)
 {
-    __shared__ float2 red[8];
+    __shared__ float4 red[8];
     pdl_wait();
     clear_counters(a.counters, a.n_counters);
     SquareSum s;
@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(256) muon_direction(const __grid_constant__ Mu
         muon_direction8(a, blockIdx.y, i, u);
         s.add8(u);
     }
-    const float2 sums = block_sum2(s.value(), red);
+    const float4 sums = block_sums(s.value(), red);
     if (threadIdx.x == 0) a.parts[blockIdx.y * static_cast<long long>(gridDim.x) + blockIdx.x] = sums;
 }
 
@@ -595,15 +595,11 @@ __device__ __forceinline__ void set_phase(Phase& ph, const NsKernelArgs& a, int 
 
 // x_0 = g / (|g| + eps) of matrix b, scaled, as a pair: this CTA's part.  Once
 // a matrix, so kept out of the phases' registers.
-__device__ __noinline__ void first_operand(const NsKernelArgs& a, int b, int cta, float2* red, float* shared_scale)
+__device__ __noinline__ void first_operand(const NsKernelArgs& a, int b, int cta, float4* red, float* shared_scale)
 {
-    float2 q = make_float2(0.0f, 0.0f);
-    for (int i = threadIdx.x; i < a.parts_n; i += kThreads) {
-        const float2 p = a.parts[static_cast<long long>(b) * a.parts_n + i];
-        q.x += p.x;
-        q.y += p.y;
-    }
-    const float f = block_scale(block_sum2(q, red), a.eps, shared_scale);
+    float4 q = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i = threadIdx.x; i < a.parts_n; i += kThreads) add_sums(q, a.parts[static_cast<long long>(b) * a.parts_n + i]);
+    const float f = block_scale(block_sums(q, red), a.eps, shared_scale);
     const uint32_t chunks = a.chunks, total = static_cast<uint32_t>(a.rows) * chunks, stride = a.ctas * kThreads;
     const void* in = a.in;
     const int dtype = a.in_dtype, cols = a.cols;
@@ -660,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__
     __shared__ volatile int abort_flag;
     __shared__ Phase plan[2];
     __shared__ int stop_flag;
-    __shared__ float2 red[kThreads / 32];
+    __shared__ float4 red[kThreads / 32];
     __shared__ float shared_scale;
     unsigned char* ring = smem_raw + (1024 - (smem_u32(smem_raw) & 1023u)) % 1024;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1051,6 +1047,15 @@ struct Layout {
 
 constexpr int kMaxSms = 160;      // GB300 has 152
 
+// CTAs that take a matrix's norm: `want` of them, but no more than eight an SM
+// over the batch
+int parts_of(int batch, long long want, int sms)
+{
+    const long long most = (8LL * sms + batch - 1) / batch;
+    if (want > most) want = most;
+    return static_cast<int>(want < kMaxNsParts ? want : kMaxNsParts);
+}
+
 Layout layout_of(int rows, int cols, int batch, int products, bool muon)
 {
     Layout l;
@@ -1062,7 +1067,7 @@ Layout layout_of(int rows, int cols, int batch, int products, bool muon)
     l.counters = at;
     at += up256(static_cast<size_t>(kMaxSms) * (kBarStride + 1) * sizeof(unsigned));
     l.parts = at;
-    at += up256(static_cast<size_t>(batch) * kMaxNsParts * sizeof(float2));
+    at += up256(static_cast<size_t>(batch) * parts_of(batch, kMaxNsParts, kMaxSms) * sizeof(float4));
     l.partial = at;
     at += static_cast<size_t>(kMaxSms) * kBM * 256 * sizeof(float);
     l.u = at;
@@ -1186,7 +1191,7 @@ cudaError_t launch_ns(const NsArgs& a, cudaStream_t st)
     const Layout l = layout_of(a.rows, a.cols, a.batch, a.products, muon);
     char* ws = static_cast<char*>(a.ws);
     unsigned* counters = reinterpret_cast<unsigned*>(ws + l.counters);
-    float2* parts = reinterpret_cast<float2*>(ws + l.parts);
+    float4* parts = reinterpret_cast<float4*>(ws + l.parts);
     MuonArgs mu;
     if (muon) {
         std::memset(&mu, 0, sizeof(mu));
@@ -1239,11 +1244,8 @@ cudaError_t launch_ns(const NsArgs& a, cudaStream_t st)
     // the norm: CTAs a matrix, four chunks a thread (Muon, with more to load for
     // each: one; 768 x 768 over 16 ranks, the whole step, 218 -> 203 us), eight CTAs an SM over the batch
     const long long chunks = static_cast<long long>(a.rows) * k.chunks;
-    long long per = (chunks + (muon ? 255 : 1023)) / (muon ? 256 : 1024), most = (8LL * sms + a.batch - 1) / a.batch;
-    if (per > most) per = most;
-    if (per > kMaxNsParts) per = kMaxNsParts;
-    k.parts_n = static_cast<int>(per);
-    const dim3 grid(static_cast<unsigned>(per), a.batch);
+    k.parts_n = parts_of(a.batch, (chunks + (muon ? 255 : 1023)) / (muon ? 256 : 1024), sms);
+    const dim3 grid(static_cast<unsigned>(k.parts_n), a.batch);
     if (muon) {
         k.in = mu.u;
         k.in_dtype = ZERO_FP32;

@@ -120,7 +120,7 @@ __device__ __forceinline__ void ns_small_body(const SmallNsArgs& a, const MuonAr
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint64_t bar, drain;
     __shared__ uint32_t tmem_base;
-    __shared__ float2 red[kSmallThreads / 32];
+    __shared__ float4 red[kSmallThreads / 32];
     __shared__ float shared_scale;
     unsigned char* x = smem_raw + (1024 - (smem_u32(smem_raw) & 1023u)) % 1024;
     const int x_lo = a.panels * kPanelBytes, g_lo = kSquarePanels * kPanelBytes;
@@ -154,7 +154,7 @@ __device__ __forceinline__ void ns_small_body(const SmallNsArgs& a, const MuonAr
             q.add8(v);
         }
     }
-    const float f = block_scale(block_sum2(q.value(), red), a.eps, &shared_scale);
+    const float f = block_scale(block_sums(q.value(), red), a.eps, &shared_scale);
     for (int i = t; i < total; i += kSmallThreads) {
         const int row = i / chunks, col = (i - row * chunks) * 8;
         float v[8];
