@@ -3,10 +3,12 @@ threads, rows of huge values, widths above 8192 with many rows."""
 import ctypes
 import threading
 
+import numpy as np
 import pytest
 import torch
 
 import zero_optimizer_step_02_gb300 as z
+from test_gpu_layernorm import BF16, FP32, TORCH, U32, UNIT, Unlike, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +48,59 @@ def test_two_host_threads_each_with_its_own_stream():
     for t in threads:
         t.join()
     assert errors == []
+
+
+# how the arrays lie: on whole words, alike inside them, differently
+LIES = [((0, 0),) * 4, ((3, 1),) * 4, ((0, 0), (3, 1), (1, 2), (5, 0))]
+
+
+@pytest.mark.parametrize("lies", LIES)
+@pytest.mark.parametrize("cols,value,eps", [(8, 2.0 ** 120, 1e-5), (16, 2.0 ** 120, 1e-5), (64, 2.0 ** 120, 1e-5),
+                                            (128, 2.0 ** 120, 1e-5), (256, 2.0 ** 110, 1e-30), (1024, 2.0 ** 110, 1e-30),
+                                            (8192, 2.0 ** 110, 1e-30), (16384, 2.0 ** 110, 1e-30)])
+@pytest.mark.parametrize("dt", [BF16, FP32])
+def test_constant_rows_of_huge_values_give_the_bias(cols, value, eps, dt, lies):
+    # mean * rstd is past fp32's range, the mean of 2^n equal values is exact and xhat is 0
+    rows = 5
+    c = Unlike(rows, cols, dt, lies)
+    c.desc.eps = eps
+    c.x[2] = value
+    c.forward()
+    assert torch.equal(c.y[2], c.bias.to(TORCH[dt]))
+    assert bool(torch.isfinite(c.y.float()).all())
+    c.backward()
+    dy, h = f64(c.dy), f64(c.dy)[2] * f64(c.gain)
+    rstd = f64(c.rstd)[2]
+    want = rstd * (h - h.mean())
+    # a sum of `cols` terms, a product, a difference and two roundings of each
+    e = rstd * U32 * ((16 + cols / 32 + 2) * np.abs(h).mean() + 4 * (np.abs(h) + np.abs(h).mean()))
+    assert np.all(np.abs(f64(c.dx)[2] - want) <= UNIT[dt] * (np.abs(want) + e) + e)
+    assert bool(torch.isfinite(c.dx.float()).all()) and bool(torch.isfinite(c.dgain).all())
+    want = dy.sum(0)
+    assert np.all(np.abs(f64(c.dbias) - want) <= (16 + rows) * U32 * np.abs(dy).sum(0))
+    c.guards_intact()
+
+
+@pytest.mark.parametrize("lies", LIES)
+@pytest.mark.parametrize("cols", [24, 97, 768, 1601, 4096, 8192, 16384])
+def test_fp32_rows_with_an_offset_are_centred_before_they_are_scaled(cols, lies):
+    # against the formula with the kernel's own mean and rstd: one rounding each
+    # for x - mean, the two products and the sum, none of the size of mean * rstd
+    c = Unlike(6, cols, FP32, lies, offset=3000.0)
+    c.forward()
+    xhat = (f64(c.x) - f64(c.mean)[:, None]) * f64(c.rstd)[:, None]
+    g, b = c.weights64()
+    e = 4 * U32 * np.abs(xhat * g) + 2 * U32 * np.abs(b)
+    assert np.all(np.abs(f64(c.y) - (xhat * g + b)) <= e)
+    c.backward()
+    c.check_backward()
+    # dx likewise: the row's two means from the same xhat
+    h = f64(c.dy) * g
+    m1, m2 = h.mean(1, keepdims=True), (h * xhat).mean(1, keepdims=True)
+    rstd = f64(c.rstd)[:, None]
+    want = rstd * (h - m1 - xhat * m2)
+    depth = 16 + cols / 32
+    e = rstd * U32 * ((depth + 2) * np.abs(h).mean(1, keepdims=True) + (depth + 6) * np.abs(xhat) * np.abs(h * xhat).mean(1, keepdims=True)
+                      + 4 * (np.abs(h) + np.abs(m1) + np.abs(xhat * m2)))
+    assert np.all(np.abs(f64(c.dx) - want) <= U32 * np.abs(want) + e)
+    c.guards_intact()

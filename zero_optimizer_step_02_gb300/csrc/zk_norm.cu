@@ -8,9 +8,10 @@
 //
 // Every sum is fp32; the results are rounded once, to the tensor's type.  The
 // sum of squares is taken about the mean in a second pass over the row (in
-// registers), so an offset in x costs the variance no digits; xhat is x * rstd -
-// mean * rstd in one fused operation, whose rounding of mean * rstd is as large
-// as that of the mean itself.
+// registers), so an offset in x costs the variance no digits.  xhat is
+// (x - mean) * rstd for fp32; for 16-bit x, whose own digits end long before, it
+// is x * rstd - mean * rstd in one fused operation (the difference costs 16-bit
+// rows up to 8% forward, bound by issue as they are, and fp32 rows nothing).
 //
 // Bound: memory.  Forward reads x and writes y, backward reads x and dy and
 // writes dx; at 6783 GB/s (a copy's rate) 8192 x 4096 bf16 cannot take less than
@@ -354,6 +355,30 @@ __device__ __forceinline__ void weights_at(const void* w, int dt, int c, int col
     for (int e = 0; e < V / 2; ++e) v[e] = pack2(f[2 * e], f[2 * e + 1]);
 }
 
+// xhat of a row with this mean and 1 / std.  |xhat| <= sqrt(cols), and an x that
+// is not the mean differs from it by 2^-25 of it or more: where |mean| * rstd
+// passes 2^40, every x is the mean and xhat is 0, however large mean * rstd (an
+// overflow would make it NaN).  rstd NaN or infinite: as they come.
+template <int DT>
+struct Centred {
+    f32x2 rs, by;
+    __device__ __forceinline__ Centred(float mean, float rstd)
+    {
+        const float nm = -mean * rstd;
+        const bool flat = fabsf(nm) > 1.099511627776e12f && is_finite_f32(rstd);
+        const float r = flat ? 0.0f : rstd, b = DT == ZERO_FP32 ? mean : flat ? 0.0f : nm;
+        rs = pack2(r, r);
+        by = pack2(b, b);
+    }
+    __device__ __forceinline__ f32x2 xhat(f32x2 x) const
+    {
+        if constexpr (DT == ZERO_FP32)
+            return mul2(sub2(x, by), rs);
+        else
+            return fma2(x, rs, by);
+    }
+};
+
 constexpr int kMaxWarps = 16;   // of a group
 
 // Sums of N values over a group of `warps` warps (LANES < 32: of so many lanes
@@ -576,8 +601,7 @@ __global__ void __launch_bounds__(512, MINB)
             if (r >= a.rows) break;
             rstd[k] = inverse_root(rstd[k] * inv_c + a.eps);
             const uintptr_t y = reinterpret_cast<uintptr_t>(yr + k * walk.apart * a.out_stride);
-            // xhat in one operation: x * rstd - mean * rstd
-            const f32x2 rs = pack2(rstd[k], rstd[k]), nm = pack2(-mean[k] * rstd[k], -mean[k] * rstd[k]);
+            const Centred<DT> row(mean[k], rstd[k]);
 #pragma unroll
             for (int i = 0; i < NCH; ++i) {
                 const int c = column(i);
@@ -587,7 +611,7 @@ __global__ void __launch_bounds__(512, MINB)
                 forget(w[k][i]);
                 widen<DT>(w[k][i], f);
 #pragma unroll
-                for (int e = 0; e < V / 2; ++e) f[e] = fma2(fma2(f[e], rs, nm), gain[i][e], bias[i][e]);
+                for (int e = 0; e < V / 2; ++e) f[e] = fma2(row.xhat(f[e]), gain[i][e], bias[i][e]);
                 unpack(f, o);
                 if (MODE == kAligned)
                     __stcs(reinterpret_cast<uint4*>(y) + t + i * width, narrowed<DT>(o));
@@ -741,7 +765,7 @@ __global__ void __launch_bounds__(512, MINB)
         float sum[2 * R];
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            const f32x2 rs = pack2(rstd[k], rstd[k]), nm = pack2(-mean[k] * rstd[k], -mean[k] * rstd[k]);
+            const Centred<DT> row(mean[k], rstd[k]);
             f32x2 s1 = 0, s2 = 0;
 #pragma unroll
             for (int i = 0; i < NCH; ++i) {
@@ -750,7 +774,7 @@ __global__ void __launch_bounds__(512, MINB)
                 widen<DT>(wd[k][i], dv);
 #pragma unroll
                 for (int e = 0; e < V / 2; ++e) {
-                    const f32x2 xhat = fma2(xv[e], rs, nm), h = mul2(dv[e], gain[i][e]);
+                    const f32x2 xhat = row.xhat(xv[e]), h = mul2(dv[e], gain[i][e]);
                     dg2[i][e] = fma2(dv[e], xhat, dg2[i][e]);
                     db2[i][e] = add2(db2[i][e], dv[e]);
                     s1 = add2(s1, h);
@@ -767,9 +791,9 @@ __global__ void __launch_bounds__(512, MINB)
             const uintptr_t out = reinterpret_cast<uintptr_t>(static_cast<T*>(a.out) + (r0 + k * walk.apart) * a.out_stride);
             // dx = rstd * (dy * gain - s1 - xhat * s2)
             const float s1 = sum[2 * k] * inv_c, s2 = sum[2 * k + 1] * inv_c;
-            // = rstd * (dy * gain + x * n2 + n1)
-            const float q2 = -s2 * rstd[k], q1 = fmaf(-mean[k], q2, -s1);
-            const f32x2 rs = pack2(rstd[k], rstd[k]), n1 = pack2(q1, q1), n2 = pack2(q2, q2);
+            // = rstd * (dy * gain + x * n2 + n1), fp32: (x - mean) * n2 and no mean in n1
+            const float q2 = -s2 * rstd[k], q1 = DT == ZERO_FP32 ? -s1 : fmaf(-mean[k], q2, -s1);
+            const f32x2 rs = pack2(rstd[k], rstd[k]), n1 = pack2(q1, q1), n2 = pack2(q2, q2), m = pack2(mean[k], mean[k]);
 #pragma unroll
             for (int i = 0; i < NCH; ++i) {
                 const int c = column(i);
@@ -782,7 +806,7 @@ __global__ void __launch_bounds__(512, MINB)
                 widen<DT>(wd[k][i], dv);
 #pragma unroll
                 for (int e = 0; e < V / 2; ++e)
-                    xv[e] = mul2(rs, fma2(xv[e], n2, fma2(dv[e], gain[i][e], n1)));
+                    xv[e] = mul2(rs, fma2(DT == ZERO_FP32 ? sub2(xv[e], m) : xv[e], n2, fma2(dv[e], gain[i][e], n1)));
                 unpack(xv, o);
                 if (MODE == kAligned)
                     __stcs(reinterpret_cast<uint4*>(out) + t + i * width, narrowed<DT>(o));
