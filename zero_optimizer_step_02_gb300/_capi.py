@@ -142,7 +142,7 @@ for _name, (_res, _args) in _SIGS.items():
 # ----------------------------------------------------------------- marshalling
 def _addr(x):
     """Device address of a torch tensor, an int, or None (NULL)."""
-    if x is None or type(x) is int:
+    if x is None or isinstance(x, int):
         return x
     return x.data_ptr()
 
