@@ -1,7 +1,9 @@
 """What the binding and the training operators' entry points accept and refuse
 at the edges: no GPU needed, no call here reaches a launch."""
 import enum
+import random
 
+import numpy as np
 import pytest
 
 
@@ -28,3 +30,51 @@ def test_addresses_may_be_any_kind_of_int(z):
     # through an entry point: refused for its alignment, not for its type
     with pytest.raises(z.ZeroError):
         z.zero_scalars_init(Address(0x1234501), stream=Address(0))
+
+
+def fits(z, coefs):
+    return z.zero_orthogonalize_workspace_bytes(z.matrices(32, 64, coefs=coefs)) > 0
+
+
+def largest(coefs, points):
+    """The largest s^2 and |b s^2 + c s^4| that a dense grid of [0, 1] meets."""
+    s, worst = np.linspace(0.0, 1.0, points), 0.0
+    with np.errstate(over="ignore", invalid="ignore"):
+        for a, b, c in coefs:
+            g = s * s
+            p = b * g + c * g * g
+            worst = max(worst, float(np.nanmax(g)), float(np.nanmax(np.abs(p))))
+            s = s * (a + p)
+    return worst
+
+
+# the slopes of the steps multiply: these leave fp16's range between the points
+# of any coarse grid (3.6 and 3.4 at most over 513 points)
+@pytest.mark.parametrize("step,times", [((2.12717, -4.55896, 1.43027), 9), ((2.13721, -4.81709, 1.67575), 8)])
+def test_schedules_that_leave_the_range_between_samples_are_refused(z, step, times):
+    assert largest([step] * times, 513) < 5.0 and largest([step] * times, 4_000_001) > 15.0
+    assert not fits(z, [step] * times)
+    # while the same steps cut off before they leave it are accepted
+    n = max(k for k in range(1, times) if largest([step] * k, 4_000_001) < 14.0)
+    assert fits(z, [step] * n)
+
+
+def test_schedules_are_followed_exactly(z):
+    rng = random.Random(5)
+    taken = 0
+    for _ in range(400):
+        coefs = [tuple(np.float32(v) for v in (rng.uniform(0.5, 4.5), rng.uniform(-7, 1), rng.uniform(-1, 4)))
+                 for _ in range(rng.randint(1, 4))]
+        worst = largest([tuple(map(float, c)) for c in coefs], 200_001)
+        if worst > 15.001:
+            assert not fits(z, coefs)
+        elif worst < 14.5:
+            # at most four steps of slope under 60: the grid is within 0.5 of the true bound
+            assert fits(z, coefs)
+            taken += 1
+    assert 40 < taken < 360
+    for coefs in ([(0.0, 0.0, 0.0)], [(1.0, 0.0, 0.0)] * 32, [(-1.5, 0.5, 0.0)] * 12, [(0.0, 2.5, -1.5)] * 3,
+                  [(3.4445, -4.7750, 2.0315)] * 32):
+        assert fits(z, coefs)
+    for coefs in ([(float("inf"), 0.0, 0.0)], [(0.0, float("nan"), 0.0)], [(1e30, 0.0, 0.0)] * 2, [(3.9, 0.0, 0.0)] * 2):
+        assert not fits(z, coefs)

@@ -82,24 +82,43 @@ constexpr int kDefaultSteps = 5;
 
 long long extent(const zero_matrices* d, long long ld) { return (d->rows - 1) * ld + d->cols; }
 
-// The products keep x, its Gram matrix G and b G + c G G in fp16 times 2^12,
+// The products keep x, its Gram matrix G and P = b G + c G G in fp16 times 2^12,
 // so their entries (bounded by the largest singular value s of x, by s^2 and
 // by |b s^2 + c s^4|) must stay below 16.  x starts with every singular value
-// in [0, 1]; the schedule is followed over a grid of them.
+// in [0, 1].  A step's polynomial is continuous and keeps 0, so it takes the
+// interval of singular values (signs included) to an interval, from its least
+// to its largest value at the ends and where it turns: the reachable values
+// after each step exactly, with none missed between samples.
 bool schedule_fits(int steps, const float* coefs)
 {
-    constexpr int kGrid = 512;
-    for (int i = 0; i <= kGrid; ++i) {
-        double s = static_cast<double>(i) / kGrid;
-        for (int k = 0; k < steps; ++k) {
-            const double a = coefs[3 * k], b = coefs[3 * k + 1], c = coefs[3 * k + 2], g = s * s;
-            const double p = b * g + c * g * g;
-            if (!(g <= 15.0) || !(std::fabs(p) <= 15.0)) return false;
-            s = s * (a + p);
+    double lo = 0.0, hi = 1.0;
+    for (int k = 0; k < steps; ++k) {
+        const double a = coefs[3 * k], b = coefs[3 * k + 1], c = coefs[3 * k + 2];
+        if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return false;
+        const double g = (hi > -lo ? hi : -lo) * (hi > -lo ? hi : -lo);   // s^2 fills [0, g]
+        const auto p = [&](double q) { return q * (b + c * q); };
+        if (!(g <= 15.0) || !(std::fabs(p(g)) <= 15.0)) return false;
+        const double top = -b / (2.0 * c);                                // where p turns
+        if (top > 0.0 && top < g && !(std::fabs(p(top)) <= 15.0)) return false;
+        const auto f = [&](double s) { return s * (a + p(s * s)); };
+        double least = std::fmin(f(lo), f(hi)), most = std::fmax(f(lo), f(hi));
+        const auto turn = [&](double q) {   // f' = a + 3 b q + 5 c q^2 is 0 at s^2 = q
+            if (!(q > 0.0 && q < g)) return;
+            for (double s : {-std::sqrt(q), std::sqrt(q)})
+                if (s > lo && s < hi) least = std::fmin(least, f(s)), most = std::fmax(most, f(s));
+        };
+        const double d = 9.0 * b * b - 20.0 * a * c;
+        if (c == 0.0) {
+            if (b != 0.0) turn(-a / (3.0 * b));
+        } else if (d >= 0.0) {
+            const double u = -0.5 * (3.0 * b + std::copysign(std::sqrt(d), b));   // the roots without cancellation
+            turn(u / (5.0 * c));
+            if (u != 0.0) turn(a / u);
         }
-        if (!std::isfinite(s)) return false;
+        lo = std::fmin(least, 0.0);
+        hi = std::fmax(most, 0.0);
     }
-    return true;
+    return std::isfinite(lo) && std::isfinite(hi);
 }
 
 zero_status check_matrices(const zero_matrices* d)
