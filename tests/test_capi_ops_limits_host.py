@@ -78,3 +78,22 @@ def test_schedules_are_followed_exactly(z):
         assert fits(z, coefs)
     for coefs in ([(float("inf"), 0.0, 0.0)], [(0.0, float("nan"), 0.0)], [(1e30, 0.0, 0.0)] * 2, [(3.9, 0.0, 0.0)] * 2):
         assert not fits(z, coefs)
+
+
+def test_muon_flags_are_checked(z):
+    import ctypes
+    a, b, c, d, e, f, g = (0x100000000 * k for k in range(1, 8))
+
+    def muon(sc=g, **kw):
+        hp = z.muon_hparams()
+        for k, v in kw.items():
+            setattr(hp, k, v)
+        ranks = (ctypes.c_void_p * 2)(a, b)
+        return z._capi.raw_status("zero_muon_step", ctypes.byref(z.matrices(32, 64)), ctypes.byref(hp), 2, ranks, c, d, e,
+                                  f, sc, None)
+
+    for k in ("nesterov", "loss_scaling", "clipping"):
+        assert muon(**{k: 2}) == 1 and muon(**{k: -1}) == 1
+    # what they read is the scalars block
+    assert muon(sc=None, loss_scaling=1) == 1 and muon(sc=None, clipping=1) == 1
+    assert z.muon_hparams(loss_scaling=True, clipping=True).loss_scaling == 1

@@ -84,7 +84,8 @@ class ZeroMatrices(ctypes.Structure):
 
 class ZeroMuonHparams(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_float), ("momentum", ctypes.c_float), ("weight_decay", ctypes.c_float),
-                ("rms_scale", ctypes.c_float), ("loss_scale", ctypes.c_float), ("nesterov", ctypes.c_int)]
+                ("rms_scale", ctypes.c_float), ("loss_scale", ctypes.c_float), ("nesterov", ctypes.c_int),
+                ("loss_scaling", ctypes.c_int), ("clipping", ctypes.c_int)]
 
 
 _SIGS = {
@@ -479,8 +480,12 @@ def matrices(rows, cols, batch=1, dtype=ZERO_BF16, out_dtype=None, in_ld=0, out_
     return d
 
 
-def muon_hparams(lr=0.02, momentum=0.95, weight_decay=0.0, rms_scale=0.0, loss_scale=1.0, nesterov=True):
-    return ZeroMuonHparams(lr, momentum, weight_decay, rms_scale, loss_scale, int(bool(nesterov)))
+def muon_hparams(lr=0.02, momentum=0.95, weight_decay=0.0, rms_scale=0.0, loss_scale=1.0, nesterov=True,
+                 loss_scaling=False, clipping=False):
+    """loss_scaling, clipping: by the scalars block that zero_muon_step is then given (loss scale and
+    skipped steps, clip coefficient)."""
+    return ZeroMuonHparams(lr, momentum, weight_decay, rms_scale, loss_scale, int(bool(nesterov)),
+                           int(bool(loss_scaling)), int(bool(clipping)))
 
 
 def zero_orthogonalize_workspace_bytes(desc):
@@ -492,7 +497,8 @@ def zero_muon_workspace_bytes(desc):
 
 
 def zero_orthogonalize(desc, g, out, ws, scalars=None, stream=None):
-    """out = the orthogonalised g, matrix by matrix; ws: zero_orthogonalize_workspace_bytes(desc) bytes."""
+    """out = the orthogonalised g, matrix by matrix; ws: zero_orthogonalize_workspace_bytes(desc) bytes.
+    Without scalars a bounded wait that runs out is not reported."""
     _check(_lib.zero_orthogonalize(ctypes.byref(desc), _addr(g), _addr(out), _addr(ws), _addr(scalars),
                                    _stream(stream)), "zero_orthogonalize")
 
@@ -500,7 +506,8 @@ def zero_orthogonalize(desc, g, out, ws, scalars=None, stream=None):
 def zero_muon_step(desc, hp, rank_grads, momentum, master, lp_out, ws, scalars=None, stream=None):
     """One Muon step of the batch: rank mean, momentum, orthogonalised update,
     fp32 master and 16-bit weights (lp_out, or None); momentum and master in
-    place.  ws: zero_muon_workspace_bytes(desc) bytes."""
+    place.  ws: zero_muon_workspace_bytes(desc) bytes.  Without scalars a
+    bounded wait that runs out is not reported."""
     ranks = _ptr_array(rank_grads)
     _check(_lib.zero_muon_step(ctypes.byref(desc), ctypes.byref(hp), len(ranks), ranks, _addr(momentum),
                                _addr(master), _addr(lp_out), _addr(ws), _addr(scalars), _stream(stream)),

@@ -249,7 +249,10 @@ ZERO_API zero_status zero_muon_step(const zero_matrices* d, const zero_muon_hpar
     const float v[] = {hp->lr, hp->momentum, hp->weight_decay, hp->rms_scale, hp->loss_scale};
     for (float x : v)
         if (!std::isfinite(x) || x < 0.0f) return ZERO_ERR_INVALID_ARG;
-    if (hp->momentum >= 1.0f || (hp->nesterov != 0 && hp->nesterov != 1)) return ZERO_ERR_INVALID_ARG;
+    if (hp->momentum >= 1.0f) return ZERO_ERR_INVALID_ARG;
+    for (int f : {hp->nesterov, hp->loss_scaling, hp->clipping})
+        if (f != 0 && f != 1) return ZERO_ERR_INVALID_ARG;
+    if ((hp->loss_scaling || hp->clipping) && sc == nullptr) return ZERO_ERR_INVALID_ARG;
     for (int r = 0; r < n_d; ++r)
         if ((s = zk::check_dev(rank_grads[r])) != ZERO_OK) return s;
     if ((s = zk::check_dev(momentum)) != ZERO_OK || (s = zk::check_dev(master)) != ZERO_OK) return s;
@@ -276,6 +279,8 @@ ZERO_API zero_status zero_muon_step(const zero_matrices* d, const zero_muon_hpar
     a.divisor = static_cast<float>(n_d) * (hp->loss_scale > 0.0f ? hp->loss_scale : 1.0f);
     a.mu = hp->momentum;
     a.nesterov = hp->nesterov;
+    a.loss_scaling = hp->loss_scaling;
+    a.clipping = hp->clipping;
     a.momentum = momentum;
     a.master = master;
     a.lp = lp_out;

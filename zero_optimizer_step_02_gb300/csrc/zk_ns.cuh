@@ -168,6 +168,8 @@ __device__ __forceinline__ float block_scale(float4 sums, float eps, float* shar
 struct MuonArgs {
     const void* rank[ZERO_MAX_RANKS];
     int n_d, dtype, nesterov;
+    int loss_scaling, clipping;  // the divisor's scale and the coefficient are the scalars block's
+    zero_dev_scalars* sc;
     float divisor, mu;
     float* momentum;
     float* u;
@@ -178,20 +180,29 @@ struct MuonArgs {
     int n_counters;
 };
 
-// Rank mean (rank order, fp32), momentum, and the update direction u of
-// elements 8 i .. of matrix b: m <- mu m + g, u = g + mu m (Nesterov) or m;
-// zeros past the matrix.
-__device__ __forceinline__ void muon_direction8(const MuonArgs& a, int b, uint32_t i, float (&u)[8])
+// What the rank sums are divided and multiplied by (without clipping: 1, exact).
+struct MuonMean {
+    float divisor, coef;
+    __device__ __forceinline__ explicit MuonMean(const MuonArgs& a)
+    {
+        divisor = a.loss_scaling ? __fmul_rn(static_cast<float>(a.n_d), a.sc->loss_scale) : a.divisor;
+        coef = a.clipping ? a.sc->clip_coef : 1.0f;
+    }
+    __device__ __forceinline__ float of(float sum) const { return __fmul_rn(__fdiv_rn(sum, divisor), coef); }
+};
+
+// whether this step is one to skip (set by muon_check, or before the call)
+__device__ __forceinline__ bool muon_skips(const MuonArgs& a)
 {
-    const int n = a.elems - 8 * i < 8 ? static_cast<int>(a.elems - 8 * i) : 8;
-    const long long at = b * a.stride + 8ll * i;
-    float g[8], m[8];
+    return a.loss_scaling && *reinterpret_cast<volatile int*>(&a.sc->nonfinite) != 0;
+}
+
+// the ranks' sums (rank order, fp32) of elements `at` .. of which n <= 8 exist
+__device__ __forceinline__ void rank_sums8(const MuonArgs& a, long long at, int n, float (&g)[8])
+{
 #pragma unroll
-    for (int e = 0; e < 8; ++e) g[e] = m[e] = 0.0f;
-    float* mp = a.momentum + at;
+    for (int e = 0; e < 8; ++e) g[e] = 0.0f;
     if (n == 8) {
-        const float4 x = *reinterpret_cast<const float4*>(mp), y = *reinterpret_cast<const float4*>(mp + 4);
-        m[0] = x.x, m[1] = x.y, m[2] = x.z, m[3] = x.w, m[4] = y.x, m[5] = y.y, m[6] = y.z, m[7] = y.w;
 #pragma unroll 4
         for (int q = 0; q < a.n_d; ++q) {
             const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.rank[q]) + at);
@@ -206,16 +217,33 @@ __device__ __forceinline__ void muon_direction8(const MuonArgs& a, int b, uint32
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             if (e >= n) continue;
-            m[e] = mp[e];
             for (int q = 0; q < a.n_d; ++q) {
                 const uint16_t h = static_cast<const uint16_t*>(a.rank[q])[at + e];
                 g[e] += a.dtype == ZERO_BF16 ? Lp<ZERO_BF16>::widen(h) : Lp<ZERO_FP16>::widen(h);
             }
         }
     }
+}
+
+// Momentum and the update direction u of elements 8 i .. of matrix b:
+// m <- mu m + g, u = g + mu m (Nesterov) or m; zeros past the matrix.
+__device__ __forceinline__ void muon_direction8(const MuonArgs& a, const MuonMean& mean_of, int b, uint32_t i, float (&u)[8])
+{
+    const int n = a.elems - 8 * i < 8 ? static_cast<int>(a.elems - 8 * i) : 8;
+    const long long at = b * a.stride + 8ll * i;
+    float g[8], m[8];
+    float* mp = a.momentum + at;
+    if (n == 8) {
+        const float4 x = *reinterpret_cast<const float4*>(mp), y = *reinterpret_cast<const float4*>(mp + 4);
+        m[0] = x.x, m[1] = x.y, m[2] = x.z, m[3] = x.w, m[4] = y.x, m[5] = y.y, m[6] = y.z, m[7] = y.w;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m[e] = e < n ? mp[e] : 0.0f;
+    }
+    rank_sums8(a, at, n, g);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const float mean = __fdiv_rn(g[e], a.divisor);
+        const float mean = mean_of.of(g[e]);
         m[e] = __fadd_rn(__fmul_rn(a.mu, m[e]), mean);
         u[e] = e >= n ? 0.0f : a.nesterov ? __fadd_rn(mean, __fmul_rn(a.mu, m[e])) : m[e];
     }

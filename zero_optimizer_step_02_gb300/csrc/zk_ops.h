@@ -66,6 +66,7 @@ struct NsArgs {
     int n_d;
     float divisor, mu;
     int nesterov;
+    int loss_scaling, clipping;   // from the scalars block
     float* momentum;
     float* master;
     void* lp;

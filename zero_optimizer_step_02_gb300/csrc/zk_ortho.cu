@@ -96,6 +96,7 @@ struct NsKernelArgs {
     unsigned* tile_bar;          // [groups][ctas]
     float* partial;              // [groups * ctas][128 * BN]
     zero_dev_scalars* sc;
+    int guarded;                 // nothing to do where sc's non-finite flag is set (loss scaling)
     int starve;                  // issue no copy, so that every wait runs out
     unsigned long long timeout_ns;
 };
@@ -461,6 +462,25 @@ __global__ void __launch_bounds__(256) ns_sqnorm(const __grid_constant__ PrepArg
     if (threadIdx.x == 0) a.parts[blockIdx.y * static_cast<long long>(gridDim.x) + blockIdx.x] = sums;
 }
 
+// Dynamic loss scaling: flags a step in which an averaged gradient is not finite,
+// before anything of it is written.  Reads the ranks' gradients once; only calls
+// with loss scaling launch it.
+__global__ void __launch_bounds__(256) muon_check(const __grid_constant__ MuonArgs a)
+{
+    pdl_wait();
+    if (muon_skips(a)) return;
+    const MuonMean mean(a);
+    bool bad = false;
+    for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i * 8u < a.elems; i += gridDim.x * 256) {
+        const uint32_t left = a.elems - 8 * i;
+        float g[8];
+        rank_sums8(a, blockIdx.y * a.stride + 8ll * i, left < 8 ? static_cast<int>(left) : 8, g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) bad |= !is_finite_f32(mean.of(g[e]));
+    }
+    if (bad) atomicOr(&a.sc->nonfinite, 1);
+}
+
 // The update direction of every matrix, with the sums of its squares: reads the
 // ranks' gradients and the momentum once, writes the momentum and the direction
 // in fp32.  Bound by memory: 2 x 4096 x 4096 over four ranks in 97 us (6.9
@@ -469,11 +489,13 @@ __global__ void __launch_bounds__(256) muon_direction(const __grid_constant__ Mu
 {
     __shared__ float4 red[8];
     pdl_wait();
+    if (muon_skips(a)) return;
+    const MuonMean mean(a);
     clear_counters(a.counters, a.n_counters);
     SquareSum s;
     for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i * 8u < a.elems; i += gridDim.x * 256) {
         float u[8];
-        muon_direction8(a, blockIdx.y, i, u);
+        muon_direction8(a, mean, blockIdx.y, i, u);
         s.add8(u);
     }
     const float4 sums = block_sums(s.value(), red);
@@ -650,6 +672,7 @@ template <int CG, int BN, bool JOINT>
 __global__ void __launch_bounds__(kThreads, 1) ns_kernel(const __grid_constant__ NsKernelArgs a)
 {
     using S = MmShape<CG, BN, JOINT>;
+    if (a.guarded && *reinterpret_cast<volatile int*>(&a.sc->nonfinite) != 0) return;   // the same for every thread
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint64_t full[S::kStages], empty[S::kStages], acc_full[2], acc_empty[2], drain;
     __shared__ uint32_t tmem_base;
@@ -1199,6 +1222,9 @@ cudaError_t launch_ns(const NsArgs& a, cudaStream_t st)
         mu.n_d = a.n_d;
         mu.dtype = a.in_dtype;
         mu.nesterov = a.nesterov;
+        mu.loss_scaling = a.loss_scaling;
+        mu.clipping = a.clipping;
+        mu.sc = a.sc;
         mu.divisor = a.divisor;
         mu.mu = a.mu;
         mu.momentum = a.momentum;
@@ -1210,9 +1236,15 @@ cudaError_t launch_ns(const NsArgs& a, cudaStream_t st)
         mu.counters = counters;
         mu.n_counters = kMaxSms * (kBarStride + 1);
     }
-    if (small_ns_fits(a.rows, a.cols, a.products)) return launch_small_ns(a, muon ? &mu : nullptr, st);
     const int sms = sm_count();
     if (sms == 0) return cudaErrorInvalidDevice;
+    // the norm: CTAs a matrix, four chunks a thread (Muon, with more to load for
+    // each: one; 768 x 768 over 16 ranks, the whole step, 218 -> 203 us), eight CTAs an SM over the batch
+    const int chunks = (a.cols + 7) / 8, want = muon ? 256 : 1024;
+    const int parts_n = parts_of(a.batch, (static_cast<long long>(a.rows) * chunks + want - 1) / want, sms);
+    const dim3 grid(static_cast<unsigned>(parts_n), a.batch);
+    if (muon && a.loss_scaling) ZK_GO(launch_after(muon_check, grid, dim3(256), 0, st, mu));
+    if (small_ns_fits(a.rows, a.cols, a.products)) return launch_small_ns(a, muon ? &mu : nullptr, st);
     const Plan plan = plan_of(a.rows, a.cols, a.batch, a.products, sms);
     NsKernelArgs k;
     std::memset(&k, 0, sizeof(k));
@@ -1232,7 +1264,7 @@ cudaError_t launch_ns(const NsArgs& a, cudaStream_t st)
     k.ctas = plan.ctas;
     std::memcpy(k.split, plan.split, sizeof(k.split));
     std::memcpy(k.coef, a.coef, sizeof(k.coef));
-    k.chunks = (a.cols + 7) / 8;
+    k.chunks = chunks;
     k.eps = a.eps;
     k.parts = parts;
     k.group_bar = counters;
@@ -1241,11 +1273,7 @@ cudaError_t launch_ns(const NsArgs& a, cudaStream_t st)
     k.sc = a.sc;
     k.timeout_ns = kDefaultTimeoutNs;
 
-    // the norm: CTAs a matrix, four chunks a thread (Muon, with more to load for
-    // each: one; 768 x 768 over 16 ranks, the whole step, 218 -> 203 us), eight CTAs an SM over the batch
-    const long long chunks = static_cast<long long>(a.rows) * k.chunks;
-    k.parts_n = parts_of(a.batch, (chunks + (muon ? 255 : 1023)) / (muon ? 256 : 1024), sms);
-    const dim3 grid(static_cast<unsigned>(k.parts_n), a.batch);
+    k.parts_n = parts_n;
     if (muon) {
         k.in = mu.u;
         k.in_dtype = ZERO_FP32;
@@ -1253,6 +1281,7 @@ cudaError_t launch_ns(const NsArgs& a, cudaStream_t st)
         k.in_stride = mu.u_stride;
         k.in_vec = a.cols % 4 == 0;
         k.res = RES_MUON;
+        k.guarded = a.loss_scaling;
         k.master = a.master;
         k.lp = a.lp;
         k.out_dtype = a.lp_dtype;

@@ -117,6 +117,10 @@ __device__ __forceinline__ void issue(uint32_t tmem, uint32_t a, int a_lo, uint3
 template <bool MUON>
 __device__ __forceinline__ void ns_small_body(const SmallNsArgs& a, const MuonArgs* mu)
 {
+    if (MUON && mu->loss_scaling) {
+        pdl_wait();
+        if (muon_skips(*mu)) return;   // the same for every thread
+    }
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint64_t bar, drain;
     __shared__ uint32_t tmem_base;
@@ -141,9 +145,10 @@ __device__ __forceinline__ void ns_small_body(const SmallNsArgs& a, const MuonAr
     const int chunks = (a.cols + 7) / 8, total = a.rows * chunks;
     SquareSum q;
     if (MUON) {
+        const MuonMean mean(*mu);
         for (uint32_t i = t; 8 * i < mu->elems; i += kSmallThreads) {
             float u[8];
-            muon_direction8(*mu, b, i, u);
+            muon_direction8(*mu, mean, b, i, u);
             q.add8(u);
         }
     } else {
