@@ -104,3 +104,27 @@ def test_fp32_rows_with_an_offset_are_centred_before_they_are_scaled(cols, lies)
                       + 4 * (np.abs(h) + np.abs(m1) + np.abs(xhat * m2)))
     assert np.all(np.abs(f64(c.dx) - want) <= U32 * np.abs(want) + e)
     c.guards_intact()
+
+
+# Widths above 8192 with many rows to a part: even and odd numbers of them, a
+# last pair that is one row, parts without a last row.  A column's sum is a
+# chain over a part's rows (16 parts at least), then over every sixteenth part
+# (304 at most), then a tree of sixteen.
+@pytest.mark.parametrize("lies", [((0, 0),) * 4, ((8, 8),) * 4, ((3, 1),) * 4, ((0, 0), (3, 1), (1, 2), (5, 0))])
+@pytest.mark.parametrize("rows,cols", [(700, 16384), (333, 20001), (129, 40000), (67, 65536), (1300, 8200), (33, 131073)])
+@pytest.mark.parametrize("dt", [BF16, FP32])
+def test_many_rows_above_8192_columns(rows, cols, dt, lies):
+    c = Unlike(rows, cols, dt, lies)
+    c.forward()
+    c.check_forward()
+    c.backward()
+    c.check_backward(dgain=False, dbias=False)
+    x, dy = f64(c.x), f64(c.dy)
+    mean, rstd = f64(c.mean)[:, None], f64(c.rstd)[:, None]
+    xhat, e_x = (x - mean) * rstd, 3 * U32 * (np.abs(x) + np.abs(mean)) * rstd
+    depth = rows / 16 + 1 + 304 / 16 + 4
+    for t, terms, e_t in ((c.dgain, dy * xhat, np.abs(dy) * e_x), (c.dbias, dy, 0 * dy)):
+        e = (depth + 2) * U32 * np.abs(terms).sum(0) + e_t.sum(0)
+        want = terms.sum(0)
+        assert np.all(np.abs(f64(t) - want) <= U32 * np.abs(want) + e)
+    c.guards_intact()
