@@ -653,6 +653,17 @@ ZERO_API zero_status zero_debug_stream_timeout(int kernel, void* scratch, zero_d
 ZERO_API zero_status zero_debug_wait_timeout(zero_dev_scalars* scalars_dev, long long timeout_ns,
                                              void* stream);
 
+/* How zero_orthogonalize (muon 0) or zero_muon_step (muon 1) cuts a batch up on
+ * a device of `sms` SMs (>= 2).  Host only; for tests of each form.         */
+typedef struct {
+    int products;              /* 1 or 3                                             */
+    int tile_rows, tile_cols;  /* of the result; 0: each matrix in one SM            */
+    int groups;                /* matrices under way at a time                       */
+    int units;                 /* CTAs (tile_rows 128) or pairs (256) of a group     */
+    int split[3];              /* units that share a tile's depth, in the three products of a step */
+} zero_matrix_plan;
+ZERO_API zero_status zero_debug_matrix_plan(const zero_matrices* desc, int muon, int sms, zero_matrix_plan* out);
+
 /* The matrix product's timeout path: one 64 x 64 x 64 product whose copies are
  * never issued, so every bounded wait runs out after timeout_ns (at most 10 s);
  * it sets ZERO_DEV_TIMEOUT in scalars->status, gives its tensor memory back and

@@ -97,3 +97,42 @@ def test_muon_flags_are_checked(z):
     # what they read is the scalars block
     assert muon(sc=None, loss_scaling=1) == 1 and muon(sc=None, clipping=1) == 1
     assert z.muon_hparams(loss_scaling=True, clipping=True).loss_scaling == 1
+
+
+# ------------------------------------------- the forms of the matrix updates
+def test_the_tested_shapes_take_the_forms_they_stand_for(z):
+    from matrix_forms import FORMS, MUON_FORMS, form_of
+    for (rows, cols, batch, products), form in FORMS.items():
+        assert form_of(z, rows, cols, batch, products) == (products, form), (rows, cols, batch, products)
+    for (rows, cols, batch), form in MUON_FORMS.items():
+        assert form_of(z, rows, cols, batch, 0, True) == (3, form), (rows, cols, batch)
+
+
+def test_no_form_is_left_out(z):
+    """Whatever form some shape takes has a shape that the GPU tests run."""
+    from matrix_forms import FORMS, form_of
+    tested = {(k[3], v) for k, v in FORMS.items()} | {(3, None)}
+    rng = random.Random(11)
+    reached = {}
+    for _ in range(6000):
+        rows, cols, batch = (int(2 ** rng.uniform(0, e)) for e in (13, 13, 6))
+        if rows * cols * batch > 1 << 26:
+            continue
+        for products in (1, 3):
+            reached.setdefault(form_of(z, rows, cols, batch, products), (rows, cols, batch))
+    missing = {f: s for f, s in reached.items() if f not in tested}
+    assert not missing
+    assert len(reached) >= 12
+
+
+def test_matrix_plan_arguments_are_checked(z):
+    d = z.matrices(300, 400)
+    for muon, sms in ((2, 152), (-1, 152), (False, 1)):
+        with pytest.raises(z.ZeroError):
+            import ctypes
+            out = z._capi.ZeroMatrixPlan()
+            z._capi._check(z._capi.raw_status("zero_debug_matrix_plan", ctypes.byref(d), muon, sms, ctypes.byref(out)), "plan")
+    assert z._capi.raw_status("zero_debug_matrix_plan", None, 0, 152, None) == 1
+    for sms in (2, 3, 64, 152, 160, 1000):
+        p = z.zero_debug_matrix_plan(d, sms=sms)
+        assert p.groups * p.units * (p.tile_rows // 128) <= min(sms, 160)

@@ -88,6 +88,12 @@ class ZeroMuonHparams(ctypes.Structure):
                 ("loss_scaling", ctypes.c_int), ("clipping", ctypes.c_int)]
 
 
+class ZeroMatrixPlan(ctypes.Structure):
+    """zero_matrix_plan of zero.h: how a batch of matrices is cut up."""
+    _fields_ = [("products", ctypes.c_int), ("tile_rows", ctypes.c_int), ("tile_cols", ctypes.c_int),
+                ("groups", ctypes.c_int), ("units", ctypes.c_int), ("split", ctypes.c_int * 3)]
+
+
 _SIGS = {
     "zero_status_str": (ctypes.c_char_p, [_i32]),
     "zero_abi_version": (_i32, []),
@@ -128,6 +134,7 @@ _SIGS = {
     "zero_muon_step": (_i32, [ctypes.POINTER(ZeroMatrices), ctypes.POINTER(ZeroMuonHparams), _i32, _vp, _vp, _vp, _vp,
                               _vp, _vp, _vp]),
     "zero_debug_matmul_timeout": (_i32, [_vp, _vp, _ll, _vp]),
+    "zero_debug_matrix_plan": (_i32, [ctypes.POINTER(ZeroMatrices), _i32, _i32, ctypes.POINTER(ZeroMatrixPlan)]),
     "zero_layernorm_workspace_bytes": (_sz, [ctypes.POINTER(ZeroLayerNorm)]),
     "zero_layernorm_forward": (_i32, [ctypes.POINTER(ZeroLayerNorm), _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "zero_layernorm_backward": (_i32, [ctypes.POINTER(ZeroLayerNorm), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
@@ -512,6 +519,13 @@ def zero_muon_step(desc, hp, rank_grads, momentum, master, lp_out, ws, scalars=N
     _check(_lib.zero_muon_step(ctypes.byref(desc), ctypes.byref(hp), len(ranks), ranks, _addr(momentum),
                                _addr(master), _addr(lp_out), _addr(ws), _addr(scalars), _stream(stream)),
            "zero_muon_step")
+
+
+def zero_debug_matrix_plan(desc, muon=False, sms=152):
+    """How a batch of matrices is cut up on a device of `sms` SMs (host only)."""
+    out = ZeroMatrixPlan()
+    _check(_lib.zero_debug_matrix_plan(ctypes.byref(desc), int(bool(muon)), sms, ctypes.byref(out)), "zero_debug_matrix_plan")
+    return out
 
 
 def zero_debug_matmul_timeout(scratch, scalars, timeout_ns, stream=None):

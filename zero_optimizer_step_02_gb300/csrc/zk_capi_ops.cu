@@ -296,6 +296,15 @@ ZERO_API zero_status zero_muon_step(const zero_matrices* d, const zero_muon_hpar
     return from_cuda(zk::launch_ns(a, as_stream(stream)));
 }
 
+ZERO_API zero_status zero_debug_matrix_plan(const zero_matrices* d, int muon, int sms, zero_matrix_plan* out)
+{
+    zero_status s;
+    if ((s = check_matrices(d)) != ZERO_OK) return s;
+    if (out == nullptr || sms < 2 || (muon != 0 && muon != 1)) return ZERO_ERR_INVALID_ARG;
+    zk::ns_plan(d->rows, d->cols, d->batch, products_of(d, muon != 0), sms, out);
+    return ZERO_OK;
+}
+
 ZERO_API zero_status zero_debug_matmul_timeout(void* scratch, zero_dev_scalars* sc, long long timeout_ns, void* stream)
 {
     ZK_CALL_RANGE();

@@ -79,6 +79,8 @@ struct NsArgs {
 
 size_t ns_workspace_bytes(int rows, int cols, int batch, int products, bool muon);
 cudaError_t launch_ns(const NsArgs& a, cudaStream_t st);
+// how a call is cut up on a device of `sms` SMs (zero_matrix_plan)
+void ns_plan(int rows, int cols, int batch, int products, int sms, zero_matrix_plan* out);
 // one matrix product whose copies are never issued (tests the timeout path);
 // scratch: 16 KB
 cudaError_t launch_mm_starved(void* scratch, zero_dev_scalars* sc, unsigned long long timeout_ns, cudaStream_t st);

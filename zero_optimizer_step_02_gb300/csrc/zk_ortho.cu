@@ -1180,6 +1180,22 @@ size_t ns_workspace_bytes(int rows, int cols, int batch, int products, bool muon
     return layout_of(rows, cols, batch, products, muon).end;
 }
 
+void ns_plan(int rows, int cols, int batch, int products, int sms, zero_matrix_plan* out)
+{
+    std::memset(out, 0, sizeof(*out));
+    out->products = products;
+    if (small_ns_fits(rows, cols, products)) {
+        out->groups = batch;
+        return;
+    }
+    const Plan p = plan_of(rows, cols, batch, products, sms < kMaxSms ? sms : kMaxSms);
+    out->tile_rows = kBM * p.cg;
+    out->tile_cols = p.bn;
+    out->groups = p.groups;
+    out->units = p.ctas / p.cg;
+    std::memcpy(out->split, p.split, sizeof(out->split));
+}
+
 #define ZK_GO(expr)                             \
     do {                                        \
         const cudaError_t e_ = (expr);          \
