@@ -511,15 +511,15 @@ typedef struct {
  * contents need not be kept or cleared); 0 for an invalid descriptor.       */
 ZERO_API size_t zero_layernorm_workspace_bytes(const zero_layernorm* desc);
 
-/* y may be x (same stride); any other overlap of the two is refused, and no
+/* y may be x (same stride, or one row); any other overlap of the two is refused, and no
  * other array that is written may overlap any.  gain NULL: ones, bias NULL:
  * zeros; mean and rstd NULL: not stored.  One kernel.                       */
 ZERO_API zero_status zero_layernorm_forward(const zero_layernorm* desc, const void* x, const void* gain,
                                             const void* bias, void* y, float* mean, float* rstd, void* stream);
 
 /* mean and rstd as the forward call stored them.  dx may be dy or x (same
- * stride; other overlaps of them are refused), no other array that is written
- * may overlap any.  dgain and dbias are overwritten, not accumulated; either
+ * stride, or one row; other overlaps of them are refused), no other array that
+ * is written may overlap any.  dgain and dbias are overwritten, not accumulated; either
  * may be NULL (not computed).  Two kernels; three for rows of more than
  * 8176 to 8192 columns (as they lie).                                       */
 ZERO_API zero_status zero_layernorm_backward(const zero_layernorm* desc, const void* dy, const void* x,

@@ -128,3 +128,20 @@ def test_many_rows_above_8192_columns(rows, cols, dt, lies):
         want = terms.sum(0)
         assert np.all(np.abs(f64(t) - want) <= U32 * np.abs(want) + e)
     c.guards_intact()
+
+
+@pytest.mark.parametrize("cols", [40, 768, 1601, 16384])
+@pytest.mark.parametrize("dt", [BF16, FP32])
+def test_one_row_in_place_whatever_its_strides(cols, dt):
+    c = Unlike(1, cols, dt, LIES[0])
+    c.forward()
+    c.backward()
+    d = z.layernorm(1, cols, dtype=dt, x_stride=cols + 3, y_stride=5 * cols, dy_stride=cols, dx_stride=2 * cols)
+    for over in ("x", "dy"):
+        k = Unlike(1, cols, dt, LIES[0])
+        z.zero_layernorm_backward(d, k.dy, k.x, k.gain, c.mean, c.rstd, getattr(k, over), k.dgain, k.dbias, k.ws)
+        assert torch.equal(getattr(k, over), c.dx) and torch.equal(k.dgain, c.dgain)
+        k.guards_intact()
+    z.zero_layernorm_forward(d, c.x, c.gain, c.bias, c.x)
+    assert torch.equal(c.x, c.y)
+    c.guards_intact()

@@ -23,6 +23,8 @@ zero_status check_elems(const void* p, int dt)
 
 // ------------------------------------------------------------- layer norm
 long long stride_of(long long s, int cols) { return s == 0 ? cols : s; }
+// a single row's stride says nothing
+long long row_stride(const zero_layernorm* d, long long s) { return d->rows == 1 ? d->cols : stride_of(s, d->cols); }
 
 zero_status check_ln(const zero_layernorm* d)
 {
@@ -72,7 +74,7 @@ zk::LnArgs ln_args(const zero_layernorm* d)
     a.dtype = d->dtype;
     a.w_dtype = d->w_dtype;
     a.eps = d->eps;
-    a.x_stride = stride_of(d->x_stride, d->cols);
+    a.x_stride = row_stride(d, d->x_stride);
     return a;
 }
 
@@ -334,7 +336,7 @@ ZERO_API zero_status zero_layernorm_forward(const zero_layernorm* d, const void*
     if (bias != nullptr && (s = check_elems(bias, d->w_dtype)) != ZERO_OK) return s;
     if (!zk::aligned(mean, 4) || !zk::aligned(rstd, 4)) return ZERO_ERR_MISALIGNED;
     zk::LnArgs a = ln_args(d);
-    a.out_stride = stride_of(d->y_stride, d->cols);
+    a.out_stride = row_stride(d, d->y_stride);
     if (shares(x, a.x_stride, y, a.out_stride, d->rows, d->cols, zk::dtype_bytes(d->dtype))) return ZERO_ERR_INVALID_ARG;
     a.x = x;
     a.gain = gain;
@@ -363,8 +365,8 @@ ZERO_API zero_status zero_layernorm_backward(const zero_layernorm* d, const void
     if (dbias != nullptr && (s = check_elems(dbias, d->w_dtype)) != ZERO_OK) return s;
     if ((s = zk::check_dev(ws, 256)) != ZERO_OK) return s;
     zk::LnArgs a = ln_args(d);
-    a.dy_stride = stride_of(d->dy_stride, d->cols);
-    a.out_stride = stride_of(d->dx_stride, d->cols);
+    a.dy_stride = row_stride(d, d->dy_stride);
+    a.out_stride = row_stride(d, d->dx_stride);
     const int es = zk::dtype_bytes(d->dtype);
     if (shares(x, a.x_stride, dx, a.out_stride, d->rows, d->cols, es) ||
         shares(dy, a.dy_stride, dx, a.out_stride, d->rows, d->cols, es))
