@@ -14,17 +14,17 @@
 // rows up to 8% forward, bound by issue as they are, and fp32 rows nothing).
 //
 // Bound: memory.  Forward reads x and writes y, backward reads x and dy and
-// writes dx; at 6783 GB/s (a copy's rate) 8192 x 4096 bf16 cannot take less than
-// 19.8 us forward and 29.7 us backward.  Measured: forward 22.7 us (0.87 of a
-// copy), 16384 x 4096 42.5 us (0.93); backward 16384 x 4096 72 us (0.82; fp32 128
-// us, 0.93), its second kernel included.  Next to memory it is issue: a CTA of
-// sixteen warps an SM, 53% of the issue slots busy, fixed-latency and shared-
-// memory waits in between; every instruction a row fewer showed (the root and the
-// division 4 to 9%, addresses kept from row to row 4 to 20%).  Few rows are bound
-// by latency: 8 x 768 2.4 us, 256 x 768 backward 6 us (two kernels, the second's
-// start hidden behind the first).  Rows that do not lie on 16-byte words pay for
-// it: 2999 x 1601 fp32 forward 10.7 us alike and 11.2 us with unlike gaps (floor
-// 5.7), 5003 x 1601 fp16 backward 22.3 us (floor 7.1).
+// writes dx; at 6788 GB/s (a copy's rate) 8192 x 4096 bf16 cannot take less than
+// 19.8 us forward and 29.7 us backward.  Measured, call after call in a graph:
+// forward 22.9 us (0.86 of a copy), 16384 x 4096 42.4 us (0.93); backward 16384 x
+// 4096 72.8 us (0.81; fp32 131 us, 0.91), its second kernel included.  Next to
+// memory it is issue: a CTA of sixteen warps an SM, 53% of the issue slots busy,
+// fixed-latency and shared-memory waits in between; every instruction a row fewer
+// showed (the root and the division 4 to 9%, addresses kept from row to row 4 to
+// 20%).  Few rows are bound by latency: 8 x 768 2.3 us, 256 x 768 backward 6.3 us
+// (two kernels, the second's start hidden behind the first).  Rows that do not lie
+// on 16-byte words pay for it: 2999 x 1601 fp32 forward 11.6 us alike and 12.1 us
+// with unlike gaps (floor 5.7), 5003 x 1601 fp16 backward 21.8 us (floor 7.1).
 #include "zk_common.cuh"
 #include "zk_launch.h"
 #include "zk_ops.h"

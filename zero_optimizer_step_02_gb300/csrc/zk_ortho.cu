@@ -24,15 +24,15 @@
 //
 // Work and floor.  With m the short and n the long side, a step multiplies
 // m (m + 1) n + m^2 (m + 1) + 2 m^2 n times and adds as often (G and P are
-// symmetric: half their blocks), three times that with products = 3; at 1926
+// symmetric: half their blocks), three times that with products = 3; at 1912
 // TFLOP/s (a large library product's rate) 4096 x 14336 cannot take less than
-// 2.05 ms, twelve 768 x 768 56 us.  Large matrices are bound by the tensor
-// cores and, in effect, by power (4096 x 14336: 2.75 to 2.83 ms, 1.4 PFLOP/s).
+// 2.07 ms, twelve 768 x 768 57 us.  Large matrices are bound by the tensor
+// cores and, in effect, by power (4096 x 14336: 2.84 ms, 1.4 PFLOP/s).
 // Mid sizes are bound by what fifteen dependent products cost beside their
 // MMAs: a meeting of the CTAs (1 to 2 us), the first tiles' way from L2 (1 us)
 // and the last tiles' results (2 to 6 us); a 256 x 256 matrix, whose products
 // take 1 us each, pays 6.4 us a product.  Hence one launch for the whole
-// iteration (a launch for each product: 12 x 768 x 768 390 us, now 221), the
+// iteration (a launch for each product: 12 x 768 x 768 390 us, now 222), the
 // depth of a tile split among CTAs where tiles are few, and 32 x 32 pieces of
 // results that go out in whole 64-byte lines.
 #include <climits>
@@ -441,7 +441,7 @@ __device__ __forceinline__ void clear_counters(unsigned* c, int n)
 }
 
 // The sums of squares of every matrix, a partial sum for each CTA.  Reads the
-// input once: 4096 x 14336 bf16 in 25 us (4.6 TB/s, 1% of the call), 12 x 768 x
+// input once: 4096 x 14336 bf16 in 28 us (4.2 TB/s, 1% of the call), 12 x 768 x
 // 768 in 6 us.  Four loads under way a thread cost registers and were slower
 // (43 and 9 us).
 __global__ void __launch_bounds__(256) ns_sqnorm(const __grid_constant__ PrepArgs a)
@@ -463,8 +463,9 @@ __global__ void __launch_bounds__(256) ns_sqnorm(const __grid_constant__ PrepArg
 }
 
 // Dynamic loss scaling: flags a step in which an averaged gradient is not finite,
-// before anything of it is written.  Reads the ranks' gradients once; only calls
-// with loss scaling launch it.
+// before anything of it is written.  Reads the ranks' gradients once: 2 x 4096 x
+// 4096 over four ranks in 53 us (268 MB, 5 TB/s), 768 x 2304 over eight in 10 us;
+// only calls with loss scaling launch it.
 __global__ void __launch_bounds__(256) muon_check(const __grid_constant__ MuonArgs a)
 {
     pdl_wait();
@@ -483,8 +484,8 @@ __global__ void __launch_bounds__(256) muon_check(const __grid_constant__ MuonAr
 
 // The update direction of every matrix, with the sums of its squares: reads the
 // ranks' gradients and the momentum once, writes the momentum and the direction
-// in fp32.  Bound by memory: 2 x 4096 x 4096 over four ranks in 97 us (6.9
-// TB/s, 1.8% of the step); 768 x 2304 over eight ranks, 50 MB, in 16 us.
+// in fp32.  Bound by memory: 2 x 4096 x 4096 over four ranks in 98 us (6.8
+// TB/s, 1.7% of the step); 768 x 2304 over eight ranks, 50 MB, in 15 us.
 __global__ void __launch_bounds__(256) muon_direction(const __grid_constant__ MuonArgs a)
 {
     __shared__ float4 red[8];
@@ -516,14 +517,14 @@ __global__ void __launch_bounds__(256) muon_direction(const __grid_constant__ Mu
 // to 750 for 512; a pair's 256 x 256 tile brings 32 KB a CTA for 512 clocks of
 // MMAs, and measures 518.
 //
-// The forms, us for the whole five steps (timed side by side):
+// The forms, us for the whole five steps (timed side by side, cold L2):
 //                           one CTA 128    pair 128    pair 256
-//     24 x 384 x 384             131         159         177
-//     4 x 1024 x 1024            177         215         197
-//     12 x 768 x 768             225         222         227
-//     12 x 768 x 768, three      353         321         359
-//     2048 x 2048, three         444         386         512
-//     4096 x 4096               1336        1274         929
+//     24 x 384 x 384             135         167         183
+//     4 x 1024 x 1024            182         227         205
+//     12 x 768 x 768             231         231         229
+//     12 x 768 x 768, three      363         325         370
+//     2048 x 2048, three         455         396         518
+//     4096 x 4096               1362        1306         939
 // A 128 x 256 tile of one CTA was slower than the best of these everywhere, so
 // there is none.
 template <int CG, int BN, bool JOINT>
@@ -981,9 +982,11 @@ struct Plan {
 };
 
 // Times of a CTA or a pair, in us, that the choice goes by, fitted to shapes
-// timed in each form (from 256 x 256 to 4096 x 4096, one and three products; of
-// sixteen, the choice is within 2% of the best form for thirteen and 6% for
-// all): a 64-deep stage, the results of a tile beside the next tile's products
+// timed in each form.  Of 32 calls (sixteen shapes from 256 x 256 to 4096 x 4096,
+// one and three products) timed in every form side by side, the chosen form is the
+// best or within 1% of it for 27 and within 4% for all (single matrices of 512 to
+// 1024 with three products, where the pair form 128 wide is 2 to 4% faster): a
+// 64-deep stage, the results of a tile beside the next tile's products
 // and alone at the end, the same with an exchange of partial sums, the meeting
 // of a group and the first copies after it.
 struct Costs {
