@@ -595,8 +595,6 @@ typedef struct {
                             sqrt(max(1, rows / cols))                                */
     float loss_scale;    /* a fixed scale the gradients carry; 0 reads as 1          */
     int nesterov;        /* 1: direction g + mu m, 0: m                              */
-    int loss_scaling;    /* 1: dynamic loss scaling, as in zero_hparams (below)      */
-    int clipping;        /* 1: the averaged gradient times scalars_dev->clip_coef    */
 } zero_muon_hparams;
 
 /* One Muon step of a batch of equal matrices that lie in the flat parameter
@@ -608,23 +606,33 @@ typedef struct {
  *   lp_out = 16-bit cast of w (NULL: none)
  * momentum, master: fp32, updated in place.  rank_grads: host array of n_d
  * device pointers to the first matrix.  All 16-byte aligned; no array that is
- * written may overlap another one.
- *
- * loss_scaling and clipping (0 or 1) need the step's scalars_dev.  clipping: the
- * coefficient that zero_grad_sqnorm, or the clipped step before, left there.
- * loss_scaling: the divisor is n_d * scalars_dev->loss_scale (the field
- * loss_scale is not read), a kernel more reads the gradients first, and where an
- * averaged gradient of any of the call's matrices is not finite, or the
- * non-finite flag is set already, momentum, master and lp_out stay as they are
- * and the flag is set.  So the calls of a step come before the one that commits
- * its scalars (zero_step_fused, zero_adam_shard_step): with the flag set that
- * one skips its update too and halves the scale.  A call does not undo the calls
- * before it; a zero_reduce_scatter over a flat space that holds the matrices too,
- * before the first of them, has all skip or none.  Otherwise scalars_dev (may be
- * NULL) only receives ZERO_DEV_TIMEOUT if a bounded wait runs out.          */
+ * written may overlap another one.  scalars_dev (may be NULL) only receives
+ * ZERO_DEV_TIMEOUT if a bounded wait runs out.                              */
 ZERO_API zero_status zero_muon_step(const zero_matrices* desc, const zero_muon_hparams* hp, int n_d,
                                     const void* const* rank_grads, float* momentum, float* master, void* lp_out,
                                     void* ws, zero_dev_scalars* scalars_dev, void* stream);
+
+/* The same under the loss scaling and clipping of the Adam step of the same
+ * model (opts NULL or zeros: zero_muon_step).  Either needs scalars_dev.
+ * clipping: the averaged gradient times the coefficient that zero_grad_sqnorm,
+ * or the clipped step before, left there.  loss_scaling: the divisor is n_d *
+ * scalars_dev->loss_scale (hp->loss_scale is not read), a kernel more reads the
+ * gradients first, and where an averaged gradient of any of the call's matrices
+ * is not finite, or the non-finite flag is set already, momentum, master and
+ * lp_out stay as they are and the flag is set.  So the calls of a step come
+ * before the one that commits its scalars (zero_step_fused,
+ * zero_adam_shard_step): with the flag set that one skips its update too and
+ * halves the scale.  A call does not undo the calls before it; a
+ * zero_reduce_scatter over a flat space that holds the matrices too, before the
+ * first of them, has all skip or none.                                      */
+typedef struct {
+    int loss_scaling;    /* 0 or 1: dynamic loss scaling, as in zero_hparams         */
+    int clipping;        /* 0 or 1: multiply by scalars_dev->clip_coef               */
+} zero_muon_opts;
+ZERO_API zero_status zero_muon_step_ex(const zero_matrices* desc, const zero_muon_hparams* hp,
+                                       const zero_muon_opts* opts, int n_d, const void* const* rank_grads,
+                                       float* momentum, float* master, void* lp_out, void* ws,
+                                       zero_dev_scalars* scalars_dev, void* stream);
 
 /* ----------------------------------------------------------- diagnostics --- */
 /* Launch one kernel that waits on a barrier nothing completes, with a wait

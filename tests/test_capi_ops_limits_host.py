@@ -84,19 +84,19 @@ def test_muon_flags_are_checked(z):
     import ctypes
     a, b, c, d, e, f, g = (0x100000000 * k for k in range(1, 8))
 
-    def muon(sc=g, **kw):
-        hp = z.muon_hparams()
-        for k, v in kw.items():
-            setattr(hp, k, v)
+    def muon(sc=g, nesterov=1, loss_scaling=0, clipping=0):
+        hp, opts = z.muon_hparams(), z._capi.ZeroMuonOpts(loss_scaling, clipping)
+        hp.nesterov = nesterov
         ranks = (ctypes.c_void_p * 2)(a, b)
-        return z._capi.raw_status("zero_muon_step", ctypes.byref(z.matrices(32, 64)), ctypes.byref(hp), 2, ranks, c, d, e,
-                                  f, sc, None)
+        return z._capi.raw_status("zero_muon_step_ex", ctypes.byref(z.matrices(32, 64)), ctypes.byref(hp), ctypes.byref(opts),
+                                  2, ranks, c, d, e, f, sc, None)
 
     for k in ("nesterov", "loss_scaling", "clipping"):
         assert muon(**{k: 2}) == 1 and muon(**{k: -1}) == 1
     # what they read is the scalars block
     assert muon(sc=None, loss_scaling=1) == 1 and muon(sc=None, clipping=1) == 1
-    assert z.muon_hparams(loss_scaling=True, clipping=True).loss_scaling == 1
+    # the hyper-parameters' layout is what it was
+    assert ctypes.sizeof(z._capi.ZeroMuonHparams) == 24
 
 
 # ------------------------------------------- the forms of the matrix updates

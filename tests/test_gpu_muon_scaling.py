@@ -21,8 +21,9 @@ def same(a, b):
     return all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a, b))
 
 
-def step(job, **hp):
-    z.zero_muon_step(job.desc, z.muon_hparams(**dict(job.hp, **hp)), job.grads, job.momentum, job.master, job.lp, job.ws, job.sc)
+def step(job, loss_scaling=False, clipping=False, **hp):
+    z.zero_muon_step_ex(job.desc, z.muon_hparams(**dict(job.hp, **hp)), job.grads, job.momentum, job.master, job.lp, job.ws,
+                        job.sc, loss_scaling, clipping)
     torch.cuda.synchronize()
 
 
@@ -150,11 +151,11 @@ def test_skipped_and_taken_steps_in_one_graph():
     z.zero_scalars_init(job.sc, 1.0)
     job.new_grads(0)
     good = [t.clone() for t in job.grads]
-    hp = z.muon_hparams(**dict(job.hp, loss_scaling=True))
+    hp = z.muon_hparams(**job.hp)
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        z.zero_muon_step(job.desc, hp, job.grads, job.momentum, job.master, job.lp, job.ws, job.sc)
+        z.zero_muon_step_ex(job.desc, hp, job.grads, job.momentum, job.master, job.lp, job.ws, job.sc, loss_scaling=True)
     before = state(job)
     job.view(job.grads[1])[1, 5, 5] = float("inf")
     graph.replay()

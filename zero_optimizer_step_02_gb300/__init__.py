@@ -26,7 +26,7 @@ from ._capi import (NOALLOC_SCRATCH_BYTES, ZERO_BF16, ZERO_FP16, ZERO_FP32, ZERO
                     zero_step_layers, zero_layers_workspace_bytes, LayerStack, ZeroLayer,
                     layernorm, zero_layernorm_workspace_bytes, zero_layernorm_forward, zero_layernorm_backward,
                     matrices, muon_hparams, zero_orthogonalize_workspace_bytes, zero_orthogonalize,
-                    zero_muon_workspace_bytes, zero_muon_step, zero_debug_matmul_timeout, zero_debug_matrix_plan)
+                    zero_muon_workspace_bytes, zero_muon_step, zero_muon_step_ex, zero_debug_matmul_timeout, zero_debug_matrix_plan)
 
 __all__ = ["Plan", "StepBuffers", "read_scalars", "row_len", "hparams", "rank_ptrs", "ZeroError", "ZeroHparams",
            "LayerStack", "ZeroLayer", "layernorm", "matrices", "muon_hparams",

@@ -84,8 +84,11 @@ class ZeroMatrices(ctypes.Structure):
 
 class ZeroMuonHparams(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_float), ("momentum", ctypes.c_float), ("weight_decay", ctypes.c_float),
-                ("rms_scale", ctypes.c_float), ("loss_scale", ctypes.c_float), ("nesterov", ctypes.c_int),
-                ("loss_scaling", ctypes.c_int), ("clipping", ctypes.c_int)]
+                ("rms_scale", ctypes.c_float), ("loss_scale", ctypes.c_float), ("nesterov", ctypes.c_int)]
+
+
+class ZeroMuonOpts(ctypes.Structure):
+    _fields_ = [("loss_scaling", ctypes.c_int), ("clipping", ctypes.c_int)]
 
 
 class ZeroMatrixPlan(ctypes.Structure):
@@ -133,6 +136,8 @@ _SIGS = {
     "zero_orthogonalize": (_i32, [ctypes.POINTER(ZeroMatrices), _vp, _vp, _vp, _vp, _vp]),
     "zero_muon_step": (_i32, [ctypes.POINTER(ZeroMatrices), ctypes.POINTER(ZeroMuonHparams), _i32, _vp, _vp, _vp, _vp,
                               _vp, _vp, _vp]),
+    "zero_muon_step_ex": (_i32, [ctypes.POINTER(ZeroMatrices), ctypes.POINTER(ZeroMuonHparams),
+                                 ctypes.POINTER(ZeroMuonOpts), _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "zero_debug_matmul_timeout": (_i32, [_vp, _vp, _ll, _vp]),
     "zero_debug_matrix_plan": (_i32, [ctypes.POINTER(ZeroMatrices), _i32, _i32, ctypes.POINTER(ZeroMatrixPlan)]),
     "zero_layernorm_workspace_bytes": (_sz, [ctypes.POINTER(ZeroLayerNorm)]),
@@ -487,12 +492,8 @@ def matrices(rows, cols, batch=1, dtype=ZERO_BF16, out_dtype=None, in_ld=0, out_
     return d
 
 
-def muon_hparams(lr=0.02, momentum=0.95, weight_decay=0.0, rms_scale=0.0, loss_scale=1.0, nesterov=True,
-                 loss_scaling=False, clipping=False):
-    """loss_scaling, clipping: by the scalars block that zero_muon_step is then given (loss scale and
-    skipped steps, clip coefficient)."""
-    return ZeroMuonHparams(lr, momentum, weight_decay, rms_scale, loss_scale, int(bool(nesterov)),
-                           int(bool(loss_scaling)), int(bool(clipping)))
+def muon_hparams(lr=0.02, momentum=0.95, weight_decay=0.0, rms_scale=0.0, loss_scale=1.0, nesterov=True):
+    return ZeroMuonHparams(lr, momentum, weight_decay, rms_scale, loss_scale, int(bool(nesterov)))
 
 
 def zero_orthogonalize_workspace_bytes(desc):
@@ -532,6 +533,17 @@ def zero_debug_matmul_timeout(scratch, scalars, timeout_ns, stream=None):
     """One matrix product whose copies are never issued: every wait runs out (tests the timeout path)."""
     _check(_lib.zero_debug_matmul_timeout(_addr(scratch), _addr(scalars), timeout_ns, _stream(stream)),
            "zero_debug_matmul_timeout")
+
+
+def zero_muon_step_ex(desc, hp, rank_grads, momentum, master, lp_out, ws, scalars, loss_scaling=False, clipping=False,
+                      stream=None):
+    """zero_muon_step under the loss scaling (scale and skipped steps) and clipping of the step whose
+    scalars block is given."""
+    ranks = _ptr_array(rank_grads)
+    opts = ZeroMuonOpts(int(bool(loss_scaling)), int(bool(clipping)))
+    _check(_lib.zero_muon_step_ex(ctypes.byref(desc), ctypes.byref(hp), ctypes.byref(opts), len(ranks), ranks,
+                                  _addr(momentum), _addr(master), _addr(lp_out), _addr(ws), _addr(scalars),
+                                  _stream(stream)), "zero_muon_step_ex")
 
 
 def zero_launch_count():

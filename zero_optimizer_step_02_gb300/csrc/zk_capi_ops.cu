@@ -237,6 +237,14 @@ ZERO_API zero_status zero_muon_step(const zero_matrices* d, const zero_muon_hpar
                                     void* ws, zero_dev_scalars* sc, void* stream)
 {
     ZK_CALL_RANGE();
+    return zero_muon_step_ex(d, hp, nullptr, n_d, rank_grads, momentum, master, lp_out, ws, sc, stream);
+}
+
+ZERO_API zero_status zero_muon_step_ex(const zero_matrices* d, const zero_muon_hparams* hp, const zero_muon_opts* opts,
+                                       int n_d, const void* const* rank_grads, float* momentum, float* master,
+                                       void* lp_out, void* ws, zero_dev_scalars* sc, void* stream)
+{
+    ZK_CALL_RANGE();
     zero_status s;
     if ((s = check_matrices(d)) != ZERO_OK) return s;
     if (hp == nullptr || rank_grads == nullptr) return ZERO_ERR_INVALID_ARG;
@@ -252,9 +260,10 @@ ZERO_API zero_status zero_muon_step(const zero_matrices* d, const zero_muon_hpar
     for (float x : v)
         if (!std::isfinite(x) || x < 0.0f) return ZERO_ERR_INVALID_ARG;
     if (hp->momentum >= 1.0f) return ZERO_ERR_INVALID_ARG;
-    for (int f : {hp->nesterov, hp->loss_scaling, hp->clipping})
+    const int loss_scaling = opts != nullptr ? opts->loss_scaling : 0, clipping = opts != nullptr ? opts->clipping : 0;
+    for (int f : {hp->nesterov, loss_scaling, clipping})
         if (f != 0 && f != 1) return ZERO_ERR_INVALID_ARG;
-    if ((hp->loss_scaling || hp->clipping) && sc == nullptr) return ZERO_ERR_INVALID_ARG;
+    if ((loss_scaling || clipping) && sc == nullptr) return ZERO_ERR_INVALID_ARG;
     for (int r = 0; r < n_d; ++r)
         if ((s = zk::check_dev(rank_grads[r])) != ZERO_OK) return s;
     if ((s = zk::check_dev(momentum)) != ZERO_OK || (s = zk::check_dev(master)) != ZERO_OK) return s;
@@ -281,8 +290,8 @@ ZERO_API zero_status zero_muon_step(const zero_matrices* d, const zero_muon_hpar
     a.divisor = static_cast<float>(n_d) * (hp->loss_scale > 0.0f ? hp->loss_scale : 1.0f);
     a.mu = hp->momentum;
     a.nesterov = hp->nesterov;
-    a.loss_scaling = hp->loss_scaling;
-    a.clipping = hp->clipping;
+    a.loss_scaling = loss_scaling;
+    a.clipping = clipping;
     a.momentum = momentum;
     a.master = master;
     a.lp = lp_out;
