@@ -735,8 +735,9 @@ ZERO_API zero_status zero_adamw_tensors(const zero_hparams* hp, const zero_tenso
  *
  * h, o, hout, y, a gate for every token and their gradients have `dtype`;
  * gains, biases, a gate vector and their gradients `w_dtype`; stats is fp32
- * [rows][4] (16-byte aligned): mean and rstd of o, then of hout, which the
- * backward pass reads (0 and 1 without that norm; mean 0 for rms).  Strides are
+ * [rows][4] (16-byte aligned): mean and rstd of o, then of hout (0 and 1 without
+ * that norm; mean 0 for rms).  The backward pass uses those of the norms that there
+ * are, whatever the others' places hold, and an rms norm's mean is 0.  Strides are
  * in elements between rows, 0 meaning cols, else >= cols: h_stride of h, hout and
  * their gradients, o_stride of o and do, y_stride of y and dy, gate_stride of a
  * gate for every token and its gradient.  All other pointers need only the

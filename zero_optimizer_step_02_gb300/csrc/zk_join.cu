@@ -671,8 +671,15 @@ __global__ void __launch_bounds__(TT, 1) join_backward(const __grid_constant__ J
         for (int i = 0; i < N; ++i) sum[k][i] = 0ull;
     const f32x2 scale = pack2(a.res_scale, a.res_scale);
     const float4* stats = reinterpret_cast<const float4*>(a.stats) + walk.r0;
-    const auto statistics = [&](int i) {   // of the row of turn i, the next one to be asked for
-        const float4 st = a.stats != nullptr && i < walk.mine[0] ? *stats : make_float4(0.0f, 1.0f, 0.0f, 1.0f);
+    const bool post = a.post != ZERO_NORM_NONE, pre = a.pre != ZERO_NORM_NONE;
+    // of the row of turn i, the next one to be asked for; those of a norm that is not
+    // there (and an rms norm's mean) are not the caller's to give
+    const auto statistics = [&](int i) {
+        float4 st = a.stats != nullptr && i < walk.mine[0] ? *stats : make_float4(0.0f, 1.0f, 0.0f, 1.0f);
+        if (a.post != ZERO_NORM_LAYER) st.x = 0.0f;
+        if (!post) st.y = 1.0f;
+        if (a.pre != ZERO_NORM_LAYER) st.z = 0.0f;
+        if (!pre) st.w = 1.0f;
         stats += walk.step;
         return st;
     };
@@ -680,7 +687,6 @@ __global__ void __launch_bounds__(TT, 1) join_backward(const __grid_constant__ J
     unsigned char *slot = mine, *const end = mine + DEPTH * stage;
     // LAG: turn i takes pre's gradient of its row and post's of the row before,
     // whose sums share a barrier; a turn more finishes the last one.
-    const bool post = a.post != ZERO_NORM_NONE, pre = a.pre != ZERO_NORM_NONE;
     const int turns = walk.turns + (LAG && post ? 1 : 0);
     f32x2 uw[N], xw[N];   // the row before: gate * d * gain, and o normalised
     float rw = 1.0f;
