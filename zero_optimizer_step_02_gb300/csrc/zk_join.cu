@@ -703,10 +703,10 @@ __global__ void __launch_bounds__(TT, 1) join_backward(const __grid_constant__ J
         if (pre) {
             in.read(u, 1, 0, slot, i, places);
             in.read(x, 2, 0, slot, i, places);
-            const f32x2 r = pack2(st.w, st.w), off = pack2(-st.z * st.w, -st.z * st.w);
+            const Centred<DT> row(st.z, st.w);
 #pragma unroll
             for (int k = 0; k < N; ++k) {
-                x[k] = fma2(x[k], r, off);
+                x[k] = row.xhat(x[k]);
                 sum[2][k] = fma2(u[k], x[k], sum[2][k]);
                 sum[3][k] = add2(sum[3][k], u[k]);
                 u[k] = mul2(u[k], qg[k]);
@@ -741,9 +741,9 @@ __global__ void __launch_bounds__(TT, 1) join_backward(const __grid_constant__ J
         if (active) put_row<kH, DT, NCH, MODE>(a.out[0], 0, w, c, a, places);
         in.read(xw, 3, 0, slot, i, places);
         {
-            const f32x2 r = pack2(st.y, st.y), off = pack2(-st.x * st.y, -st.x * st.y);
+            const Centred<DT> row(st.x, st.y);
 #pragma unroll
-            for (int k = 0; k < N; ++k) xw[k] = fma2(xw[k], r, off);
+            for (int k = 0; k < N; ++k) xw[k] = row.xhat(xw[k]);
         }
         if constexpr (TOK) {
             f32x2 g[N];

@@ -115,6 +115,30 @@ __device__ __forceinline__ float both(f32x2 v)
     return a + b;
 }
 
+// xhat of a row with this mean and 1 / std.  |xhat| <= sqrt(cols), and an x that
+// is not the mean differs from it by 2^-25 of it or more: where |mean| * rstd
+// passes 2^40, every x is the mean and xhat is 0, however large mean * rstd (an
+// overflow would make it NaN).  rstd NaN or infinite: as they come.
+template <int DT>
+struct Centred {
+    f32x2 rs, by;
+    __device__ __forceinline__ Centred(float mean, float rstd)
+    {
+        const float nm = -mean * rstd;
+        const bool flat = fabsf(nm) > 1.099511627776e12f && is_finite_f32(rstd);
+        const float r = flat ? 0.0f : rstd, b = DT == ZERO_FP32 ? mean : flat ? 0.0f : nm;
+        rs = pack2(r, r);
+        by = pack2(b, b);
+    }
+    __device__ __forceinline__ f32x2 xhat(f32x2 x) const
+    {
+        if constexpr (DT == ZERO_FP32)
+            return mul2(sub2(x, by), rs);
+        else
+            return fma2(x, rs, by);
+    }
+};
+
 // a chunk without the columns before 0 and from `cols` on (zeros there); c: its first
 template <int DT>
 __device__ __forceinline__ uint4 masked(const uint4& w, int c, int cols)
