@@ -703,7 +703,10 @@ ZERO_API size_t zero_adamw_tensors_workspace_bytes(const zero_hparams* hp, const
 /* One step of every tensor of the list, which commits the step scalars as
  * zero_step_fused does (t, beta powers, loss scale).  One kernel for up to 400
  * tensors.  With clipping the norm is that of all the list's gradients, and a
- * kernel more reads them first; so it does with loss scaling, where a
+ * kernel more reads them first.  The norm of finite gradients is finite, however
+ * large they are; without loss scaling an infinite one makes the coefficient 0 and
+ * one that is not a number NaN, as max_norm / norm says, and so every weight.  The
+ * kernel runs with loss scaling too, where a
  * non-finite value in any of them (or the non-finite flag set by an earlier
  * call of the step) leaves every tensor as it was and halves the scale.
  * The same inputs, as far from 16-byte boundaries, give the same bits on the

@@ -558,7 +558,11 @@ k_adamw(const __grid_constant__ TensorTable<CAP> t, const __grid_constant__ Adam
 
 // Squared norm of every unscaled gradient: one fp64 partial sum a CTA (see
 // sq_accumulate), which the last CTA of the last launch adds up in order for the
-// clip coefficient; under loss scaling the non-finite flag.
+// clip coefficient; under loss scaling the non-finite flag.  Squares and a lane's
+// sums are fp32, which a finite gradient from 1.8e19 on leaves: a warp whose lanes
+// then hold an infinity or a NaN (the rounding errors' sum keeps one to the end)
+// reads its share once more and adds it up in fp64, whose range no list of fp32
+// values leaves.
 constexpr int kNormAhead = 4;   // tiles under way
 
 struct Squares {
@@ -566,13 +570,10 @@ struct Squares {
     float inv, divisor;   // inv 0: the divisor is not a power of two
     bool bad;
 
+    __device__ __forceinline__ float unscaled(float x) const { return inv != 0.0f ? __fmul_rn(x, inv) : __fdiv_rn(x, divisor); }
     __device__ __forceinline__ void take(float x, float y)
     {
-        if (inv != 0.0f) {
-            x = __fmul_rn(x, inv), y = __fmul_rn(y, inv);
-        } else {
-            x = __fdiv_rn(x, divisor), y = __fdiv_rn(y, divisor);
-        }
+        x = unscaled(x), y = unscaled(y);
         bad |= !is_finite_f32(x) | !is_finite_f32(y);
         sq_accumulate2(x, y, hi, lo);
     }
@@ -600,6 +601,30 @@ struct Squares {
         }
     }
 };
+
+// A lane's part of the squared norm of tiles [first, last), in fp64.
+template <int CAP>
+__device__ __noinline__ double squares_in_fp64(const TensorTable<CAP>& t, int first, int last, const Squares& sq)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    double part = 0.0;
+    int i = tensor_of(t, first);
+    for (int tile = first; tile < last; ++tile) {
+        while (i + 1 < t.n && t.e[i + 1].tile0 <= tile) ++i;
+        const TensorEntry& e = t.e[i];
+        const long long at = static_cast<long long>(tile - e.tile0) * kTensorTile + warp * kStateBlock, left = e.n - at;
+        if (left <= 0) continue;
+        float g[8];
+        load_grad<false>(static_cast<const char*>(e.grad) + at * (e.grad_dtype == ZERO_FP32 ? 4 : 2), e.grad_dtype, lane,
+                         left < kStateBlock ? static_cast<int>(left) : kStateBlock, g);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const double x = sq.unscaled(g[k]);
+            part = __dadd_rn(part, __dmul_rn(x, x));
+        }
+    }
+    return part;
+}
 
 template <int CAP>
 __global__ void __launch_bounds__(kThreadsT, 6)
@@ -640,7 +665,12 @@ k_tensors_norm(const __grid_constant__ TensorTable<CAP> t, const __grid_constant
     unpack2(sq.hi, h0, h1);
     unpack2(sq.lo, l0, l1);
     const bool bad = sq.bad;
-    const double part = warp_sum_f64(__dadd_rn(__dadd_rn(static_cast<double>(h0), static_cast<double>(l0)), __dadd_rn(static_cast<double>(h1), static_cast<double>(l1))));
+    double part = __dadd_rn(__dadd_rn(static_cast<double>(h0), static_cast<double>(l0)), __dadd_rn(static_cast<double>(h1), static_cast<double>(l1)));
+    const bool left_range = !(is_finite_f32(h0) && is_finite_f32(h1) && is_finite_f32(l0) && is_finite_f32(l1));
+    // (with a non-finite gradient under loss scaling the step is skipped, whatever the norm)
+    if (a.clip && __any_sync(0xFFFFFFFFu, left_range) && !(a.hp.loss_scaling && __any_sync(0xFFFFFFFFu, bad)))
+        part = squares_in_fp64(t, first, last, sq);
+    part = warp_sum_f64(part);
     if (lane == 0) red[warp] = part;
     if (__syncthreads_or(bad) && a.hp.loss_scaling && threadIdx.x == 0) atomicExch(&a.sc->nonfinite, 1);
     if (!a.clip) return;
@@ -662,7 +692,8 @@ k_tensors_norm(const __grid_constant__ TensorTable<CAP> t, const __grid_constant
         all = warp_sum_f64(all);
         if (lane == 0) {
             a.sc->sqnorm = all;
-            a.sc->clip_coef = clip_coefficient(a.hp.max_norm, all);
+            // max_norm over a norm that is not a number is not 1
+            a.sc->clip_coef = isnan(all) ? __uint_as_float(0x7FC00000u) : clip_coefficient(a.hp.max_norm, all);
             a.sc->ctas_done = 0u;
         }
     }
