@@ -40,6 +40,7 @@ struct Consts {
     float b1, b2, omb1, omb2, bc1, sbc2, eps, coef, divisor;
     float factor;    // of the gradient, without a division: 0 where that takes one
     uint32_t turn;   // this step's part of the 8-bit states' thresholds
+    float lift;      // the 8-bit states' divisors and dividends times this: 1, or what makes a subnormal eps a normal number
 };
 
 // The step's constants (one thread).
@@ -61,6 +62,8 @@ __device__ __forceinline__ void step_consts(const AdamwArgs& a, Consts* out)
     k.divisor = c.divisor;
     // g / 1 * coef, or g / 2^k, in one product, which rounds as the two do
     k.factor = c.divisor == 1.0f ? k.coef : c.div_pow2 && k.coef == 1.0f ? c.inv_divisor : 0.0f;
+    // the near reciprocal takes a subnormal for 0: 0 / eps would be NaN
+    k.lift = k.eps > 0.0f && k.eps < 1.17549435e-38f ? 4294967296.0f : 1.0f;
     k.turn = static_cast<uint32_t>(a.sc->t) * static_cast<uint32_t>(a.sc->t) * kTurnStep;
     *out = k;
 }
@@ -349,7 +352,8 @@ __device__ __forceinline__ void update(Held<true>& h, const TensorEntry& t, long
     unscale(h.g, c);
     const f32x2 ms = pack2(h.ms, h.ms), rs = pack2(h.rs, h.rs), b1 = pack2(c.b1, c.b1), b2 = pack2(c.b2, c.b2);
     const f32x2 omb1 = pack2(c.omb1, c.omb1), omb2 = pack2(c.omb2, c.omb2);
-    const f32x2 eps = pack2(c.eps, c.eps), step = pack2(-r.step, -r.step), decay = pack2(r.decay, r.decay);
+    const float eps1 = __fmul_rn(c.eps, c.lift), step1 = -__fmul_rn(r.step, c.lift);
+    const f32x2 eps = pack2(eps1, eps1), step = pack2(step1, step1), lift = pack2(c.lift, c.lift), decay = pack2(r.decay, r.decay);
     float m[8], root[8], mtop = 0.0f, rtop = 0.0f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -364,7 +368,7 @@ __device__ __forceinline__ void update(Held<true>& h, const TensorEntry& t, long
         unpack2(mul2(omb2, mul2(x, x)), b0, b1_);
         root[2 * k] = a0 = __fsqrt_rn(__fadd_rn(a0, b0)), root[2 * k + 1] = a1 = __fsqrt_rn(__fadd_rn(a1, b1_));
         rtop = max_or_nan(rtop, max_or_nan(a0, a1));
-        unpack2(add2(pack2(a0, a1), eps), a0, a1);
+        unpack2(fma2(pack2(a0, a1), lift, eps), a0, a1);
         const f32x2 inv = pack2(reciprocal_near(a0), reciprocal_near(a1));
         unpack2(fma2(mul2(momentum, step), inv, mul2(pack2(h.p[2 * k], h.p[2 * k + 1]), decay)), h.p[2 * k], h.p[2 * k + 1]);
     }
