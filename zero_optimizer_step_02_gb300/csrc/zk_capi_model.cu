@@ -244,29 +244,45 @@ struct Bytes {
 bool overlap(const Bytes& a, const Bytes& b)
 {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-    return a.p != nullptr && b.p != nullptr && x < y + static_cast<uintptr_t>(b.n) && y < x + static_cast<uintptr_t>(a.n);
+    return a.p != nullptr && b.p != nullptr && a.n > 0 && b.n > 0 && x < y + static_cast<uintptr_t>(b.n) && y < x + static_cast<uintptr_t>(a.n);
 }
 
-// Whether one of `lone`, written beside the rows, meets an array of rows (from its
-// first byte to its last) or another one of `lone`.
-bool lone_clash(const zk::JoinArgs& a, std::initializer_list<int> in, std::initializer_list<int> out, std::initializer_list<Bytes> lone)
+// Whether bytes of `b` are bytes of a row of the array at p (between the rows' own
+// bytes of a strided array there may be others').
+bool meets_rows(const zk::JoinArgs& a, const void* p, int kind, const Bytes& b)
 {
-    const long long es = zk::dtype_bytes(a.dtype);
-    const auto meets_rows = [&](const void* p, int kind) {
-        const Bytes rows = {p, a.rows == 0 ? 0 : ((a.rows - 1) * a.stride[kind] + a.cols) * es};
-        for (const Bytes& b : lone)
-            if (overlap(rows, b)) return true;
+    const long long es = zk::dtype_bytes(a.dtype), row = a.cols * es, pitch = a.stride[kind] * es;
+    if (a.rows == 0 || !overlap({p, (a.rows - 1) * pitch + row}, b)) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(b.p);
+    if (y <= x) return true;   // reaches into the first row
+    const long long in = static_cast<long long>((y - x) % static_cast<uintptr_t>(pitch));
+    return in < row || (in + b.n > pitch && y - x < static_cast<uintptr_t>((a.rows - 1) * pitch));
+}
+
+// Whether one of `written`, beside the rows, meets a row, another of them or one of
+// `read`; or a row that is written (all of `out`) one of `read`.
+bool lone_clash(const zk::JoinArgs& a, std::initializer_list<int> in, std::initializer_list<int> out, std::initializer_list<Bytes> written,
+                std::initializer_list<Bytes> read)
+{
+    const auto any_meets = [&](const void* p, int kind, std::initializer_list<Bytes> all) {
+        for (const Bytes& b : all)
+            if (meets_rows(a, p, kind, b)) return true;
         return false;
     };
     int i = 0;
     for (int k : in)
-        if (meets_rows(a.in[i++], k)) return true;
+        if (any_meets(a.in[i++], k, written)) return true;
     i = 0;
-    for (int k : out)
-        if (meets_rows(a.out[i++], k)) return true;
-    for (const Bytes* x = lone.begin(); x != lone.end(); ++x)
-        for (const Bytes* y = lone.begin(); y != x; ++y)
+    for (int k : out) {
+        if (any_meets(a.out[i], k, written) || any_meets(a.out[i], k, read)) return true;
+        ++i;
+    }
+    for (const Bytes* x = written.begin(); x != written.end(); ++x) {
+        for (const Bytes* y = written.begin(); y != x; ++y)
             if (overlap(*x, *y)) return true;
+        for (const Bytes& y : read)
+            if (overlap(*x, y)) return true;
+    }
     return false;
 }
 
@@ -412,7 +428,10 @@ ZERO_API zero_status zero_residual_norm_forward(const zero_residual_norm* d, con
     a.in[2] = a.token_gate ? gate : nullptr;
     a.out[0] = hout;
     a.out[1] = y;
-    if (rows_clash(a, {0, 1, 3}, {0, 2}) || lone_clash(a, {0, 1, 3}, {0, 2}, {{stats, 16 * d->rows}})) return ZERO_ERR_INVALID_ARG;
+    const long long vec = static_cast<long long>(d->cols) * ws;
+    if (rows_clash(a, {0, 1, 3}, {0, 2}) ||
+        lone_clash(a, {0, 1, 3}, {0, 2}, {{stats, 16 * d->rows}}, {{post_gain, vec}, {post_bias, vec}, {a.gate, vec}, {pre_gain, vec}, {pre_bias, vec}}))
+        return ZERO_ERR_INVALID_ARG;
     a.post_gain = post_gain;
     a.post_bias = post_bias;
     a.pre_gain = pre_gain;
@@ -464,10 +483,11 @@ ZERO_API zero_status zero_residual_norm_backward(const zero_residual_norm* d, co
     if (d->rows > 0 && (dh == o || (a.token_gate && dh == gate))) return ZERO_ERR_INVALID_ARG;   // written before those are read
     if (a.token_gate) dgate = nullptr;
     const long long vec = static_cast<long long>(d->cols) * we;
+    const Bytes stat = {post || pre ? stats : nullptr, 16 * d->rows};
     if (lone_clash(a, {0, 2, 0, 1, 3}, {0, 1, 3},
                    {{dpost_gain, vec}, {dpost_bias, vec}, {dgate, vec}, {dpre_gain, vec}, {dpre_bias, vec},
-                    {ws, static_cast<long long>(join_parts_bytes(d))}}) ||
-        overlap({stats, 16 * d->rows}, {ws, static_cast<long long>(join_parts_bytes(d))}))
+                    {ws, static_cast<long long>(join_parts_bytes(d))}},
+                   {{post_gain, vec}, {post_bias, vec}, {a.gate, vec}, {pre_gain, vec}, stat}))
         return ZERO_ERR_INVALID_ARG;
     a.post_gain = post_gain;
     a.post_bias = post_bias;
