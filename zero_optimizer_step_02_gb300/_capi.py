@@ -705,8 +705,12 @@ def zero_embedding_workspace_bytes(desc):
 
 
 def _check_ids(desc, ids):
-    if ids is not None and not isinstance(ids, int) and (8 * ids.element_size() != desc.id_bits or ids.is_floating_point()):
+    if ids is None or isinstance(ids, int):
+        return
+    if 8 * ids.element_size() != desc.id_bits or ids.is_floating_point():
         raise ValueError("ids: integers of %d bits expected" % desc.id_bits)
+    if ids.numel() < desc.tokens or not ids.is_contiguous():   # a batch's [:, :-1] is not, and would be read as if it were
+        raise ValueError("ids: %d contiguous elements expected" % desc.tokens)
 
 
 def zero_embedding_forward(desc, ids, table, out, scalars=None, stream=None):
