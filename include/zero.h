@@ -660,8 +660,11 @@ ZERO_API zero_status zero_muon_step_ex(const zero_matrices* desc, const zero_muo
  *          between the two, in 2^-20 of the way, plus u / 2^20 reaches 1:
  *          u = ((0xC13FA9A9 * t * t + 0x91E10DA5 * i) mod 2^32) >> 12,
  *          t the committed steps before the call, i the element in its tensor
- * (rounding to nearest would hold a moment that decays slowly where it is; over
- * the steps this rounding's mean is the value).  A positive root keeps at least
+ * Scale and factor are products, of which one takes a reciprocal: a block then needs
+ * one division for both its moments.  Their second rounding is up to 2^-23 of a
+ * code's value, whose neighbours lie 2^-4 of it away or further.  (Rounding to
+ * nearest would hold a moment that decays slowly where it is; over the steps this
+ * rounding's mean is the value.)  A positive root keeps at least
  * the smallest code (2^-9).  A block whose largest magnitude is under 2^-100
  * gets scale and codes 0; one that holds an infinity or a NaN gets codes 0 and a
  * NaN as its scale, for the whole block.  All-zero codes and scales are zero
@@ -691,7 +694,10 @@ typedef struct {
  * bytes take the wide loads.  No array that is written may share a byte with
  * another array of the list (ZERO_ERR_INVALID_ARG).  More than ZERO_MAX_TENSORS
  * tensors, or ZERO_MAX_TENSOR_ELEMS elements in one, are ZERO_ERR_BOUNDS.  The
- * list is read only by the calls below, so calls may share it.               */
+ * list is read only by the calls below, so calls may share it.  A list is made
+ * anew when an address changes, which takes tens of microseconds of host time for
+ * hundreds of tensors (the Python binding's checks some 5 a tensor): a program
+ * whose gradients stay where they are makes one list.                        */
 typedef struct zero_tensors zero_tensors;
 ZERO_API zero_status zero_tensors_create(zero_tensors** out, int n, const zero_tensor* tensors);
 ZERO_API void zero_tensors_destroy(zero_tensors* tensors);
@@ -735,6 +741,9 @@ ZERO_API zero_status zero_adamw_tensors(const zero_hparams* hp, const zero_tenso
  * and the gradients of the gains and biases, sums over the rows.  Sums are fp32
  * or wider whatever the types, and each result is rounded once.  The same
  * inputs, as far from 16-byte boundaries, give the same bits on the same device.
+ * A row of more than a CTA's words is shared by CTAs that wait for each other's
+ * sums, with a limit.  The calls take no scalars block to report one that ran out
+ * in: what waits for those sums is NaN.
  *
  * h, o, hout, y, a gate for every token and their gradients have `dtype`;
  * gains, biases, a gate vector and their gradients `w_dtype`; stats is fp32

@@ -17,12 +17,12 @@
 // which is most of the table where there are more rows than tokens.
 //
 // What a call cannot do without, at a copy's rate, and what it takes (us; bf16):
-//   lookup, 16384 of 128256 x 4096     28.1   35.7: rows of 8 KB from all over memory
-//   gradient, 16384 to 128256 x 4096    175    203: the table's zeros, at a copy's
+//   lookup, 16384 of 128256 x 4096     28.1   34.2: rows of 8 KB from all over memory
+//   gradient, 16384 to 128256 x 4096    175    201: the table's zeros, at a copy's
 //       rate; 10 of it are the sort, which moves nothing of that
-//   gradient, 8192 to 50257 x 768      13.2   25.5: the sort (8), then the rows of a
+//   gradient, 8192 to 50257 x 768      13.2   25.0: the sort (8), then the rows of a
 //       window, eight at a time, and the parts of the row with the most tokens
-//   added to, 5000 to 1031 x 333 fp32   1.3   19.5: the same latencies
+//   added to, 5000 to 1031 x 333 fp32   1.3   19.2: the same latencies
 #include <cstring>
 
 #include "zk_common.cuh"

@@ -17,13 +17,14 @@
 // What a call cannot do without, at a copy's rate, and what it takes (us; bf16, rms
 // before and after, a gate vector, in a graph of calls):
 //   forward   8192 x 4096   39.6   52      backward   8192 x 4096   59.4   100
-//             16384 x 768   14.9   24                 16384 x 768   22.3    50
-//             4096 x 16384  79.2  151                 4096 x 16384   119   349
+//             16384 x 768   14.9   23                 16384 x 768   22.3    50
+//             4096 x 16384  79.2  156                 4096 x 16384   119   349
 //             5003 x 1601    9.5   32                 5003 x 1601   14.2    53  (fp16)
 // Not memory but a row's own chain bounds them: words in, a sum over the team, the
 // next norm's sum, words out, with sixteen warps an SM (eight backward from 2048
 // columns on), as the weights and column sums of a thread's columns fill the
-// registers; so the work is in few barriers, in sums dealt out among the lanes and
+// registers (and, 512 threads forward above 4096 columns, 32 to 280 bytes of spills a
+// thread); so the work is in few barriers, in sums dealt out among the lanes and
 // in addresses that only advance.  In a cluster a sum costs a message's way, and
 // rows of odd widths twice the instructions a column.
 #include <cstring>

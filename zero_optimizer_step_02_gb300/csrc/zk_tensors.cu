@@ -13,14 +13,14 @@
 //
 // What a call cannot do without, at a copy's rate, and what it takes (us; bf16
 // gradients and 16-bit weights):
-//   105M parameters of 12 layers, 32-bit states   435.7   454; clipped 518 to 525: the
-//       norm pass reads the gradients once more (31 of it at a copy's rate, 56 in all,
+//   105M parameters of 12 layers, 32-bit states   435.7   461; clipped 521: the
+//       norm pass reads the gradients once more (31 of it at a copy's rate, 60 in all,
 //       as it adds squares up with their rounding errors, in packed fp32)
-//   436M parameters, 8-bit states                1032.9   1237: some 70 instructions an
-//       element pair leave 1 in 6 of the copy's rate unused; roots and quotients of
-//       the codes are IEEE's
+//   436M parameters, 8-bit states                1032.9   1230: some 70 instructions an
+//       element pair leave 1 in 6 of the copy's rate unused: IEEE's roots, and the
+//       codes' thresholds, roundings and packing
 //   300 odd fp32 tensors                          133.5   152
-//   10 tensors of 1.4M parameters                   2.2   7.0: one launch
+//   10 tensors of 1.4M parameters                   2.2   7.3: one launch
 #include <cuda_fp8.h>
 
 #include "zk_common.cuh"
@@ -411,8 +411,8 @@ __device__ __forceinline__ void step(const TensorEntry& t, long long at, int n, 
 // Whole tiles with 8-bit states come through a ring in shared memory, by bulk
 // copies: a tile has fewer bytes than one with 32-bit states, and its arithmetic
 // takes as long as the memory, so that what 24 warps an SM ask for at a time does
-// not cover the latency (436M parameters 1617 us by direct loads, 1237 through the
-// ring; with 32-bit states direct loads reach 97 % of a copy's rate).
+// not cover the latency (436M parameters 1617 us by direct loads, 1230 through the
+// ring; with 32-bit states direct loads reach 95 to 97 % of a copy's rate).
 constexpr int kRing = 3;
 constexpr int kRingStage = kTensorTile * (4 + 4 + 1 + 1);   // fp32 gradients, weights, codes
 struct Ring {
@@ -729,11 +729,11 @@ namespace {
 // CTAs of the step: several times as many as run at a time.  Those far from their
 // memory take half as long again as the others (with equal shares an SM was busy for
 // 292 to 458 K clocks), and an SM that is done early takes the next: 436M parameters
-// with 8-bit states, with approximate quotients, 1484 us with 456 CTAs, 1228 with 1824
-// and 1180 with 14592 (14 tiles each).  Shorter shares wait for the step's constants too often; those of 32-bit
-// states, which have no ring to fill meanwhile, are twice as long (105M parameters
-// 454 us, with 14 tiles 481).  Whole multiples: 1839 CTAs, where 456 run at a time,
-// leave the last 15 a turn to themselves (504 us).
+// with 8-bit states 1357 us with 456 CTAs, 1230 with 15048 (14 tiles each), 1209 with
+// 3648 (56 each).  Shorter shares wait for the step's constants too often; those of
+// 32-bit states, which have no ring to fill meanwhile, are twice as long (105M
+// parameters 461 us, 457 with 456 CTAs).  Whole multiples: 1839 CTAs, where 456 run at
+// a time, leave the last 15 a turn to themselves (504 us).
 int step_grid(int tiles, bool ring)
 {
     const int turns = tiles / ((ring ? 1 : 2) * kTilesEach * kStepCtas);
