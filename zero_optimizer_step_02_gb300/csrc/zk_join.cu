@@ -23,7 +23,7 @@
 // Not memory but a row's own chain bounds them: words in, a sum over the team, the
 // next norm's sum, words out, with sixteen warps an SM (eight backward from 2048
 // columns on), as the weights and column sums of a thread's columns fill the
-// registers (and, 512 threads forward above 4096 columns, 32 to 280 bytes of spills a
+// registers (and, 512 threads forward above 4096 columns, up to 280 bytes of spills a
 // thread); so the work is in few barriers, in sums dealt out among the lanes and
 // in addresses that only advance.  In a cluster a sum costs a message's way, and
 // rows of odd widths twice the instructions a column.
